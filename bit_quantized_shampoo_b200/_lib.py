@@ -35,6 +35,9 @@ CODEBOOK_DYNAMIC_TREE = 1
 ROOT_EIGEN = 0
 ROOT_NEWTON = 1
 ROOT_NEWTON_Q4 = 2
+ACT8_FP32 = 0
+ACT8_BF16 = 1
+ACT8_FP16 = 2
 
 
 class Config(C.Structure):
@@ -59,6 +62,8 @@ class Shampoo4Error(RuntimeError):
         super().__init__(f"{fn} returned {STATUS_NAMES.get(status, status)}")
         self.status = status
 
+
+_P, _I, _N = C.c_void_p, C.c_int32, C.c_int64        # pointer, int32, int64
 
 _SIGS = {
     "shampoo4_init": [C.POINTER(Config), C.POINTER(Param), C.c_int32, C.POINTER(C.c_void_p)],
@@ -100,6 +105,15 @@ _SIGS = {
     "shampoo4_graft_update": [C.c_void_p, C.POINTER(GraftConfig), C.c_void_p, C.c_int64, C.c_float,
                               C.POINTER(C.c_void_p), c_i64_p, C.POINTER(C.c_void_p), c_i64_p,
                               C.POINTER(C.c_void_p), c_i64_p, C.c_void_p],
+    "act8_pack": [_P, _I, _N, _N, _N, _I, _P, _N, _P, _P],
+    "act8_unpack": [_P, _N, _P, _N, _N, _I, _P, _I, _N, _P],
+    "act8_matmul": [_P, _N, _P, _P, _N, _P, _P, _N, _N, _N, _P, _I, _N, _P, _P],
+    "act8_linear": [_P, _I, _N, _P, _N, _P, _P, _N, _N, _N, _P, _N, _P, _P, _I, _N, _P, _P],
+    "act8_grad_workspace": [_I, _I, _I, _N, _N, _N, c_size_p],
+    "act8_weight_grad": [_P, _I, _N, _P, _N, _P, _I, _N, _N, _N, _P, _I, _N, _I, _P, C.c_size_t, _P, _P],
+    "act8_input_grad": [_P, _I, _N, _P, _N, _P, _N, _N, _N, _P, _I, _N, _I, _P, C.c_size_t, _P, _P],
+    "act8_swiglu": [_P, _N, _P, _N, _I, _N, _N, _I, _P, _N, _P, _N, _P, _P, _N, _P, _P],
+    "act8_swiglu_backward": [_P, _N, _I, _P, _N, _P, _P, _N, _P, _N, _N, _I, _P, _N, _P, _N, _P],
     "shampoo4_timing_enable": [C.c_void_p, C.c_int32],
     "shampoo4_timing_read": [C.c_void_p, C.c_int32, C.POINTER(C.c_double), c_i64_p, C.POINTER(C.c_double),
                              C.POINTER(C.c_double)],

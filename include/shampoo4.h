@@ -28,6 +28,9 @@
  *                   eigenbasis and eigenvalues and rebuilds it per update
  *   refresh_rank / refresh_world (config) deal the refresh of the factors to
  *                   several ranks, whose state spans the caller exchanges
+ *   act8_*          8-bit activation checkpoints, the integer product on
+ *                   them, its gradients and a gated activation: the training
+ *                   side whose fp32 weight gradients update_stats reads
  *   a CUDA graph captured around the step calls replays them: a call
  *                   enqueues only kernels and memsets on its stream
  *
@@ -501,6 +504,106 @@ shampoo4_status shampoo4_graft_update(shampoo4_handle h, const shampoo4_graft_co
                                       const float* const* d_dirs, const int64_t* ld_dirs,
                                       float* const* d_weights, const int64_t* ld_weights,
                                       shampoo4_stream_t stream);
+
+/* ---- 8-bit activations ---------------------------------------------------
+ * The activation side of memory-efficient training, next to the 4-bit
+ * optimizer state: a layer's input is kept as 8-bit codes, which are both the
+ * operand of the integer product of the forward pass and the checkpoint the
+ * backward pass reads; the weight gradient comes out in fp32, as
+ * shampoo4_update_stats takes it.
+ *
+ * Storage.  A matrix of rows x cols is stored as one signed byte per element
+ * (rows ldc bytes apart) and a fp32 scale per group of `group` consecutive
+ * columns of a row: group = 32, 64, 128 or 256 (the last group of a row may
+ * be short), or 0 for one scale per row.  Scales are dense, rows x
+ * ceil(cols / group).  Per group, with a = max |x|:
+ *   scale = fp32(a / 127) (IEEE division), at most 8454659 * 2^98 so that
+ *           127 * scale stays finite;
+ *   code  = the integer nearest to the exact quotient 127 x / a, ties to
+ *           even, in [-127, 127];  value = code * scale.
+ * A group of zeros has scale 0 and codes 0; one that holds a NaN has scale
+ * NaN, one that holds an infinity and no NaN has scale +Inf, both with codes
+ * 0, so that every value read back from it is NaN.
+ *
+ * Rules of all act8 calls.  Code rows are 16-byte aligned (base address and
+ * ldc multiples of 16, ldc >= cols); other matrices are row-major, aligned to
+ * their element, leading dimension >= cols (16-byte aligned rows take the
+ * vector path); scales and biases are fp32.  Bytes between cols and a leading
+ * dimension are neither read into a result nor written.  At most 2^30 rows
+ * or columns.  Outputs must not overlap inputs.  Bad arguments return
+ * SHAMPOO4_ERR_INVALID_ARG before anything is enqueued; an empty result does
+ * nothing.  Everything is enqueued on `stream` of the current device, which
+ * must be the tensors' own; nothing is allocated, and the calls hold no
+ * state: they may overlap freely and be captured into graphs.  d_flags
+ * (optional, may be NULL) is a device word the caller owns and zeroes; the
+ * products OR SHAMPOO4_FLAG_TIMEOUT into it. */
+typedef enum { ACT8_FP32 = 0, ACT8_BF16 = 1, ACT8_FP16 = 2 } act8_dtype;
+
+/* Quantize x (rows x cols of `dtype`) into codes and scales. */
+shampoo4_status act8_pack(const void* d_x, int32_t dtype, int64_t rows, int64_t cols, int64_t ldx, int32_t group,
+                          int8_t* d_codes, int64_t ldc, float* d_scales, shampoo4_stream_t stream);
+
+/* x = code * scale (one fp32 multiply), rounded once to `dtype`. */
+shampoo4_status act8_unpack(const int8_t* d_codes, int64_t ldc, const float* d_scales, int64_t rows, int64_t cols,
+                            int32_t group, void* d_x, int32_t dtype, int64_t ldx, shampoo4_stream_t stream);
+
+/* Y[t, o] = xs[t] ws[o] sum_i xc[t, i] wc[o, i] (+ bias[o]): x is tokens x
+ * inner, W is out x inner, both with one scale per row (group 0).  The
+ * integer sum is exact (inner <= 2^17, codes in [-127, 127]); it is converted
+ * to fp32, scaled and biased in fp32 and rounded once to `dtype`. */
+shampoo4_status act8_matmul(const int8_t* d_xc, int64_t ldxc, const float* d_xs, const int8_t* d_wc, int64_t ldwc,
+                            const float* d_ws, const float* d_bias, int64_t tokens, int64_t out, int64_t inner,
+                            void* d_y, int32_t dtype, int64_t ldy, uint32_t* d_flags, shampoo4_stream_t stream);
+
+/* act8_pack of x with one scale per token, then act8_matmul: a linear layer.
+ * The codes (d_xc, d_xs) are the layer's checkpoint for act8_weight_grad; a
+ * caller that needs none passes scratch. */
+shampoo4_status act8_linear(const void* d_x, int32_t xdtype, int64_t ldx, const int8_t* d_wc, int64_t ldwc,
+                            const float* d_ws, const float* d_bias, int64_t tokens, int64_t out, int64_t inner,
+                            int8_t* d_xc, int64_t ldxc, float* d_xs, void* d_y, int32_t ydtype, int64_t ldy,
+                            uint32_t* d_flags, shampoo4_stream_t stream);
+
+/* The gradients of Y = X W^T from the stored codes, with dY (tokens x out) in
+ * `dtype` and the result in `result`:
+ *   act8_weight_grad  dW[o, i] = sum_t dY[t, o] x[t, i],  x = value of xc
+ *                     (any group)
+ *   act8_input_grad   dX[t, i] = sum_o dY[t, o] w[o, i],  w = value of wc
+ *                     (one scale per row)
+ * accumulate != 0 adds the product to the result's contents (in fp32,
+ * rounded once).  Arithmetic: tensor-core products of bfloat16 with fp32
+ * sums.  A bfloat16 dY enters exactly, fp16 as an exact sum of two bfloat16,
+ * fp32 as such a sum to 2^-16.  The code values enter as a sum of two
+ * bfloat16, to 2^-16; when both dY and the result are bfloat16 they are
+ * rounded to one (off by 2^-8 at most).  A non-finite element of dY, or a
+ * non-finite scale, makes every result it enters non-finite.
+ * d_workspace: act8_grad_workspace bytes, 256-byte aligned (weight != 0 for
+ * act8_weight_grad), scratch of the one call; SHAMPOO4_ERR_WORKSPACE when
+ * smaller. */
+shampoo4_status act8_grad_workspace(int32_t weight, int32_t dtype, int32_t result, int64_t tokens, int64_t out,
+                                    int64_t inner, size_t* bytes);
+shampoo4_status act8_weight_grad(const void* d_dy, int32_t dtype, int64_t lddy, const int8_t* d_xc, int64_t ldxc,
+                                 const float* d_xs, int32_t group, int64_t tokens, int64_t out, int64_t inner,
+                                 void* d_dw, int32_t result, int64_t lddw, int32_t accumulate, void* d_workspace,
+                                 size_t workspace_bytes, uint32_t* d_flags, shampoo4_stream_t stream);
+shampoo4_status act8_input_grad(const void* d_dy, int32_t dtype, int64_t lddy, const int8_t* d_wc, int64_t ldwc,
+                                const float* d_ws, int64_t tokens, int64_t out, int64_t inner, void* d_dx,
+                                int32_t result, int64_t lddx, int32_t accumulate, void* d_workspace,
+                                size_t workspace_bytes, uint32_t* d_flags, shampoo4_stream_t stream);
+
+/* The gated activation h = gate * sigmoid(gate) * up (rows x cols, all of
+ * `dtype`, fp32 arithmetic rounded once), which keeps gate and up as 8-bit
+ * codes in the same pass; and its gradients from those codes:
+ *   dup = dh gate sig,   dgate = dh up sig (1 + gate (1 - sig)),
+ *   sig = sigmoid(gate). */
+shampoo4_status act8_swiglu(const void* d_gate, int64_t ldg, const void* d_up, int64_t ldu, int32_t dtype,
+                            int64_t rows, int64_t cols, int32_t group, void* d_h, int64_t ldh, int8_t* d_gate_codes,
+                            int64_t ldgc, float* d_gate_scales, int8_t* d_up_codes, int64_t lduc, float* d_up_scales,
+                            shampoo4_stream_t stream);
+shampoo4_status act8_swiglu_backward(const void* d_dh, int64_t lddh, int32_t dtype, const int8_t* d_gate_codes,
+                                     int64_t ldgc, const float* d_gate_scales, const int8_t* d_up_codes, int64_t lduc,
+                                     const float* d_up_scales, int64_t rows, int64_t cols, int32_t group,
+                                     void* d_dgate, int64_t lddg, void* d_dup, int64_t lddu,
+                                     shampoo4_stream_t stream);
 
 void shampoo4_destroy(shampoo4_handle h);
 const char* shampoo4_status_string(shampoo4_status s);
