@@ -109,7 +109,7 @@ _SIGS = {
     "act8_unpack": [_P, _N, _P, _N, _N, _I, _P, _I, _N, _P],
     "act8_matmul": [_P, _N, _P, _P, _N, _P, _P, _N, _N, _N, _P, _I, _N, _P, _P],
     "act8_linear": [_P, _I, _N, _P, _N, _P, _P, _N, _N, _N, _P, _N, _P, _P, _I, _N, _P, _P],
-    "act8_grad_workspace": [_I, _I, _I, _N, _N, _N, c_size_p],
+    "act8_grad_workspace": [_I, _I, _I, _N, _N, _N, _I, c_size_p],
     "act8_weight_grad": [_P, _I, _N, _P, _N, _P, _I, _N, _N, _N, _P, _I, _N, _I, _P, C.c_size_t, _P, _P],
     "act8_input_grad": [_P, _I, _N, _P, _N, _P, _N, _N, _N, _P, _I, _N, _I, _P, C.c_size_t, _P, _P],
     "act8_swiglu": [_P, _N, _P, _N, _I, _N, _N, _I, _P, _N, _P, _N, _P, _P, _N, _P, _P],

@@ -17,7 +17,7 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libshampoo4.so")
 
 SOURCES = ["quant4.cu", "gemm_simt.cu", "gemm_tc.cu", "kernels_misc.cu", "graft.cu", "shampoo4.cu", "noalloc.cu",
-           "act8.cu", "act8_gemm.cu"]
+           "act8.cu", "act8_grad.cu", "act8_gemm.cu"]
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo", "-std=c++17",
          "-Xcompiler", "-fPIC", "-I" + INCLUDE, "-I" + CSRC]

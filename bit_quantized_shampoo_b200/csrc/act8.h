@@ -1,40 +1,48 @@
 // Internal launchers of the 8-bit activation operators (act8.cu holds the
-// codec, the gated activation and the C entry points, act8_gemm.cu the
-// products).
+// codec, the gated activation and the C entry points, act8_grad.cu the
+// gradients' operand passes, act8_gemm.cu the products).
 #pragma once
 #include "common.cuh"
 
 namespace s4 {
 
 constexpr int64_t kAct8MaxDim = int64_t(1) << 30;      // rows or columns of any matrix
-constexpr int64_t kAct8MaxInner = int64_t(1) << 17;    // 127^2 * 2^17 < 2^31: the integer sum stays exact
+constexpr int64_t kAct8MaxInner = int64_t(1) << 17;    // 128 * 127 * 2^17 < 2^31: an integer sum stays exact
 constexpr int kAct8CodeAlign = 16;                     // bytes, of code rows (TMA)
+constexpr int kAct8Digits = 3;                         // base-256 digits of a fixed-point gradient
 
-// An operand of a product in bfloat16 parts: value = hi + lo (lo optional).
-struct Act8Parts {
-  const void* hi;
-  const void* lo;
+// A matrix as TMA reads it: `parts` planes of rows x ld elements, `plane`
+// rows apart, 16-byte aligned rows.
+struct Act8Operand {
+  const void* p;
   int64_t ld;                                          // elements
+  int64_t plane;                                       // rows from one plane to the next
 };
 
 struct Act8Out {
-  void* y;
+  void* y;                                             // R x M
   int64_t ld;
   int32_t dtype;
   int32_t accumulate;                                  // y += product (in fp32, rounded once)
-  const float* row_scale;                              // optional
-  const float* col_scale;                              // optional
-  const float* bias;                                   // optional
+  const float* row_scale;                              // of R, optional
+  const float* col_scale;                              // of M, optional
+  const float* bias;                                   // of M, optional
 };
 
-// Y[m, n] = row_scale[m] col_scale[n] sum_k A[m, k] B[n, k] + bias[n] on int8 codes.
-shampoo4_status launch_act8_gemm_i8(const int8_t* a, int64_t lda, const int8_t* b, int64_t ldb, int64_t M, int64_t N,
-                                    int64_t K, const Act8Out& out, uint32_t* flags, cudaStream_t st);
+// All products: Y[r, m] = row_scale[r] col_scale[m] sum_k B[r, k] A[m, k] + bias[m].
 
-// Y[m, n] = sum_k A(m, k) B(k, n) on bfloat16 parts; b is K x N row-major, a
-// is M x K row-major (a_mn = 0) or K x M row-major (a_mn = 1).  Products
-// taken: hi hi, hi lo (when b.lo), lo hi (when a.lo).
-shampoo4_status launch_act8_gemm_bf16(const Act8Parts& a, int a_mn, const Act8Parts& b, int64_t M, int64_t N,
-                                      int64_t K, const Act8Out& out, uint32_t* flags, cudaStream_t st);
+// int8 codes both: a is M x K, b is R x K (K contiguous).
+shampoo4_status launch_act8_codes(const Act8Operand& a, const Act8Operand& b, int64_t M, int64_t R, int64_t K,
+                                  const Act8Out& out, uint32_t* flags, cudaStream_t st);
+// a: codes K x M (M contiguous); b: kAct8Digits planes of R x K digits, most
+// significant first: B = 65536 d0 + 256 d1 + d2.
+shampoo4_status launch_act8_digits(const Act8Operand& a, const Act8Operand& b, int64_t M, int64_t R, int64_t K,
+                                   const Act8Out& out, uint32_t* flags, cudaStream_t st);
+// bfloat16 both: a is K x M in a_parts planes (A = their sum), b is R x K
+// (b_mn = 0) or K x R (b_mn = 1) in b_parts planes.  The products of parts i
+// and j with i + j < max(a_parts, b_parts) are taken.
+shampoo4_status launch_act8_bf16(const Act8Operand& a, int a_parts, const Act8Operand& b, int b_parts, int b_mn,
+                                 int64_t M, int64_t R, int64_t K, const Act8Out& out, uint32_t* flags,
+                                 cudaStream_t st);
 
 }  // namespace s4

@@ -1,17 +1,30 @@
-// Products of the 8-bit activation operators on the sm_100a tensor cores:
+// Products of the 8-bit activation operators on the sm_100a tensor cores,
+// all of the form  Y[r, m] = sum_k B[r, k] A[m, k]  with m contiguous in Y:
 //
-//   act8_matmul        int8 codes x int8 codes, exact int32 sums
-//                      (tcgen05.mma kind::i8), scaled in the epilogue
-//   act8_weight_grad,  bfloat16 parts x bfloat16 parts, fp32 sums
-//   act8_input_grad    (tcgen05.mma kind::f16)
+//   act8_matmul / act8_linear   A = weight codes, B = token codes: int8 x int8,
+//                               exact int32 sums (tcgen05.mma kind::i8)
+//   act8_weight_grad and        A = the stored codes, read in place (their
+//   act8_input_grad             contraction index is the row: MN-major), B =
+//                               the gradient in three signed base-256 digits
+//                               of fixed point: three int8 products with
+//                               exact int32 sums, joined in the epilogue
+//   the same in bfloat16        A = the codes' values in one to three
+//                               bfloat16 parts, B = the gradient in one to
+//                               three (kind::f16, fp32 sums)
 //
-// One persistent CTA per SM walks the output tiles (128 x 256).  Operands
-// come by TMA into a ring of stages, each holding 128 bytes of K (128 codes
-// or 64 bfloat16) of every part; the accumulator is double-buffered in
-// tensor memory, so one tile's epilogue runs under the next one's products.
-// Warp roles (192 threads): warp 0 issues the loads, warp 1 the MMAs, warps
-// 2..5 drain the accumulator.  Every wait is bounded (2 s); on expiry the
-// roles raise SHAMPOO4_FLAG_TIMEOUT, wait for what they issued and leave.
+// A pair of CTAs (cta_group::2) owns a tile of 256 columns m by R rows: each
+// CTA stages its 128 columns of A and half of the rows of B, and the leader's
+// MMAs read both halves, so B crosses each SM's shared memory port once per
+// pair.  TMEM lanes are columns m: a warp's 32 lanes write 32 consecutive
+// results of a row without a transposing pass.  Digits are stacked along the
+// MMA's N, so A is read once for all three.  The accumulator is
+// double-buffered in tensor memory: one tile's epilogue runs under the next
+// one's products.  The pairs are persistent, one CTA per SM.
+//
+// Warp roles (192 threads): warp 0 issues the TMA loads, warp 1 of the leader
+// the MMAs, warps 2..5 drain the accumulator.  Every wait is bounded (2 s);
+// on expiry a role raises SHAMPOO4_FLAG_TIMEOUT and stops, and the pair waits
+// for what it issued before it frees tensor memory and leaves.
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -25,290 +38,401 @@ namespace s4 {
 namespace {
 
 enum { kI8 = 0, kBf16 = 1 };
-constexpr int kTileM = 128;               // rows of a CTA's accumulator: the TMEM lanes
-constexpr int kRowBytes = 128;            // bytes of K per stage (K-major), one swizzle atom row
-constexpr int kPitch = 36;                // staging row pitch in words: conflict-free both ways
+constexpr int kLanes = 128;               // columns m per CTA: the TMEM lanes
+constexpr int kRowBytes = 128;            // bytes of a swizzle atom row
 
-template <int KIND, bool A_MN, bool B_MN, int BN, int NA, int NB, int STAGES>
+// KIND; A_MN/B_MN: the operand's row index (not k) is contiguous; R: rows of
+// a tile; PA, PB: bfloat16 parts; ND: digit planes of B (stacked along N);
+// CG: CTAs per tile; CHUNK: k-blocks per accumulation into registers (0: the
+// whole sum in tensor memory).
+template <int KIND_, bool A_MN_, bool B_MN_, int R_, int PA_, int PB_, int ND_, int CG_, int STAGES_, int CHUNK_>
 struct Cfg {
-  static constexpr int kKElems = KIND == kI8 ? 128 : 64;       // K per stage
-  static constexpr int kATile = kTileM * kRowBytes;
-  static constexpr int kBTile = BN * kRowBytes;
-  static constexpr int kStage = NA * kATile + NB * kBTile;
-  static constexpr int kEpiWarp = 32 * kPitch * 4;
-  static constexpr int kSmem = STAGES * kStage + 4 * kEpiWarp + 1024;
-  static constexpr int kTmemCols = 2 * BN;
+  static constexpr int KIND = KIND_, R = R_, PA = PA_, PB = PB_, ND = ND_, CG = CG_, STAGES = STAGES_, CHUNK = CHUNK_;
+  static constexpr bool A_MN = A_MN_, B_MN = B_MN_;
+  static constexpr int kK = KIND == kI8 ? 128 : 64;            // k per stage
+  static constexpr int kN = ND * R;                            // MMA N
+  static constexpr int kBRows = R / CG;                        // rows of each digit plane a CTA stages
+  static constexpr int kATile = kLanes * kRowBytes;
+  static constexpr int kBTile = ND * kBRows * kRowBytes;
+  static constexpr int kStage = PA * kATile + PB * kBTile;
+  static constexpr int kSmem = STAGES * kStage + 1024;
+  // with several parts the products of lower parts (2^-8 of the first and
+  // less) have columns of their own: the tensor core truncates each addition
+  // at the accumulator's magnitude
+  static constexpr bool kSmallApart = PA > 1 || PB > 1;
+  static constexpr int kAccCols = kN <= 128 && !kSmallApart ? 128 : 256;   // columns from one accumulator to the other
+  static_assert(!kSmallApart || 2 * kN <= kAccCols, "both sums fit");
+  static constexpr int kTmemCols = 2 * kAccCols;
   static_assert(kSmem <= 227 * 1024, "stages fit in shared memory");
-  static_assert(KIND == kBf16 || (!A_MN && !B_MN && NA == 1 && NB == 1), "codes are K-major");
+  static_assert(kN <= 256 && kN % 32 == 0 && kBRows % 8 == 0 && kBTile % 1024 == 0, "tile shape");
+  static_assert(KIND == kBf16 || (PA == 1 && PB == 1 && !B_MN), "integer operands");
+  static_assert(KIND == kI8 || (ND == 1 && A_MN), "bfloat16 operands");
 };
 
 struct GemmArgs {
-  CUtensorMap a[2], b[2];
-  int32_t M, N, kblocks, tiles_m, tiles_n;
+  CUtensorMap a, b;
+  int32_t M, R, kblocks, tiles_m, tiles_r;
   uint32_t* flags;
   Act8Out out;
 };
 
-// Instruction descriptor: fp32 sums of bfloat16 (type code 1) or int32 sums
-// of signed 8-bit integers (type code 1, accumulator code 2).
-template <int KIND>
-__host__ __device__ constexpr uint32_t idesc(int M, int N, int a_mn, int b_mn) {
-  return ((KIND == kI8 ? 2u : 1u) << 4) | (1u << 7) | (1u << 10) | (uint32_t(a_mn) << 15) | (uint32_t(b_mn) << 16) |
-         (uint32_t(N >> 3) << 17) | (uint32_t(M >> 4) << 24);
+// Instruction descriptor: fp32 sums of bfloat16 (type code 1, accumulator
+// code 1) or int32 sums of signed 8-bit integers (type code 1, accumulator
+// code 2).
+template <class C>
+__host__ __device__ constexpr uint32_t idesc() {
+  return ((C::KIND == kI8 ? 2u : 1u) << 4) | (1u << 7) | (1u << 10) | (uint32_t(C::A_MN) << 15) |
+         (uint32_t(C::B_MN) << 16) | (uint32_t(C::kN >> 3) << 17) | (uint32_t((C::CG * kLanes) >> 4) << 24);
 }
 
-template <int KIND>
+template <int KIND, int CG>
 __device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
-  if (KIND == kI8)
+#define S4_MMA(group, kind)                                               \
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"          \
+               "tcgen05.mma.cta_group::" group ".kind::" kind " [%0], %1, %2, %3, p;\n\t}" \
+               ::"r"(d), "l"(a), "l"(b), "r"(id), "r"(acc) : "memory")
+  if (KIND == kI8) {
+    if (CG == 2) S4_MMA("2", "i8"); else S4_MMA("1", "i8");
+  } else {
+    if (CG == 2) S4_MMA("2", "f16"); else S4_MMA("1", "f16");
+  }
+#undef S4_MMA
+}
+
+// Shared-memory address of the same variable in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t in_cta(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ uint32_t cta_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+// Tile load whose bytes count on a barrier of either CTA of the pair.
+template <int CG>
+__device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap* map, int x, int y, int plane, uint32_t bar) {
+  if (CG == 2)
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}"
-        ::"r"(d), "l"(a), "l"(b), "r"(id), "r"(acc) : "memory");
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2 "
+        "[%0], [%1, {%2, %3, %4}], [%5];"
+        ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(plane), "r"(bar) : "memory");
   else
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
-        ::"r"(d), "l"(a), "l"(b), "r"(id), "r"(acc) : "memory");
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
+        ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(plane), "r"(bar) : "memory");
+}
+// Arrive on the barrier (of every CTA of the pair) once the MMAs issued so far are done.
+template <int CG>
+__device__ __forceinline__ void commit(uint64_t* bar) {
+  if (CG == 2)
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
+        ::"r"(smem_u32(bar)), "h"(uint16_t(3)) : "memory");
+  else
+    mma_commit(bar);
 }
 
-// K-major (128-byte swizzle): rows of 128 B, 8-row groups 1024 B apart, an
-// MMA's K (32 bytes) along the row.  MN-major: boxes of 64 elements (128 B)
-// by 64 K rows, 8192 B apart; 8-row K groups 1024 B apart, an MMA's K is 16
-// rows.
-template <bool MN>
+// K-major (128-byte swizzle): rows of 128 B, 8-row groups 1024 B apart; an
+// MMA's k (32 bytes) lies along the row.  MN-major: boxes of 128 bytes of
+// rows by kK k's, one box per 128 bytes of rows; 8-k groups 1024 B apart,
+// an MMA's k is 32 (int8) or 16 (bfloat16) box rows.
+template <class C, bool MN>
 __device__ __forceinline__ uint64_t tile_desc(uint32_t base, int kk) {
-  return MN ? smem_desc(base + kk * 2048, 8192, 1024, 2) : smem_desc(base + kk * 32, 16, 1024, 2);
+  constexpr int kStep = C::KIND == kI8 ? 4096 : 2048;
+  return MN ? smem_desc(base + kk * kStep, C::kK * kRowBytes, 1024, 2) : smem_desc(base + kk * 32, 16, 1024, 2);
 }
 
-template <bool MN, int ROWS, int KELEMS>
-__device__ __forceinline__ void load_tile(const CUtensorMap* map, int mn0, int k0, uint32_t dst, uint64_t* bar) {
+// Rows mn0 .. mn0 + rows - 1 by k0 .. k0 + kK - 1 of one operand plane.
+template <class C, bool MN, int ROWS>
+__device__ __forceinline__ void load_tile(const CUtensorMap* map, int mn0, int k0, int plane, uint32_t dst,
+                                          uint32_t bar) {
   if (!MN) {
-    tma_load_2d(dst, map, k0, mn0, bar);
+    load_box<C::CG>(dst, map, k0, mn0, plane, bar);
   } else {
+    constexpr int kWide = C::KIND == kI8 ? 128 : 64;                // elements of 128 bytes
 #pragma unroll
-    for (int g = 0; g < ROWS / 64; ++g) tma_load_2d(dst + g * 8192, map, mn0 + 64 * g, k0, bar);
+    for (int g = 0; g < (ROWS + kWide - 1) / kWide; ++g)
+      load_box<C::CG>(dst + g * C::kK * kRowBytes, map, mn0 + kWide * g, k0, plane, bar);
   }
 }
 
 // Tile t in an order that keeps the tiles in flight close in both operands:
-// groups of 8 tile rows, walked column by column.
-__device__ __forceinline__ void tile_of(const GemmArgs& g, int t, int& tm, int& tn) {
-  const int per = 8 * g.tiles_n;
-  const int grp = t / per, r = t - grp * per;
-  const int rows = min(8, g.tiles_m - 8 * grp);
-  tn = r / rows;
-  tm = 8 * grp + (r - tn * rows);
+// groups of 8 column tiles, walked row tile by row tile.
+__device__ __forceinline__ void tile_of(const GemmArgs& g, int t, int& tm, int& tr) {
+  const int per = 8 * g.tiles_r;
+  const int grp = t / per, x = t - grp * per;
+  const int cols = min(8, g.tiles_m - 8 * grp);
+  tr = x / cols;
+  tm = 8 * grp + (x - tr * cols);
 }
 
 __device__ __forceinline__ float to_f32(float x) { return x; }
 __device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ float to_f32(__half x) { return __half2float(x); }
-template <class T> __device__ __forceinline__ T from_f32(float x);
-template <> __device__ __forceinline__ float from_f32<float>(float x) { return x; }
-template <> __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
-template <> __device__ __forceinline__ __half from_f32<__half>(float x) { return __float2half_rn(x); }
+__device__ __forceinline__ void put(float* p, float x) { *p = x; }
+__device__ __forceinline__ void put(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
+__device__ __forceinline__ void put(__half* p, float x) { *p = __float2half_rn(x); }
 
-// Four results (columns c .. c + 3 of one row) into y, rounded once.
-template <class T>
-__device__ __forceinline__ void store4(T* p, int c, int N, bool vec, bool add, float (&v)[4]) {
-  struct alignas(4 * sizeof(T)) V4 { T e[4]; };
-  if (vec && c + 4 <= N) {
-    if (add) {
-      const V4 o = *reinterpret_cast<const V4*>(p);
+// A chunk of 32 rows (TMEM columns) of this lane's column m.
+template <class C>
+__device__ __forceinline__ void load_chunk(uint32_t tacc, int i, float (&v)[32]) {
+  uint32_t r[32];
+  if (C::ND == 1) {
+    tmem_ld32(tacc + uint32_t(32 * i), r);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) v[j] += to_f32(o.e[j]);
+    for (int j = 0; j < 32; ++j) v[j] = C::KIND == kI8 ? __int2float_rn(int(r[j])) : __uint_as_float(r[j]);
+    if (C::kSmallApart) {
+      tmem_ld32(tacc + uint32_t(C::kN + 32 * i), r);
+#pragma unroll
+      for (int j = 0; j < 32; ++j) v[j] += __uint_as_float(r[j]);
     }
-    V4 r;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) r.e[j] = from_f32<T>(v[j]);
-    *reinterpret_cast<V4*>(p) = r;
   } else {
+    // MMA columns: [CTA half][digit][row of the half]
+    constexpr int kPer = C::kBRows / 32;
+    const uint32_t c = tacc + uint32_t((i / kPer) * C::ND * C::kBRows + 32 * (i % kPer));
+    static_assert(C::ND == 1 || C::kBRows % 32 == 0, "a chunk lies in one half");
+    tmem_ld32(c, r);
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (c + j < N) p[j] = from_f32<T>(add ? v[j] + to_f32(p[j]) : v[j]);
+    for (int j = 0; j < 32; ++j) v[j] = __int2float_rn(int(r[j]));
+#pragma unroll
+    for (int d = 1; d < C::ND; ++d) {
+      tmem_ld32(c + uint32_t(d * C::kBRows), r);
+#pragma unroll
+      for (int j = 0; j < 32; ++j) v[j] = fmaf(v[j], 256.0f, __int2float_rn(int(r[j])));
+    }
   }
 }
 
-// Rows m0 .. m0 + 31 and columns n0 .. n0 + BN - 1 by one epilogue warp:
-// 32 columns at a time out of tensor memory (lane = row), transposed through
-// the warp's staging block, then lane l takes row 4 t + l / 8, columns
-// 4 (l % 8) .. + 3, so a store instruction covers four full row segments.
-template <int KIND, int BN, class T>
-__device__ __forceinline__ void drain(const GemmArgs& g, uint32_t tacc, int m0, int n0, int lane, float* stage) {
-  T* y = static_cast<T*>(g.out.y);
-  const int64_t ld = g.out.ld;
-  const int M = g.M, N = g.N;
-  const bool vec = ((reinterpret_cast<uintptr_t>(y) | uintptr_t(ld * int64_t(sizeof(T)))) % (4 * sizeof(T))) == 0;
-  const bool add = g.out.accumulate != 0;
-  const bool any = g.kblocks > 0;
-  const int sr = lane >> 3, sc = 4 * (lane & 7);
-  float rs[8];
+// 32 rows r0.. of column m to Y: a store instruction writes 32 consecutive
+// columns of a row.  A chunk inside the matrix goes out without a test per
+// row: with one, the warp waits for each row's shuffle in turn and the
+// epilogue, not the products, set the pace (391 against 265 us at 8192 x
+// 11008 x 4096).
+template <class T>
+__device__ __forceinline__ void store_chunk(const Act8Out& o, int R, int M, int r0, int m, float cs, float bias,
+                                            float rs_lane, float (&v)[32]) {
+  T* y = static_cast<T*>(o.y) + int64_t(r0) * o.ld + m;
 #pragma unroll
-  for (int t = 0; t < 8; ++t) {
-    const int r = m0 + 4 * t + sr;
-    rs[t] = (g.out.row_scale && r < M) ? __ldg(g.out.row_scale + r) : 1.0f;
-  }
-#pragma unroll 1
-  for (int c0 = 0; c0 < BN && n0 + c0 < N; c0 += 32) {
-    uint32_t r[32];
-    if (any) {
-      tmem_ld32(tacc + uint32_t(c0), r);
-    } else {
+  for (int j = 0; j < 32; ++j) v[j] = fmaf(v[j] * __shfl_sync(0xffffffffu, rs_lane, j), cs, bias);
+  if (!o.accumulate && r0 + 32 <= R && __all_sync(0xffffffffu, m < M)) {
 #pragma unroll
-      for (int j = 0; j < 32; ++j) r[j] = 0u;
-    }
-    __syncwarp();                                        // the previous chunk's reads are done
+    for (int j = 0; j < 32; ++j) put(y + int64_t(j) * o.ld, v[j]);
+  } else if (m < M) {
 #pragma unroll
-    for (int j = 0; j < 32; j += 4) {
-      float4 x;
-      if (KIND == kI8)
-        x = make_float4(__int2float_rn(int(r[j])), __int2float_rn(int(r[j + 1])), __int2float_rn(int(r[j + 2])),
-                        __int2float_rn(int(r[j + 3])));
-      else
-        x = make_float4(__uint_as_float(r[j]), __uint_as_float(r[j + 1]), __uint_as_float(r[j + 2]),
-                        __uint_as_float(r[j + 3]));
-      *reinterpret_cast<float4*>(stage + lane * kPitch + j) = x;
-    }
-    __syncwarp();
-    const int c = n0 + c0 + sc;
-    float cs[4], bi[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      cs[j] = (g.out.col_scale && c + j < N) ? __ldg(g.out.col_scale + c + j) : 1.0f;
-      bi[j] = (g.out.bias && c + j < N) ? __ldg(g.out.bias + c + j) : 0.0f;
-    }
-#pragma unroll
-    for (int t = 0; t < 8; ++t) {
-      const int row = m0 + 4 * t + sr;
-      const float4 x = *reinterpret_cast<const float4*>(stage + (4 * t + sr) * kPitch + sc);
-      float v[4] = {x.x, x.y, x.z, x.w};
-      if (KIND == kI8) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] = v[j] * rs[t] * cs[j] + bi[j];
+    for (int j = 0; j < 32; ++j)
+      if (r0 + j < R) {
+        T* p = y + int64_t(j) * o.ld;
+        put(p, o.accumulate ? v[j] + to_f32(*p) : v[j]);
       }
-      if (row < M && c < N) store4<T>(y + int64_t(row) * ld + c, c, N, vec, add, v);
-    }
   }
 }
+__device__ __forceinline__ void store_any(const Act8Out& o, int R, int M, int r0, int m, float cs, float bias,
+                                          float rs_lane, float (&v)[32]) {
+  if (o.dtype == ACT8_FP32) store_chunk<float>(o, R, M, r0, m, cs, bias, rs_lane, v);
+  else if (o.dtype == ACT8_BF16) store_chunk<__nv_bfloat16>(o, R, M, r0, m, cs, bias, rs_lane, v);
+  else store_chunk<__half>(o, R, M, r0, m, cs, bias, rs_lane, v);
+}
+__device__ __forceinline__ float row_scale(const Act8Out& o, int R, int r) {
+  return o.row_scale && r < R ? __ldg(o.row_scale + r) : 1.0f;
+}
 
-template <int KIND, bool A_MN, bool B_MN, int BN, int NA, int NB, int STAGES>
+template <class C>
 __global__ void __launch_bounds__(192, 1) k_act8_gemm(const __grid_constant__ GemmArgs g) {
-  using C = Cfg<KIND, A_MN, B_MN, BN, NA, NB, STAGES>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  __shared__ uint64_t full_bar[STAGES], empty_bar[STAGES], acc_full[2], acc_empty[2], done_bar;
+  __shared__ uint64_t full_bar[C::STAGES], empty_bar[C::STAGES], acc_full[2], acc_empty[2], done_bar;
   __shared__ uint32_t tmem_slot;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = C::CG == 2 ? cta_rank() : 0u;
   if (threadIdx.x == 0) {
-    for (int s = 0; s < STAGES; ++s) {
+    for (int s = 0; s < C::STAGES; ++s) {
       mbar_init(&full_bar[s], 1);
       mbar_init(&empty_bar[s], 1);
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&acc_full[s], 1);
-      mbar_init(&acc_empty[s], 4);
+      mbar_init(&acc_empty[s], 4 * C::CG);
     }
     mbar_init(&done_bar, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 1) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_slot)),
-                 "r"(C::kTmemCols)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    if (C::CG == 2) {
+      asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_slot)),
+                   "r"(C::kTmemCols) : "memory");
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    } else {
+      asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_slot)),
+                   "r"(C::kTmemCols) : "memory");
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
   }
   fence_before_sync();
   __syncthreads();
+  if (C::CG == 2) cluster_sync();
   fence_after_sync();
   const uint32_t tmem = tmem_slot;
-  const int tiles = g.tiles_m * g.tiles_n, kblocks = g.kblocks;
+  const int tiles = g.tiles_m * g.tiles_r, kblocks = g.kblocks;
+  const int first = blockIdx.x / C::CG, step = gridDim.x / C::CG;
+  const int chunk = C::CHUNK ? C::CHUNK : max(kblocks, 1);
 
   if (warp == 0) {
     if (lane == 0) {                                        // ---- loads
       int it = 0;
       bool ok = true;
-      for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
-        int tm, tn;
-        tile_of(g, t, tm, tn);
-        const int m0 = tm * kTileM, n0 = tn * BN;
+      for (int t = first; ok && t < tiles; t += step) {
+        int tm, tr;
+        tile_of(g, t, tm, tr);
+        const int m0 = (tm * C::CG + int(rank)) * kLanes, r0 = tr * C::R + int(rank) * C::kBRows;
         for (int kb = 0; kb < kblocks; ++kb, ++it) {
-          const int s = it % STAGES;
-          if (!mbar_wait(&empty_bar[s], ((it / STAGES) & 1) ^ 1)) { ok = false; break; }
+          const int s = it % C::STAGES;
+          if (!mbar_wait(&empty_bar[s], ((it / C::STAGES) & 1) ^ 1)) { ok = false; break; }
           uint32_t dst = smem_u32(smem + s * C::kStage);
-          mbar_expect_tx(&full_bar[s], C::kStage);
+          uint32_t bar = smem_u32(&full_bar[s]);
+          if (rank == 0) mbar_expect_tx(&full_bar[s], C::CG * C::kStage);
+          if (C::CG == 2) bar = in_cta(bar, 0);
+          const int k0 = kb * C::kK;
 #pragma unroll
-          for (int p = 0; p < NA; ++p, dst += C::kATile)
-            load_tile<A_MN, kTileM, C::kKElems>(&g.a[p], m0, kb * C::kKElems, dst, &full_bar[s]);
+          for (int p = 0; p < C::PA; ++p, dst += C::kATile)
+            load_tile<C, C::A_MN, kLanes>(&g.a, m0, k0, p, dst, bar);
 #pragma unroll
-          for (int p = 0; p < NB; ++p, dst += C::kBTile)
-            load_tile<B_MN, BN, C::kKElems>(&g.b[p], n0, kb * C::kKElems, dst, &full_bar[s]);
+          for (int p = 0; p < C::PB * C::ND; ++p, dst += C::kBRows * kRowBytes)
+            load_tile<C, C::B_MN, C::kBRows>(&g.b, r0, k0, p, dst, bar);
         }
       }
-      // every stage's last load has been consumed (or, after a timeout, has landed) before the CTA leaves
-      for (int i = max(0, it - STAGES); i < it; ++i)
-        if (!mbar_wait(ok ? &empty_bar[i % STAGES] : &full_bar[i % STAGES], (i / STAGES) & 1)) ok = false;
+      // every stage this CTA filled has been read before it leaves
+      for (int i = max(0, it - C::STAGES); i < it; ++i)
+        if (!mbar_wait(&empty_bar[i % C::STAGES], (i / C::STAGES) & 1)) { ok = false; break; }
       if (!ok && g.flags) atomicOr(g.flags, SHAMPOO4_FLAG_TIMEOUT);
     }
   } else if (warp == 1) {
-    if (lane == 0) {                                        // ---- products
-      constexpr uint32_t id = idesc<KIND>(kTileM, BN, A_MN, B_MN);
+    if (lane == 0 && rank == 0) {                           // ---- products
+      constexpr uint32_t id = idesc<C>();
+      constexpr int kParts = C::PA > C::PB ? C::PA : C::PB;
       int it = 0, i = 0;
       bool ok = true;
-      for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x, ++i) {
-        const int ab = i & 1;
-        if (!mbar_wait(&acc_empty[ab], ((i >> 1) & 1) ^ 1)) { ok = false; break; }
-        fence_after_sync();
-        const uint32_t d = tmem + uint32_t(ab * BN);
-        for (int kb = 0; kb < kblocks; ++kb, ++it) {
-          const int s = it % STAGES;
-          if (!mbar_wait(&full_bar[s], (it / STAGES) & 1)) { ok = false; break; }
+      for (int t = first; ok && t < tiles; t += step) {
+        for (int kb = 0; ok && (kb < kblocks || kb == 0); ++i) {
+          const int ab = i & 1;
+          if (!mbar_wait(&acc_empty[ab], ((i >> 1) & 1) ^ 1)) { ok = false; break; }
           fence_after_sync();
-          const uint32_t a0 = smem_u32(smem + s * C::kStage), b0 = a0 + NA * C::kATile;
+          const uint32_t d = tmem + uint32_t(ab * C::kAccCols);
+          const int k_end = min(kb + chunk, kblocks);
+          const int k_first = kb;
+          for (; kb < k_end; ++kb, ++it) {
+            const int s = it % C::STAGES;
+            if (!mbar_wait(&full_bar[s], (it / C::STAGES) & 1)) { ok = false; break; }
+            fence_after_sync();
+            const uint32_t a0 = smem_u32(smem + s * C::kStage), b0 = a0 + C::PA * C::kATile;
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk) {
-            mma<KIND>(d, tile_desc<A_MN>(a0, kk), tile_desc<B_MN>(b0, kk), id, (kb | kk) != 0);
-            if (NB == 2) mma<KIND>(d, tile_desc<A_MN>(a0, kk), tile_desc<B_MN>(b0 + C::kBTile, kk), id, 1);
-            if (NA == 2) mma<KIND>(d, tile_desc<A_MN>(a0 + C::kATile, kk), tile_desc<B_MN>(b0, kk), id, 1);
+            for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+              for (int pa = 0; pa < C::PA; ++pa)
+#pragma unroll
+                for (int pb = 0; pb < C::PB; ++pb)
+                  if (pa + pb < kParts) {
+                    // the first product into each of the two sums overwrites it
+                    const bool opens = pa + pb == 0 || (C::PB > 1 ? pa == 0 && pb == 1 : pa == 1);
+                    mma<C::KIND, C::CG>(d + (pa + pb > 0 ? C::kN : 0),
+                                        tile_desc<C, C::A_MN>(a0 + pa * C::kATile, kk),
+                                        tile_desc<C, C::B_MN>(b0 + pb * C::kBTile, kk), id,
+                                        !(opens && kb == k_first && kk == 0));
+                  }
+            commit<C::CG>(&empty_bar[s]);
           }
-          mma_commit(&empty_bar[s]);
+          if (ok) commit<C::CG>(&acc_full[ab]);
+          if (kblocks == 0) { ++i; break; }
         }
-        if (ok) mma_commit(&acc_full[ab]);
       }
       // all MMAs issued are finished before tensor memory is freed
-      mma_commit(&done_bar);
+      if (C::CG == 2)
+        asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+            smem_u32(&done_bar)) : "memory");
+      else
+        mma_commit(&done_bar);
       if (!mbar_wait(&done_bar, 0)) ok = false;
       if (!ok && g.flags) atomicOr(g.flags, SHAMPOO4_FLAG_TIMEOUT);
     }
   } else {                                                  // ---- epilogue, warps 2..5
     const int q = warp & 3;                                 // TMEM lane quarter
-    float* stage = reinterpret_cast<float*>(smem + STAGES * C::kStage + q * C::kEpiWarp);
+    constexpr int kChunks = C::R / 32;
     int i = 0;
-    for (int t = blockIdx.x; t < tiles; t += gridDim.x, ++i) {
-      const int ab = i & 1;
-      if (!mbar_wait(&acc_full[ab], (i >> 1) & 1)) {
-        if (g.flags && lane == 0) atomicOr(g.flags, SHAMPOO4_FLAG_TIMEOUT);
-        break;
+    bool ok = true;
+    for (int t = first; ok && t < tiles; t += step) {
+      int tm, tr;
+      tile_of(g, t, tm, tr);
+      const int m = (tm * C::CG + int(rank)) * kLanes + 32 * q + lane, r0 = tr * C::R;
+      const float cs = g.out.col_scale && m < g.M ? __ldg(g.out.col_scale + m) : 1.0f;
+      const float bias = g.out.bias && m < g.M ? __ldg(g.out.bias + m) : 0.0f;
+      const int passes = max(1, (kblocks + chunk - 1) / chunk);
+      float sum[C::CHUNK ? kChunks : 1][32];
+      for (int pass = 0; pass < passes; ++pass, ++i) {
+        const int ab = i & 1;
+        if (!mbar_wait(&acc_full[ab], (i >> 1) & 1)) {
+          if (g.flags && lane == 0) atomicOr(g.flags, SHAMPOO4_FLAG_TIMEOUT);
+          ok = false;
+          break;
+        }
+        fence_after_sync();
+        const uint32_t tacc = tmem + uint32_t(ab * C::kAccCols) + (uint32_t(32 * q) << 16);
+        if (C::CHUNK) {
+#pragma unroll
+          for (int c = 0; c < kChunks; ++c) {
+            float v[32];
+            if (kblocks > 0) load_chunk<C>(tacc, c, v);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              const float x = kblocks > 0 ? v[j] : 0.0f;
+              sum[c][j] = pass == 0 ? x : sum[c][j] + x;
+            }
+          }
+        } else {
+#pragma unroll 1
+          for (int c = 0; c < kChunks && r0 + 32 * c < g.R; ++c) {
+            float v[32];
+            if (kblocks > 0) {
+              load_chunk<C>(tacc, c, v);
+            } else {
+#pragma unroll
+              for (int j = 0; j < 32; ++j) v[j] = 0.0f;
+            }
+            store_any(g.out, g.R, g.M, r0 + 32 * c, m, cs, bias, row_scale(g.out, g.R, r0 + 32 * c + lane), v);
+          }
+        }
+        fence_before_sync();
+        __syncwarp();
+        if (lane == 0) {
+          if (C::CG == 2)
+            asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(
+                in_cta(smem_u32(&acc_empty[ab]), 0)) : "memory");
+          else
+            mbar_arrive(&acc_empty[ab]);
+        }
       }
-      fence_after_sync();
-      int tm, tn;
-      tile_of(g, t, tm, tn);
-      const uint32_t tacc = tmem + uint32_t(ab * BN) + (uint32_t(32 * q) << 16);
-      const int m0 = tm * kTileM + 32 * q, n0 = tn * BN;
-      if (g.out.dtype == ACT8_FP32) drain<KIND, BN, float>(g, tacc, m0, n0, lane, stage);
-      else if (g.out.dtype == ACT8_BF16) drain<KIND, BN, __nv_bfloat16>(g, tacc, m0, n0, lane, stage);
-      else drain<KIND, BN, __half>(g, tacc, m0, n0, lane, stage);
-      fence_before_sync();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&acc_empty[ab]);
+      if (C::CHUNK && ok) {
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c)
+          if (r0 + 32 * c < g.R)
+            store_any(g.out, g.R, g.M, r0 + 32 * c, m, cs, bias, row_scale(g.out, g.R, r0 + 32 * c + lane), sum[c]);
+      }
     }
   }
   fence_before_sync();
   __syncthreads();
+  if (C::CG == 2) cluster_sync();
+  __syncwarp();
   if (warp == 1) {
     fence_after_sync();
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::kTmemCols)
-                 : "memory");
+    if (C::CG == 2)
+      asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::kTmemCols) : "memory");
+    else
+      asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::kTmemCols) : "memory");
   }
 }
 
@@ -326,83 +450,93 @@ PFN_cuTensorMapEncodeTiled_v12000 encoder() {
   return fn;
 }
 
-// Tensor map of a rows x cols row-major matrix, box of 128 bytes of a row by
-// box_rows, 128-byte swizzle, zeros outside.
-shampoo4_status encode(CUtensorMap* out, int kind, const void* base, int64_t rows, int64_t cols, int64_t ld,
+// Tensor map of an operand's planes (rows x cols each, row-major), box of
+// 128 bytes of a row by box_rows, 128-byte swizzle, zeros outside a plane.
+shampoo4_status encode(CUtensorMap* out, int kind, const Act8Operand& x, int64_t rows, int64_t cols, int planes,
                        int box_rows) {
   auto fn = encoder();
   if (!fn) return SHAMPOO4_ERR_CUDA;
   const int64_t esize = kind == kI8 ? 1 : 2;
-  if ((ld * esize) % 16 != 0 || reinterpret_cast<uintptr_t>(base) % 16 != 0) return SHAMPOO4_ERR_INVALID_ARG;
-  cuuint64_t dims[2] = {cuuint64_t(cols), cuuint64_t(rows)};
-  cuuint64_t strides[1] = {cuuint64_t(ld * esize)};
-  cuuint32_t box[2] = {cuuint32_t(128 / esize), cuuint32_t(box_rows)};
-  cuuint32_t estr[2] = {1u, 1u};
-  const CUresult r = fn(out, kind == kI8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
-                        const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+  if ((x.ld * esize) % 16 != 0 || reinterpret_cast<uintptr_t>(x.p) % 16 != 0) return SHAMPOO4_ERR_INVALID_ARG;
+  cuuint64_t dims[3] = {cuuint64_t(cols), cuuint64_t(rows), cuuint64_t(planes)};
+  cuuint64_t strides[2] = {cuuint64_t(x.ld * esize), cuuint64_t(planes > 1 ? x.plane * x.ld * esize : x.ld * esize)};
+  cuuint32_t box[3] = {cuuint32_t(128 / esize), cuuint32_t(box_rows), 1u};
+  cuuint32_t estr[3] = {1u, 1u, 1u};
+  const CUresult r = fn(out, kind == kI8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+                        const_cast<void*>(x.p), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? SHAMPOO4_OK : SHAMPOO4_ERR_CUDA;
 }
 
-template <int KIND, bool A_MN, bool B_MN, int BN, int NA, int NB, int STAGES>
-shampoo4_status launch(GemmArgs& g, int64_t M, int64_t N, int64_t K, cudaStream_t st) {
-  using C = Cfg<KIND, A_MN, B_MN, BN, NA, NB, STAGES>;
-  auto kern = k_act8_gemm<KIND, A_MN, B_MN, BN, NA, NB, STAGES>;
+template <class C>
+shampoo4_status launch(const Act8Operand& a, const Act8Operand& b, int64_t M, int64_t R, int64_t K,
+                       const Act8Out& out, uint32_t* flags, cudaStream_t st) {
+  GemmArgs g{};
+  g.out = out;
+  g.flags = flags;
   g.M = int32_t(M);
-  g.N = int32_t(N);
-  g.kblocks = int32_t((K + C::kKElems - 1) / C::kKElems);
-  const int64_t tm = (M + kTileM - 1) / kTileM, tn = (N + BN - 1) / BN;
-  if (tm * tn > INT_MAX / 2) return SHAMPOO4_ERR_INVALID_ARG;
+  g.R = int32_t(R);
+  g.kblocks = int32_t((K + C::kK - 1) / C::kK);
+  if (K > 0) {
+    S4_TRY(C::A_MN ? encode(&g.a, C::KIND, a, K, M, C::PA, C::kK) : encode(&g.a, C::KIND, a, M, K, C::PA, kLanes));
+    S4_TRY(C::B_MN ? encode(&g.b, C::KIND, b, K, R, C::PB * C::ND, C::kK)
+                   : encode(&g.b, C::KIND, b, R, K, C::PB * C::ND, C::kBRows));
+  }
+  const int64_t tm = (M + C::CG * kLanes - 1) / (C::CG * kLanes), tr = (R + C::R - 1) / C::R;
+  if (tm * tr > INT_MAX / 16) return SHAMPOO4_ERR_INVALID_ARG;
   g.tiles_m = int32_t(tm);
-  g.tiles_n = int32_t(tn);
-  S4_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem));
+  g.tiles_r = int32_t(tr);
+  auto kern = k_act8_gemm<C>;
   int dev = 0, sms = 0;
   S4_CUDA(cudaGetDevice(&dev));
   S4_CUDA(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
-  kern<<<unsigned(std::min<int64_t>(tm * tn, sms)), 192, C::kSmem, st>>>(g);
-  S4_CUDA(cudaGetLastError());
+  S4_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem));
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(unsigned(C::CG * std::min<int64_t>(tm * tr, sms / C::CG)));
+  cfg.blockDim = dim3(192);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = C::CG;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  S4_CUDA(cudaLaunchKernelEx(&cfg, kern, g));
   return SHAMPOO4_OK;
 }
 
 }  // namespace
 
-shampoo4_status launch_act8_gemm_i8(const int8_t* a, int64_t lda, const int8_t* b, int64_t ldb, int64_t M, int64_t N,
-                                    int64_t K, const Act8Out& out, uint32_t* flags, cudaStream_t st) {
-  GemmArgs g{};
-  g.out = out;
-  g.flags = flags;
-  if (K > 0) {
-    S4_TRY(encode(&g.a[0], kI8, a, M, K, lda, kTileM));
-    S4_TRY(encode(&g.b[0], kI8, b, N, K, ldb, 256));
-  }
-  return launch<kI8, false, false, 256, 1, 1, 4>(g, M, N, K, st);
+//                               kind   A_MN   B_MN   R   PA PB ND CG stages chunk
+using CodesCfg = Cfg<            kI8,   false, false, 256, 1, 1, 1, 2, 6, 0>;
+using DigitsCfg = Cfg<           kI8,   true,  false, 64,  1, 1, kAct8Digits, 2, 7, 1024>;
+template <bool B_MN> using Bf16Cfg = Cfg<kBf16, true, B_MN, 256, 1, 1, 1, 2, 6, 0>;
+template <bool B_MN, int PA, int PB, int STAGES>
+using PartsCfg = Cfg<            kBf16, true,  B_MN,  128, PA, PB, 1, 2, STAGES, 4>;
+
+shampoo4_status launch_act8_codes(const Act8Operand& a, const Act8Operand& b, int64_t M, int64_t R, int64_t K,
+                                  const Act8Out& out, uint32_t* flags, cudaStream_t st) {
+  return launch<CodesCfg>(a, b, M, R, K, out, flags, st);
 }
 
-shampoo4_status launch_act8_gemm_bf16(const Act8Parts& a, int a_mn, const Act8Parts& b, int64_t M, int64_t N,
-                                      int64_t K, const Act8Out& out, uint32_t* flags, cudaStream_t st) {
-  GemmArgs g{};
-  g.out = out;
-  g.flags = flags;
-  if (K > 0) {
-    const void* ap[2] = {a.hi, a.lo};
-    const void* bp[2] = {b.hi, b.lo};
-    for (int p = 0; p < 2; ++p) {
-      if (ap[p]) S4_TRY(a_mn ? encode(&g.a[p], kBf16, ap[p], K, M, a.ld, 64)
-                             : encode(&g.a[p], kBf16, ap[p], M, K, a.ld, kTileM));
-      if (bp[p]) S4_TRY(encode(&g.b[p], kBf16, bp[p], K, N, b.ld, 64));
-    }
-  }
-  const int na = a.lo ? 2 : 1, nb = b.lo ? 2 : 1;
-  if (na == 2 && nb == 1) return SHAMPOO4_ERR_INVALID_ARG;   // no caller rounds b while it splits a
-  if (a_mn) {
-    if (nb == 1) return launch<kBf16, true, true, 256, 1, 1, 4>(g, M, N, K, st);
-    if (na == 1) return launch<kBf16, true, true, 256, 1, 2, 2>(g, M, N, K, st);
-    return launch<kBf16, true, true, 256, 2, 2, 2>(g, M, N, K, st);
-  }
-  if (nb == 1) return launch<kBf16, false, true, 256, 1, 1, 4>(g, M, N, K, st);
-  if (na == 1) return launch<kBf16, false, true, 256, 1, 2, 2>(g, M, N, K, st);
-  return launch<kBf16, false, true, 256, 2, 2, 2>(g, M, N, K, st);
+shampoo4_status launch_act8_digits(const Act8Operand& a, const Act8Operand& b, int64_t M, int64_t R, int64_t K,
+                                   const Act8Out& out, uint32_t* flags, cudaStream_t st) {
+  return launch<DigitsCfg>(a, b, M, R, K, out, flags, st);
+}
+
+shampoo4_status launch_act8_bf16(const Act8Operand& a, int a_parts, const Act8Operand& b, int b_parts, int b_mn,
+                                 int64_t M, int64_t R, int64_t K, const Act8Out& out, uint32_t* flags,
+                                 cudaStream_t st) {
+  if (a_parts == 1 && b_parts == 1)
+    return b_mn ? launch<Bf16Cfg<true>>(a, b, M, R, K, out, flags, st)
+                : launch<Bf16Cfg<false>>(a, b, M, R, K, out, flags, st);
+  if (!b_mn || a_parts != 3) return SHAMPOO4_ERR_INVALID_ARG;    // only the weight gradient splits, its codes always in 3
+  if (b_parts == 1) return launch<PartsCfg<true, 3, 1, 3>>(a, b, M, R, K, out, flags, st);
+  if (b_parts == 2) return launch<PartsCfg<true, 3, 2, 3>>(a, b, M, R, K, out, flags, st);
+  return launch<PartsCfg<true, 3, 3, 3>>(a, b, M, R, K, out, flags, st);
 }
 
 }  // namespace s4

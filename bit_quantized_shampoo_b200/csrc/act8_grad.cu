@@ -1,0 +1,399 @@
+// Gradients of the 8-bit product, Y = X W^T:
+//
+//   act8_weight_grad   dW[o, i] = sum_t dY[t, o] sx[t] xc[t, i]
+//   act8_input_grad    dX[t, i] = sum_o dY[t, o] sw[o] wc[o, i]
+//
+// The scale belongs to the contraction index, so it has to go into a factor.
+// Three ways, chosen by the types and the scales alone (grad_path):
+//
+//  digits  One scale per row of codes.  F = dY * scale in fp32 becomes fixed
+//          point relative to its largest magnitude over the contraction,
+//          q = rint(F * Q / max|F|), Q = 127 (65536 + 256 + 1), in three
+//          signed base-256 digits; the codes stay as they are stored.  Three
+//          int8 products with exact int32 sums: the only error is q's
+//          rounding (half of max|F| / 2^23 per element) and a few fp32
+//          roundings at the end.  1.5 times a bfloat16 product's tensor-core
+//          time, against three times for operands split into bfloat16 parts.
+//  bf16    dY and the result bfloat16: the codes' values rounded to one
+//          bfloat16 (2^-8 at most, no more than the result's own rounding),
+//          dY as it is.  One bfloat16 product.
+//  parts   Scales per group of columns (no common factor per row): values and
+//          dY as exact-to-fp32 sums of bfloat16 parts (three for fp32, two
+//          for fp16, one for bfloat16), all products above 2^-24.
+//
+// The operand passes of this file stream; their bound is HBM bandwidth.
+#include <cooperative_groups.h>
+#include "act8_elt.cuh"
+
+namespace cg = cooperative_groups;
+
+namespace s4 {
+namespace {
+
+constexpr float kQMax = 8355711.0f;                    // 127 * 65536 + 127 * 256 + 127
+constexpr float kTiny = 0x1p-100f;                     // below it the fixed point stays that of kTiny
+
+// Fixed point of a row whose largest magnitude has these bits: the factor to
+// q and the scale back, NaN for a row that holds a NaN or an infinity.
+struct Fixed {
+  float inv, scale;
+  __device__ __forceinline__ explicit Fixed(uint32_t bits) {
+    const bool finite = bits < 0x7f800000u;
+    const float a = fmaxf(__uint_as_float(bits), kTiny);
+    inv = finite ? __fdiv_rn(kQMax, a) : 0.0f;
+    scale = finite ? __fdiv_rn(a, kQMax) : __uint_as_float(0x7fc00000u);
+  }
+  // The three digits as the low bytes, least significant first.
+  __device__ __forceinline__ uint32_t digits(float f) const {
+    const int q = inv == 0.0f ? 0 : __float2int_rn(fminf(fmaxf(f * inv, -kQMax), kQMax));
+    return uint32_t(q + 0x808080) ^ 0x808080u;
+  }
+};
+
+// Byte `b` of four words, the first word's in the low byte.
+__device__ __forceinline__ uint32_t bytes4(uint32_t x0, uint32_t x1, uint32_t x2, uint32_t x3, int b) {
+  const uint32_t sel = uint32_t(b | ((4 + b) << 4));
+  return __byte_perm(__byte_perm(x0, x1, sel), __byte_perm(x2, x3, sel), 0x5410);
+}
+
+// Rows of dY as they are (act8_input_grad): a CTA per row, read twice (the
+// second time from cache).
+template <class T>
+__global__ void __launch_bounds__(kThreads)
+k_act8_digit_rows(Mat dy, const float* __restrict__ scale, int8_t* digits, int64_t ld, float* row_scale, int64_t rows,
+                  int64_t cols) {
+  __shared__ uint32_t slots[kThreads / 32];
+  const int64_t row = blockIdx.x;
+  const T* x = static_cast<const T*>(dy.p) + row * dy.ld;
+  Raw8<T> r;
+  uint32_t m = 0;
+  for (int64_t c = threadIdx.x * 8; c < cols; c += kThreads * 8) {
+    load8(x, c, cols, dy.vec, r);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (c + i < cols) m = max(m, abs_bits(elt(r, i) * __ldg(scale + c + i)));
+  }
+  const Fixed f(cta_max(m, slots));
+  if (threadIdx.x == 0) row_scale[row] = f.scale;
+  for (int64_t c = threadIdx.x * 8; c < ld; c += kThreads * 8) {      // ld: the padding gets zeros
+    load8(x, c, cols, dy.vec, r);
+    uint32_t q[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) q[i] = c + i < cols ? f.digits(elt(r, i) * __ldg(scale + c + i)) : 0u;
+#pragma unroll
+    for (int d = 0; d < kAct8Digits; ++d) {
+      const int b = kAct8Digits - 1 - d;
+      *reinterpret_cast<uint2*>(digits + (d * rows + row) * ld + c) =
+          make_uint2(bytes4(q[0], q[1], q[2], q[3], b), bytes4(q[4], q[5], q[6], q[7], b));
+    }
+  }
+}
+
+// Columns of dY as rows of digits (act8_weight_grad): a cluster of 8 CTAs per
+// 64 columns, tiles of 128 tokens dealt round robin.  The first sweep finds
+// the columns' largest magnitudes (joined over distributed shared memory),
+// the second quantizes and transposes through shared memory, so that every
+// digit row is written in pieces of 128 bytes.  A thread holds 4 tokens by 8
+// columns of a tile.
+constexpr int kColTile = 64, kTokTile = 128, kColCluster = 8;
+template <class T>
+__global__ void __launch_bounds__(kThreads) __cluster_dims__(1, kColCluster, 1)
+k_act8_digit_columns(Mat dy, const float* __restrict__ scale, int8_t* digits, int64_t ld, float* row_scale,
+                     int64_t tokens, int64_t cols) {
+  constexpr int kPitch = kTokTile / 4 + 1;              // words
+  __shared__ uint32_t colmax[kColTile];
+  __shared__ uint32_t tile[kAct8Digits][kColTile][kPitch];
+  cg::cluster_group cluster = cg::this_cluster();
+  const int64_t n0 = int64_t(blockIdx.x) * kColTile;
+  const int cgrp = threadIdx.x & 7, tgrp = threadIdx.x >> 3;     // 8 columns, 4 tokens
+  const int64_t c = n0 + cgrp * 8;
+  const int64_t ntiles = (tokens + kTokTile - 1) / kTokTile;
+  const T* x = static_cast<const T*>(dy.p);
+  if (threadIdx.x < kColTile) colmax[threadIdx.x] = 0;
+  __syncthreads();
+
+  uint32_t m[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m[i] = 0;
+  for (int64_t tt = blockIdx.y; tt < ntiles; tt += kColCluster) {
+    Raw8<T> r[4];
+    float s[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int64_t t = tt * kTokTile + tgrp * 4 + j;
+      load8(x + t * dy.ld, c, t < tokens ? cols : 0, dy.vec, r[j]);
+      s[j] = t < tokens ? __ldg(scale + t) : 0.0f;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) m[i] = max(m[i], abs_bits(elt(r[j], i) * s[j]));
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {                         // over the warp's 4 token groups, then the CTA
+    m[i] = max(m[i], __shfl_xor_sync(0xffffffffu, m[i], 8));
+    m[i] = max(m[i], __shfl_xor_sync(0xffffffffu, m[i], 16));
+    if ((threadIdx.x & 24) == 0) atomicMax(&colmax[cgrp * 8 + i], m[i]);
+  }
+  cluster.sync();
+  uint32_t all = 0;
+  if (threadIdx.x < kColTile)
+    for (int k = 0; k < kColCluster; ++k) all = max(all, *cluster.map_shared_rank(&colmax[threadIdx.x], k));
+  cluster.sync();                                       // everyone has read before anyone overwrites or leaves
+  if (threadIdx.x < kColTile) {
+    colmax[threadIdx.x] = all;
+    if (blockIdx.y == 0 && n0 + threadIdx.x < cols) row_scale[n0 + threadIdx.x] = Fixed(all).scale;
+  }
+  __syncthreads();
+  float inv[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) inv[i] = Fixed(colmax[cgrp * 8 + i]).inv;
+
+  for (int64_t tt = blockIdx.y; tt < ntiles; tt += kColCluster) {
+    uint32_t q[8][4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int64_t t = tt * kTokTile + tgrp * 4 + j;
+      Raw8<T> r;
+      load8(x + t * dy.ld, c, t < tokens ? cols : 0, dy.vec, r);
+      const float s = t < tokens ? __ldg(scale + t) : 0.0f;
+      Fixed f(0u);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        f.inv = inv[i];
+        q[i][j] = f.digits(elt(r, i) * s);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int d = 0; d < kAct8Digits; ++d)
+        tile[d][cgrp * 8 + i][tgrp] = bytes4(q[i][0], q[i][1], q[i][2], q[i][3], kAct8Digits - 1 - d);
+    __syncthreads();
+    const int lane = threadIdx.x & 31;
+    const int64_t t = tt * kTokTile + lane * 4;
+    for (int w = threadIdx.x >> 5; w < kAct8Digits * kColTile; w += kThreads / 32) {
+      const int d = w / kColTile, n = w % kColTile;
+      if (n0 + n < cols && t < ld)                      // ld is a multiple of 16: a word is inside or outside
+        *reinterpret_cast<uint32_t*>(digits + (d * cols + n0 + n) * ld + t) = tile[d][n][lane];
+    }
+    __syncthreads();
+  }
+}
+
+// v in up to three bfloat16 parts: each the nearest to what is left.  The
+// first stays finite when v is (the remainder of an infinite one would be
+// infinite too).
+template <int PARTS>
+__device__ __forceinline__ void split(float v, float (&p)[3]) {
+  constexpr float kMax = 3.38953139e38f;                 // the largest finite bfloat16
+#pragma unroll
+  for (int k = 0; k < PARTS; ++k) {
+    p[k] = __bfloat162float(__float2bfloat16_rn(v));
+    if (k == 0 && PARTS > 1 && fabsf(p[0]) > kMax && fabsf(v) <= 3.402823466e38f) p[0] = copysignf(kMax, v);
+    v -= p[k];
+  }
+}
+template <int PARTS>
+__device__ __forceinline__ void store_parts(const float (&v)[8], __nv_bfloat16* o, int64_t plane, int64_t c,
+                                            int64_t cols) {
+  float p[PARTS][8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    float s[3];
+    split<PARTS>(v[i], s);
+#pragma unroll
+    for (int k = 0; k < PARTS; ++k) p[k][i] = s[k];
+  }
+#pragma unroll
+  for (int k = 0; k < PARTS; ++k) store8(o + k * plane, c, cols, true, p[k]);
+}
+
+template <int PARTS>
+__global__ void __launch_bounds__(kThreads) k_act8_expand(Ckpt k, __nv_bfloat16* o, int64_t ld, int64_t rows,
+                                                          int64_t cols, int group, int64_t groups) {
+  const Piece p;
+  if (p.row >= rows || p.c >= cols) return;
+  uint2 w;
+  load_codes8(k.codes + p.row * k.ldc, p.c, cols, w);
+  const float s = __ldg(k.scales + p.row * groups + (group ? p.c / group : 0));
+  float v[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = code_at(w, i) * s;
+  store_parts<PARTS>(v, o + p.row * ld, rows * ld, p.c, cols);
+}
+
+template <class T, int PARTS>
+__global__ void __launch_bounds__(kThreads) k_act8_split(Mat x, __nv_bfloat16* o, int64_t ld, int64_t rows,
+                                                         int64_t cols) {
+  const Piece p;
+  if (p.row >= rows || p.c >= cols) return;
+  Raw8<T> r;
+  load8(static_cast<const T*>(x.p) + p.row * x.ld, p.c, cols, x.vec, r);
+  float v[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = elt(r, i);
+  store_parts<PARTS>(v, o + p.row * ld, rows * ld, p.c, cols);
+}
+
+// ------------------------------------------------------------------ host
+
+enum GradPath { kDigits, kBf16, kParts };
+GradPath grad_path(int32_t dtype, int32_t result, int32_t group) {
+  if (dtype == ACT8_BF16 && result == ACT8_BF16) return kBf16;
+  return group == 0 ? kDigits : kParts;
+}
+
+size_t round_up(size_t n, size_t a) { return (n + a - 1) / a * a; }
+
+// Workspace of a gradient: dY (tokens x out) in the form its product takes,
+// then, but for digits, the codes' values (code_rows x inner) in bfloat16.
+struct GradPlan {
+  GradPath path;
+  int dy_parts, code_parts;
+  int64_t ld_dy, ld_code;        // elements
+  size_t scale_bytes, dy_bytes, code_bytes;
+  size_t total() const { return scale_bytes + dy_bytes + code_bytes; }
+};
+GradPlan grad_plan(bool weight, int32_t dtype, int32_t result, int32_t group, int64_t tokens, int64_t out,
+                   int64_t inner) {
+  GradPlan p{};
+  p.path = grad_path(dtype, result, group);
+  if (p.path == kDigits) {
+    const int64_t rows = weight ? out : tokens, k = weight ? tokens : out;
+    p.ld_dy = int64_t(round_up(size_t(k), 16));
+    p.scale_bytes = round_up(size_t(rows) * 4, 256);
+    p.dy_bytes = round_up(size_t(rows) * p.ld_dy * kAct8Digits, 256);
+    return p;
+  }
+  p.dy_parts = dtype == ACT8_BF16 ? 1 : (dtype == ACT8_FP16 ? 2 : 3);
+  p.code_parts = p.path == kBf16 ? 1 : 3;
+  p.ld_dy = int64_t(round_up(size_t(out), 8));
+  p.ld_code = int64_t(round_up(size_t(inner), 8));
+  // room for a copy of a bfloat16 dY whatever its alignment turns out to be
+  p.dy_bytes = round_up(size_t(tokens) * p.ld_dy * 2 * p.dy_parts, 256);
+  p.code_bytes = round_up(size_t(weight ? tokens : out) * p.ld_code * 2 * p.code_parts, 256);
+  return p;
+}
+
+shampoo4_status digit_pass(bool weight, const void* dy, int32_t dtype, int64_t lddy, const float* scale,
+                           int64_t tokens, int64_t out, int8_t* digits, int64_t ld, float* row_scale,
+                           cudaStream_t st) {
+  const Mat m = mat(dy, lddy, dtype);
+  const int64_t strips = (out + kColTile - 1) / kColTile;
+  return by_dtype(dtype, [&](auto* tag) -> shampoo4_status {
+    using T = std::remove_pointer_t<decltype(tag)>;
+    if (weight)
+      k_act8_digit_columns<T><<<dim3(unsigned(strips), kColCluster), kThreads, 0, st>>>(m, scale, digits, ld,
+                                                                                       row_scale, tokens, out);
+    else
+      k_act8_digit_rows<T><<<unsigned(tokens), kThreads, 0, st>>>(m, scale, digits, ld, row_scale, tokens, out);
+    S4_CUDA(cudaGetLastError());
+    return SHAMPOO4_OK;
+  });
+}
+
+shampoo4_status expand(const Ckpt& k, int64_t rows, int64_t cols, int32_t group, int parts, void* o, int64_t ld,
+                       cudaStream_t st) {
+  const dim3 b = piece_block(cols);
+  dim3 g;
+  if (!piece_grid(rows, cols, b, &g)) return SHAMPOO4_ERR_INVALID_ARG;
+  __nv_bfloat16* p = static_cast<__nv_bfloat16*>(o);
+  if (parts == 1) k_act8_expand<1><<<g, b, 0, st>>>(k, p, ld, rows, cols, group, group_count(cols, group));
+  else k_act8_expand<3><<<g, b, 0, st>>>(k, p, ld, rows, cols, group, group_count(cols, group));
+  S4_CUDA(cudaGetLastError());
+  return SHAMPOO4_OK;
+}
+
+shampoo4_status split_dy(const void* x, int32_t dtype, int64_t ldx, int64_t rows, int64_t cols, void* o, int64_t ld,
+                         cudaStream_t st) {
+  const dim3 b = piece_block(cols);
+  dim3 g;
+  if (!piece_grid(rows, cols, b, &g)) return SHAMPOO4_ERR_INVALID_ARG;
+  const Mat m = mat(x, ldx, dtype);
+  __nv_bfloat16* p = static_cast<__nv_bfloat16*>(o);
+  if (dtype == ACT8_BF16) k_act8_split<__nv_bfloat16, 1><<<g, b, 0, st>>>(m, p, ld, rows, cols);
+  else if (dtype == ACT8_FP16) k_act8_split<__half, 2><<<g, b, 0, st>>>(m, p, ld, rows, cols);
+  else k_act8_split<float, 3><<<g, b, 0, st>>>(m, p, ld, rows, cols);
+  S4_CUDA(cudaGetLastError());
+  return SHAMPOO4_OK;
+}
+
+// Both gradients: weight: Y[out, inner] = dY^T X; else Y[tokens, inner] = dY W.
+shampoo4_status grad(bool weight, const void* dy, int32_t dtype, int64_t lddy, const Ckpt& k, int32_t group,
+                     int64_t tokens, int64_t out, int64_t inner, Act8Out o, void* ws, size_t ws_bytes,
+                     uint32_t* flags, cudaStream_t st) {
+  const int64_t K = weight ? tokens : out, R = weight ? out : tokens;
+  if (K == 0 && o.accumulate) return SHAMPOO4_OK;
+  const GradPlan p = grad_plan(weight, dtype, o.dtype, group, tokens, out, inner);
+  if (K == 0) return launch_act8_bf16(Act8Operand{}, 1, Act8Operand{}, 1, 0, inner, R, 0, o, flags, st);
+  if (!ws || !aligned(ws, 256)) return SHAMPOO4_ERR_INVALID_ARG;
+  if (ws_bytes < p.total()) return SHAMPOO4_ERR_WORKSPACE;
+  char* w = static_cast<char*>(ws);
+  if (p.path == kDigits) {
+    float* row_scale = reinterpret_cast<float*>(w);
+    int8_t* digits = reinterpret_cast<int8_t*>(w + p.scale_bytes);
+    S4_TRY(digit_pass(weight, dy, dtype, lddy, k.scales, tokens, out, digits, p.ld_dy, row_scale, st));
+    o.row_scale = row_scale;
+    return launch_act8_digits(Act8Operand{k.codes, k.ldc, 0}, Act8Operand{digits, p.ld_dy, R}, inner, R, K, o, flags,
+                              st);
+  }
+  Act8Operand b{dy, lddy, 0};
+  if (dtype != ACT8_BF16 || !row_aligned(dy, lddy, dtype)) {
+    b = Act8Operand{w, p.ld_dy, tokens};
+    S4_TRY(split_dy(dy, dtype, lddy, tokens, out, w, p.ld_dy, st));
+  }
+  const Act8Operand a{w + p.dy_bytes, p.ld_code, K};
+  S4_TRY(expand(k, K, inner, group, p.code_parts, w + p.dy_bytes, p.ld_code, st));
+  return launch_act8_bf16(a, p.code_parts, b, p.dy_parts, weight ? 1 : 0, inner, R, K, o, flags, st);
+}
+
+}  // namespace
+}  // namespace s4
+
+// ------------------------------------------------------------------ C ABI
+
+using namespace s4;
+
+extern "C" shampoo4_status act8_grad_workspace(int32_t weight, int32_t dtype, int32_t result, int64_t tokens,
+                                               int64_t out, int64_t inner, int32_t group, size_t* bytes) {
+  if (!bytes || !dtype_ok(dtype) || !dtype_ok(result) || !group_ok(group) || !shape_ok(tokens, out) || !shape_ok(0, inner))
+    return SHAMPOO4_ERR_INVALID_ARG;
+  *bytes = tokens == 0 || out == 0 || inner == 0 ? 0 : grad_plan(weight != 0, dtype, result, group, tokens, out, inner).total();
+  return SHAMPOO4_OK;
+}
+
+static shampoo4_status grad_call(bool weight, const void* d_dy, int32_t dtype, int64_t lddy, const int8_t* codes,
+                                 int64_t ldc, const float* scales, int32_t group, int64_t tokens, int64_t out,
+                                 int64_t inner, void* d_y, int32_t result, int64_t ldy, int32_t accumulate,
+                                 void* d_ws, size_t ws_bytes, uint32_t* d_flags, shampoo4_stream_t stream) {
+  if (!shape_ok(tokens, out) || !shape_ok(0, inner) || !dtype_ok(dtype) || !dtype_ok(result) || !group_ok(group))
+    return SHAMPOO4_ERR_INVALID_ARG;
+  const int64_t M = weight ? out : tokens, K = weight ? tokens : out;
+  if (M == 0 || inner == 0) return SHAMPOO4_OK;
+  if (!mat_ok(d_y, result, M, inner, ldy) || !aligned(d_flags, 4)) return SHAMPOO4_ERR_INVALID_ARG;
+  if (K > 0 && (!mat_ok(d_dy, dtype, tokens, out, lddy) || !codes_ok(codes, ldc, inner, scales)))
+    return SHAMPOO4_ERR_INVALID_ARG;
+  const Act8Out o{d_y, ldy, result, accumulate ? 1 : 0, nullptr, nullptr, nullptr};
+  return grad(weight, d_dy, dtype, lddy, Ckpt{const_cast<int8_t*>(codes), ldc, const_cast<float*>(scales)}, group,
+              tokens, out, inner, o, d_ws, ws_bytes, d_flags, reinterpret_cast<cudaStream_t>(stream));
+}
+
+extern "C" shampoo4_status act8_weight_grad(const void* d_dy, int32_t dtype, int64_t lddy, const int8_t* d_xc,
+                                            int64_t ldxc, const float* d_xs, int32_t group, int64_t tokens,
+                                            int64_t out, int64_t inner, void* d_dw, int32_t result, int64_t lddw,
+                                            int32_t accumulate, void* d_workspace, size_t workspace_bytes,
+                                            uint32_t* d_flags, shampoo4_stream_t stream) {
+  return grad_call(true, d_dy, dtype, lddy, d_xc, ldxc, d_xs, group, tokens, out, inner, d_dw, result, lddw,
+                   accumulate, d_workspace, workspace_bytes, d_flags, stream);
+}
+
+extern "C" shampoo4_status act8_input_grad(const void* d_dy, int32_t dtype, int64_t lddy, const int8_t* d_wc,
+                                           int64_t ldwc, const float* d_ws, int64_t tokens, int64_t out,
+                                           int64_t inner, void* d_dx, int32_t result, int64_t lddx,
+                                           int32_t accumulate, void* d_workspace, size_t workspace_bytes,
+                                           uint32_t* d_flags, shampoo4_stream_t stream) {
+  return grad_call(false, d_dy, dtype, lddy, d_wc, ldwc, d_ws, 0, tokens, out, inner, d_dx, result, lddx, accumulate,
+                   d_workspace, workspace_bytes, d_flags, stream);
+}
+

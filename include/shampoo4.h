@@ -580,7 +580,7 @@ shampoo4_status act8_linear(const void* d_x, int32_t xdtype, int64_t ldx, const 
  * act8_weight_grad), scratch of the one call; SHAMPOO4_ERR_WORKSPACE when
  * smaller. */
 shampoo4_status act8_grad_workspace(int32_t weight, int32_t dtype, int32_t result, int64_t tokens, int64_t out,
-                                    int64_t inner, size_t* bytes);
+                                    int64_t inner, int32_t group, size_t* bytes);
 shampoo4_status act8_weight_grad(const void* d_dy, int32_t dtype, int64_t lddy, const int8_t* d_xc, int64_t ldxc,
                                  const float* d_xs, int32_t group, int64_t tokens, int64_t out, int64_t inner,
                                  void* d_dw, int32_t result, int64_t lddw, int32_t accumulate, void* d_workspace,

@@ -190,14 +190,15 @@ def test_grad_workspace_sizes():
     n = C.c_size_t()
 
     def size(weight, dt, res, t, o, i):
-        L.call("act8_grad_workspace", weight, dt, res, t, o, i, C.byref(n))
+        L.call("act8_grad_workspace", weight, dt, res, t, o, i, 128 if weight else 0, C.byref(n))
         return n.value
     assert size(1, L.ACT8_BF16, L.ACT8_BF16, 64, 64, 64) < size(1, L.ACT8_BF16, L.ACT8_FP32, 64, 64, 64) \
         < size(1, L.ACT8_FP32, L.ACT8_FP32, 64, 64, 64)
     assert size(1, 0, 0, 0, 64, 64) == 0
-    assert _call("act8_grad_workspace", 1, 7, 0, 1, 1, 1, C.byref(n)) == INVALID
-    assert _call("act8_grad_workspace", 1, 0, 0, -1, 1, 1, C.byref(n)) == INVALID
-    assert _call("act8_grad_workspace", 1, 0, 0, 1, 1, 1, None) == INVALID
+    assert _call("act8_grad_workspace", 1, 7, 0, 1, 1, 1, 0, C.byref(n)) == INVALID
+    assert _call("act8_grad_workspace", 1, 0, 0, 1, 1, 1, 5, C.byref(n)) == INVALID
+    assert _call("act8_grad_workspace", 1, 0, 0, -1, 1, 1, 0, C.byref(n)) == INVALID
+    assert _call("act8_grad_workspace", 1, 0, 0, 1, 1, 1, 0, None) == INVALID
 
 
 def _swiglu(g=OK16, ldg=64, u=OK16, ldu=64, dt=1, rows=4, cols=64, group=32, h=OK16, ldh=64, gc=OK16, ldgc=64,

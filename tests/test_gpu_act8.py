@@ -5,12 +5,18 @@ eps / 2 relative to the value: fp32 2^-24, fp16 2^-11, bf16 2^-8):
  - codec: codes, scales and unpacked values equal bit for bit;
  - integer product p: the sum is exact; conversion, two scalings and the bias
    addition round in fp32, the result once;
- - gradients: S = sum |dy| |x| bounds the sum of the products' magnitudes.  A
-   factor v taken as one bfloat16 is off by 2^-8 |v|; taken as two, hi + lo,
-   |lo| <= 2^-8 |v| and lo's own rounding is off by 2^-8 |lo| <= 2^-16 |v|;
-   the omitted lo * lo product is at most 2^-8 * 2^-8.  (fp16's 11 bits fit
-   hi + lo exactly.)  The tensor core adds 16 products at a time to an fp32
-   accumulator with truncation: at most 2^-22 of S per addition.
+ - gradients, with S = sum |dy| |x| the sum of the products' magnitudes:
+   bfloat16 dy and result: each value rounds to one bfloat16 (2^-8), and the
+   tensor core adds 16 products at a time to an fp32 accumulator with
+   truncation, at most 2^-22 of S per addition;
+   one scale per row: F = dy * scale rounds to fp32 (2^-24) and to fixed
+   point, off by half of max|F| / 8355711 (and by a rounding 2^-24 max|F| of
+   the factor and of the product) per code; the integer sums are exact, and
+   joining and scaling them takes 6 fp32 roundings (2^-24 each);
+   groups: value and dy are exact to 2^-24 each as bfloat16 parts, what the
+   omitted products add is below 3 * 2^-24, and of K / 16 additions per
+   product kind at most 16 are in one accumulator; its sum is then added in
+   fp32, once per 256 k.
 """
 import numpy as np
 import pytest
@@ -247,16 +253,24 @@ def test_linear_empty(tokens, out, inner):
 
 # --------------------------------------------------------------- gradients
 
-def grad_tolerance(dy, x, K, dtype, result, weight):
-    a, b = np.abs(dy), np.abs(x)
+def grad_tolerance(dy, codes, scales, group, dtype, result, weight):
+    a, b = np.abs(dy), np.abs(A.values64(codes, scales, group))
+    K = codes.shape[0]
     S = (a.T if weight else a) @ b
-    rel = 2.0 ** -8 if dtype == "bf16" and result == "bf16" else 2.0 ** -16 * (1 if dtype == "bf16" else 3)
-    products = 1 if dtype == "bf16" and result == "bf16" else (2 if dtype == "bf16" else 3)
-    return S * (1.01 * rel + products * (-(-K // 16) + 1) * 2.0 ** -22)
+    if dtype == "bf16" and result == "bf16":
+        return S * (1.01 * 2.0 ** -8 + (-(-K // 16) + 1) * 2.0 ** -22)
+    if group == 0:
+        s = scales.astype(np.float64)
+        F = a * (s if weight else s.T)
+        top = F.max(axis=0 if weight else 1, initial=0.0).reshape(-1, 1) if F.size else np.zeros((S.shape[0], 1))
+        count = np.abs(codes.astype(np.float64)).sum(axis=0, keepdims=True)
+        return top * count * (0.5 / 8355711 + 2 * 2.0 ** -24) + S * 7 * 2.0 ** -24
+    kinds = {"bf16": 3, "fp16": 5, "fp32": 6}[dtype]
+    return S * (5 * 2.0 ** -24 + kinds * 17 * 2.0 ** -22 + (K // 256 + 1) * 2.0 ** -24)
 
 
 SHAPES = [(1, 1, 1), (1, 64, 300), (2, 7, 17), (63, 130, 65), (64, 128, 256), (65, 256, 257), (200, 129, 520),
-          (513, 300, 96), (1100, 64, 128)]
+          (513, 300, 96), (1100, 64, 128), (30, 1500, 700), (3000, 140, 260)]
 TYPES = [("bf16", "bf16"), ("bf16", "fp32"), ("fp16", "fp16"), ("fp32", "fp32"), ("bf16", "fp16"), ("fp32", "bf16")]
 
 
@@ -271,7 +285,7 @@ def test_weight_grad(tokens, out, inner, dtype, result):
     dw = api.act8_weight_grad(dy, *x, group=group, dtype=DT[result], flags=flags)
     xv, d = A.values64(xc, xs, group), f64(dy)
     want = d.T @ xv
-    within(f64(dw), want, grad_tolerance(d, xv, tokens, dtype, result, True) + half_step(result) * np.abs(want)
+    within(f64(dw), want, grad_tolerance(d, xc, xs, group, dtype, result, True) + half_step(result) * np.abs(want)
            + TINY[result])
     assert int(flags.item()) == 0
 
@@ -285,7 +299,7 @@ def test_input_grad(tokens, out, inner, dtype, result):
     dx = api.act8_input_grad(dy, *w, dtype=DT[result])
     wv, d = A.values64(wc, ws), f64(dy)
     want = d @ wv
-    within(f64(dx), want, grad_tolerance(d, wv, out, dtype, result, False) + half_step(result) * np.abs(want)
+    within(f64(dx), want, grad_tolerance(d, wc, ws, 0, dtype, result, False) + half_step(result) * np.abs(want)
            + TINY[result])
 
 
@@ -297,7 +311,8 @@ def test_grads_strides_and_accumulation(pad, offset, dtype):
     x, xc, xs = stored(90, 133, 71, 64)
     w, wc, ws = stored(200, 133, 72)
     d = f64(dy)
-    for weight, vals in ((True, A.values64(xc, xs, 64)), (False, A.values64(wc, ws))):
+    for weight, codes, scales, group in ((True, xc, xs, 64), (False, wc, ws, 0)):
+        vals = A.values64(codes, scales, group)
         rows = 200 if weight else 90
         room = torch.full((rows, 150), 2.0, dtype=DT[dtype], device="cuda")
         out = room[:, 4:137]
@@ -308,7 +323,7 @@ def test_grads_strides_and_accumulation(pad, offset, dtype):
         else:
             api.act8_input_grad(dy, *w, out=out, accumulate=True)
         want = f64(start) + (d.T if weight else d) @ vals
-        tol = grad_tolerance(d, vals, 90 if weight else 200, dtype, dtype, weight)
+        tol = grad_tolerance(d, codes, scales, group, dtype, dtype, weight)
         within(f64(out), want, tol + (2.0 ** -23 + half_step(dtype)) * np.abs(want) + 2.0 ** -23 * np.abs(f64(start))
                + TINY[dtype])
         assert torch.all(room[:, :4] == 2) and torch.all(room[:, 137:] == 2)
@@ -461,9 +476,9 @@ def test_layer_matches_the_oracle():
     dg, du = A.swiglu_grad(d @ wd, *kept)
     wants = [hv @ wd.T, dg @ wg + du @ wu, dg.T @ xv, du.T @ xv, d.T @ hv]
     for g, want in zip(got, wants):
-        # the stages' bounds are relative to sums of magnitudes; with random signs and these lengths (at most
-        # 200) those are below 16 times the result's norm: 16 (3 2^-16 + 42 2^-22) twice over
-        assert np.linalg.norm(f64(g) - want) <= 16 * 2 * (3 * 2.0 ** -16 + 42 * 2.0 ** -22) * np.linalg.norm(want)
+        # a stage's bound: with random signs and these lengths (at most 200) the sums of magnitudes, and the rows'
+        # largest elements times the codes' counts, are below 16 and 256 times the result; twice over
+        assert np.linalg.norm(f64(g) - want) <= 2 * (16 * 7 * 2.0 ** -24 + 256 * 3 * 2.0 ** -24) * np.linalg.norm(want)
 
 
 def test_layer_gradients_feed_the_optimizer_step():
