@@ -395,14 +395,15 @@ def _act8_store(rows, cols, group, device):
     (code pointer, leading dimension, scale pointer)."""
     ld = (cols + 15) // 16 * 16
     codes = torch.empty_strided((rows, cols), (ld, 1), dtype=torch.int8, device=device)
-    scales = torch.empty((rows, _act8_groups(cols, group)), dtype=torch.float32, device=device)
+    groups = _act8_groups(cols, group)
+    scales = torch.empty_strided((rows, groups), (groups, 1), dtype=torch.float32, device=device)
     return codes, scales, (codes.data_ptr(), ld, scales.data_ptr())
 
 
 def _act8_out(out, rows, cols, dtype, device, name="out"):
     """The result tensor and its (pointer, dtype code, leading dimension)."""
     if out is None:
-        out = torch.empty((rows, cols), dtype=dtype, device=device)
+        out = torch.empty_strided((rows, cols), (cols, 1), dtype=dtype, device=device)
         return out, out.data_ptr(), _ACT8_DTYPES[dtype], cols if rows > 1 else (cols + 15) // 16 * 16
     p, code, _, _, ld = _act8_mat(out, name, (rows, cols), device)
     return out, p, code, ld
@@ -493,7 +494,7 @@ def act8_matmul(x_codes, x_scales, w_codes, w_scales, bias=None, dtype=torch.bfl
 
 
 def _act8_on(stream, make):
-    """make() under ``stream``, so that the caching allocator keeps the
+    """make(), under ``stream`` when one is given, so that the caching allocator keeps the
     scratch it allocates for the work enqueued there."""
     if stream is None:
         return make()
@@ -510,7 +511,14 @@ def act8_linear(x, w_codes, w_scales, bias=None, out=None, checkpoint=False, fla
     wp, ldw, ws = _act8_codes(w_codes, w_scales, 0, "w", dev)
     n = _act8_inner(inner, w_codes, "act8_linear")
     out, op, dt, ldo = _act8_out(out, tokens, n, x.dtype, dev)
-    codes, scales, (cp, ldc, sp) = _act8_on(stream, lambda: _act8_store(tokens, inner, 0, dev))
+    if checkpoint:
+        codes, scales, (cp, ldc, sp) = _act8_store(tokens, inner, 0, dev)
+    else:                          # scratch of this call: codes, then scales, in one buffer
+        ldc = (inner + 15) // 16 * 16
+        size = tokens * ldc + 4 * tokens
+        work = _act8_on(stream, lambda: torch.empty_strided((size,), (1,), dtype=torch.int8, device=dev))
+        cp = work.data_ptr()
+        sp = cp + tokens * ldc
     _act8_call(dev, stream, "act8_linear", xp, xdt, ldx, wp, ldw, ws, _act8_vec(bias, n, _BIAS_TYPES, "bias", dev),
                tokens, n, inner, cp, ldc, sp, op, dt, ldo, _act8_vec(flags, 1, _FLAG_TYPES, "flags", dev))
     return (out, codes, scales) if checkpoint else out
@@ -529,7 +537,7 @@ def _act8_grad(fn, dy, codes, scales, group, rows, dtype, out, accumulate, flags
     out, op, odt, ldo = _act8_out(out, rows, inner, dtype, dev)
     need = C.c_size_t()
     L.call("act8_grad_workspace", int(weight), ddt, odt, tokens, n, inner, group, need)
-    work = _act8_on(stream, lambda: torch.empty(need.value, dtype=torch.uint8, device=dev))
+    work = _act8_on(stream, lambda: torch.empty_strided((need.value,), (1,), dtype=torch.int8, device=dev))
     given = (dp, ddt, ldd, cp, ldc, sp) + ((group,) if weight else ())
     _act8_call(dev, stream, fn, *given, tokens, n, inner, op, odt, ldo, int(bool(accumulate)), work.data_ptr(),
                need.value, _act8_vec(flags, 1, _FLAG_TYPES, "flags", dev))

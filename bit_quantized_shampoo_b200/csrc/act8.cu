@@ -79,6 +79,7 @@ __global__ void __launch_bounds__(kThreads) k_act8_pack_groups(Mat x, Ckpt o, in
 template <class T, int IT>
 __global__ void __launch_bounds__(kThreads) k_act8_pack_rows(Mat x, Ckpt o, int64_t rows, int64_t cols) {
   __shared__ uint32_t slots[kThreads / 32];
+  let_next_start();
   for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
     const T* xr = static_cast<const T*>(x.p) + row * x.ld;
     int8_t* cr = o.codes + row * o.ldc;
@@ -286,6 +287,15 @@ static shampoo4_status check_product(int64_t tokens, int64_t out, int64_t inner)
   return SHAMPOO4_OK;
 }
 
+static shampoo4_status matmul(const int8_t* xc, int64_t ldxc, const float* xs, const int8_t* wc, int64_t ldwc,
+                              const float* ws, const float* bias, int64_t tokens, int64_t out, int64_t inner, void* y,
+                              int32_t dtype, int64_t ldy, bool after_pack, uint32_t* flags, cudaStream_t st) {
+  // no columns: no group, so no scale either
+  const Act8Out o{y, ldy, dtype, 0, inner > 0 ? xs : nullptr, inner > 0 ? ws : nullptr, bias};
+  return launch_act8_codes(Act8Operand{wc, ldwc, 0}, Act8Operand{xc, ldxc, 0}, out, tokens, inner, o, after_pack,
+                           flags, st);
+}
+
 extern "C" shampoo4_status act8_matmul(const int8_t* d_xc, int64_t ldxc, const float* d_xs, const int8_t* d_wc,
                                        int64_t ldwc, const float* d_ws, const float* d_bias, int64_t tokens,
                                        int64_t out, int64_t inner, void* d_y, int32_t dtype, int64_t ldy,
@@ -297,10 +307,8 @@ extern "C" shampoo4_status act8_matmul(const int8_t* d_xc, int64_t ldxc, const f
     return SHAMPOO4_ERR_INVALID_ARG;
   if (inner > 0 && (!codes_ok(d_xc, ldxc, inner, d_xs) || !codes_ok(d_wc, ldwc, inner, d_ws)))
     return SHAMPOO4_ERR_INVALID_ARG;
-  // no columns: no group, so no scale either
-  const Act8Out o{d_y, ldy, dtype, 0, inner > 0 ? d_xs : nullptr, inner > 0 ? d_ws : nullptr, d_bias};
-  return launch_act8_codes(Act8Operand{d_wc, ldwc, 0}, Act8Operand{d_xc, ldxc, 0}, out, tokens, inner, o, d_flags,
-                           reinterpret_cast<cudaStream_t>(stream));
+  return matmul(d_xc, ldxc, d_xs, d_wc, ldwc, d_ws, d_bias, tokens, out, inner, d_y, dtype, ldy, false, d_flags,
+                reinterpret_cast<cudaStream_t>(stream));
 }
 
 extern "C" shampoo4_status act8_linear(const void* d_x, int32_t xdtype, int64_t ldx, const int8_t* d_wc, int64_t ldwc,
@@ -316,8 +324,9 @@ extern "C" shampoo4_status act8_linear(const void* d_x, int32_t xdtype, int64_t 
                   (inner > 0 && !codes_ok(d_wc, ldwc, inner, d_ws))))
     return SHAMPOO4_ERR_INVALID_ARG;
   S4_TRY(act8_pack(d_x, xdtype, tokens, inner, ldx, 0, d_xc, ldxc, d_xs, stream));
-  return act8_matmul(d_xc, ldxc, d_xs, d_wc, ldwc, d_ws, d_bias, tokens, out, inner, d_y, ydtype, ldy, d_flags,
-                     stream);
+  if (out == 0) return SHAMPOO4_OK;
+  return matmul(d_xc, ldxc, d_xs, d_wc, ldwc, d_ws, d_bias, tokens, out, inner, d_y, ydtype, ldy, inner > 0, d_flags,
+                reinterpret_cast<cudaStream_t>(stream));
 }
 
 extern "C" shampoo4_status act8_swiglu(const void* d_gate, int64_t ldg, const void* d_up, int64_t ldu, int32_t dtype,

@@ -31,9 +31,12 @@ struct Act8Out {
 
 // All products: Y[r, m] = row_scale[r] col_scale[m] sum_k B[r, k] A[m, k] + bias[m].
 
-// int8 codes both: a is M x K, b is R x K (K contiguous).
+// int8 codes both: a is M x K, b is R x K (K contiguous).  after_pass: b was
+// written by the kernel enqueued just before on this stream, and a was not;
+// the launch may then overlap that kernel's end.  (The other two always
+// follow their own operand pass.)
 shampoo4_status launch_act8_codes(const Act8Operand& a, const Act8Operand& b, int64_t M, int64_t R, int64_t K,
-                                  const Act8Out& out, uint32_t* flags, cudaStream_t st);
+                                  const Act8Out& out, bool after_pass, uint32_t* flags, cudaStream_t st);
 // a: codes K x M (M contiguous); b: kAct8Digits planes of R x K digits, most
 // significant first: B = 65536 d0 + 256 d1 + d2.
 shampoo4_status launch_act8_digits(const Act8Operand& a, const Act8Operand& b, int64_t M, int64_t R, int64_t K,

@@ -107,6 +107,10 @@ __device__ __forceinline__ uint32_t cta_max(uint32_t m, uint32_t* slots) {
   return __reduce_max_sync(0xffffffffu, lane < int(blockDim.x >> 5) ? slots[lane] : 0u);
 }
 
+// The product enqueued next may be launched now (it waits for this kernel's
+// results itself).
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 struct Mat {
   const void* p;
   int64_t ld;

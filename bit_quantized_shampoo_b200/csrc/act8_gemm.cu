@@ -21,15 +21,18 @@
 // double-buffered in tensor memory: one tile's epilogue runs under the next
 // one's products.  The pairs are persistent, one CTA per SM.
 //
-// Warp roles (192 threads): warp 0 issues the TMA loads, warp 1 of the leader
-// the MMAs, warps 2..5 drain the accumulator.  Every wait is bounded (2 s);
+// Warp roles (320 threads): warp 0 issues the TMA loads, warp 1 of the leader
+// the MMAs, warps 2..9 drain the accumulator, two per lane quarter with half of
+// the rows each.  Every wait is bounded (2 s);
 // on expiry a role raises SHAMPOO4_FLAG_TIMEOUT and stops, and the pair waits
 // for what it issued before it frees tensor memory and leaves.
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <algorithm>
+#include <atomic>
 #include <climits>
+#include <cmath>
 #include "act8.h"
 #include "plan.h"
 #include "tcgen05.cuh"
@@ -39,6 +42,7 @@ namespace {
 
 enum { kI8 = 0, kBf16 = 1 };
 constexpr int kLanes = 128;               // columns m per CTA: the TMEM lanes
+constexpr int kPairThreads = 320, kSmallThreads = 192;
 constexpr int kRowBytes = 128;            // bytes of a swizzle atom row
 
 // KIND; A_MN/B_MN: the operand's row index (not k) is contiguous; R: rows of
@@ -64,7 +68,7 @@ struct Cfg {
   static_assert(!kSmallApart || 2 * kN <= kAccCols, "both sums fit");
   static constexpr int kTmemCols = 2 * kAccCols;
   static_assert(kSmem <= 227 * 1024, "stages fit in shared memory");
-  static_assert(kN <= 256 && kN % 32 == 0 && kBRows % 8 == 0 && kBTile % 1024 == 0, "tile shape");
+  static_assert(R % 64 == 0 && kN <= 256 && kN % 32 == 0 && kBRows % 8 == 0 && kBTile % 1024 == 0, "tile shape");
   static_assert(KIND == kBf16 || (PA == 1 && PB == 1 && !B_MN), "integer operands");
   static_assert(KIND == kI8 || (ND == 1 && A_MN), "bfloat16 operands");
 };
@@ -113,6 +117,11 @@ __device__ __forceinline__ uint32_t cta_rank() {
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
+// The kernel before this one on the stream may still run (a programmatic
+// launch): from here on its results are visible.  Weight codes are older
+// than that kernel, so they are fetched before the wait.
+__device__ __forceinline__ void wait_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // Tile load whose bytes count on a barrier of either CTA of the pair.
 template <int CG>
 __device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap* map, int x, int y, int plane, uint32_t bar) {
@@ -242,7 +251,7 @@ __device__ __forceinline__ float row_scale(const Act8Out& o, int R, int r) {
 }
 
 template <class C>
-__global__ void __launch_bounds__(192, 1) k_act8_gemm(const __grid_constant__ GemmArgs g) {
+__global__ void __launch_bounds__(kPairThreads, 1) k_act8_gemm(const __grid_constant__ GemmArgs g) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ uint64_t full_bar[C::STAGES], empty_bar[C::STAGES], acc_full[2], acc_empty[2], done_bar;
@@ -257,7 +266,7 @@ __global__ void __launch_bounds__(192, 1) k_act8_gemm(const __grid_constant__ Ge
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&acc_full[s], 1);
-      mbar_init(&acc_empty[s], 4 * C::CG);
+      mbar_init(&acc_empty[s], 8 * C::CG);
     }
     mbar_init(&done_bar, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -286,6 +295,7 @@ __global__ void __launch_bounds__(192, 1) k_act8_gemm(const __grid_constant__ Ge
     if (lane == 0) {                                        // ---- loads
       int it = 0;
       bool ok = true;
+      wait_previous();
       for (int t = first; ok && t < tiles; t += step) {
         int tm, tr;
         tile_of(g, t, tm, tr);
@@ -359,17 +369,22 @@ __global__ void __launch_bounds__(192, 1) k_act8_gemm(const __grid_constant__ Ge
       if (!mbar_wait(&done_bar, 0)) ok = false;
       if (!ok && g.flags) atomicOr(g.flags, SHAMPOO4_FLAG_TIMEOUT);
     }
-  } else {                                                  // ---- epilogue, warps 2..5
+  } else {                                                  // ---- epilogue, warps 2..9
     const int q = warp & 3;                                 // TMEM lane quarter
-    constexpr int kChunks = C::R / 32;
+    constexpr int kChunks = C::R / 64;                      // of this warp: half of the tile's
+    const int c0 = (warp - 2) / 4 * kChunks;
     int i = 0;
     bool ok = true;
+    wait_previous();
     for (int t = first; ok && t < tiles; t += step) {
       int tm, tr;
       tile_of(g, t, tm, tr);
-      const int m = (tm * C::CG + int(rank)) * kLanes + 32 * q + lane, r0 = tr * C::R;
+      const int m = (tm * C::CG + int(rank)) * kLanes + 32 * q + lane, r0 = tr * C::R + 32 * c0;
       const float cs = g.out.col_scale && m < g.M ? __ldg(g.out.col_scale + m) : 1.0f;
       const float bias = g.out.bias && m < g.M ? __ldg(g.out.bias + m) : 0.0f;
+      float rs[kChunks];                                    // fetched under the products
+#pragma unroll
+      for (int c = 0; c < kChunks; ++c) rs[c] = row_scale(g.out, g.R, r0 + 32 * c + lane);
       const int passes = max(1, (kblocks + chunk - 1) / chunk);
       float sum[C::CHUNK ? kChunks : 1][32];
       for (int pass = 0; pass < passes; ++pass, ++i) {
@@ -385,7 +400,7 @@ __global__ void __launch_bounds__(192, 1) k_act8_gemm(const __grid_constant__ Ge
 #pragma unroll
           for (int c = 0; c < kChunks; ++c) {
             float v[32];
-            if (kblocks > 0) load_chunk<C>(tacc, c, v);
+            if (kblocks > 0) load_chunk<C>(tacc, c0 + c, v);
 #pragma unroll
             for (int j = 0; j < 32; ++j) {
               const float x = kblocks > 0 ? v[j] : 0.0f;
@@ -393,23 +408,26 @@ __global__ void __launch_bounds__(192, 1) k_act8_gemm(const __grid_constant__ Ge
             }
           }
         } else {
-#pragma unroll 1
-          for (int c = 0; c < kChunks && r0 + 32 * c < g.R; ++c) {
+#pragma unroll
+          for (int c = 0; c < kChunks; ++c) {
+            if (r0 + 32 * c >= g.R) break;
             float v[32];
             if (kblocks > 0) {
-              load_chunk<C>(tacc, c, v);
+              load_chunk<C>(tacc, c0 + c, v);
             } else {
 #pragma unroll
               for (int j = 0; j < 32; ++j) v[j] = 0.0f;
             }
-            store_any(g.out, g.R, g.M, r0 + 32 * c, m, cs, bias, row_scale(g.out, g.R, r0 + 32 * c + lane), v);
+            store_any(g.out, g.R, g.M, r0 + 32 * c, m, cs, bias, rs[c], v);
           }
         }
         fence_before_sync();
         __syncwarp();
         if (lane == 0) {
           if (C::CG == 2)
-            asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(
+            // relaxed: the accumulator is in registers (its loads are complete), and a release would
+            // wait for the results' stores (54 against 41 us for a 4096 x 4096 weight gradient of 64 tokens)
+            asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(
                 in_cta(smem_u32(&acc_empty[ab]), 0)) : "memory");
           else
             mbar_arrive(&acc_empty[ab]);
@@ -419,7 +437,7 @@ __global__ void __launch_bounds__(192, 1) k_act8_gemm(const __grid_constant__ Ge
 #pragma unroll
         for (int c = 0; c < kChunks; ++c)
           if (r0 + 32 * c < g.R)
-            store_any(g.out, g.R, g.M, r0 + 32 * c, m, cs, bias, row_scale(g.out, g.R, r0 + 32 * c + lane), sum[c]);
+            store_any(g.out, g.R, g.M, r0 + 32 * c, m, cs, bias, rs[c], sum[c]);
       }
     }
   }
@@ -433,6 +451,217 @@ __global__ void __launch_bounds__(192, 1) k_act8_gemm(const __grid_constant__ Ge
       asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::kTmemCols) : "memory");
     else
       asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::kTmemCols) : "memory");
+  }
+}
+
+// Columns m .. m + 3 of row r to Y.
+template <class T>
+__device__ __forceinline__ void store_row4(const Act8Out& o, int r, int m, int M, float (&v)[4]) {
+  T* p = static_cast<T*>(o.y) + int64_t(r) * o.ld + m;
+  struct alignas(4 * sizeof(T)) V4 { T e[4]; };
+  if (!o.accumulate && m + 4 <= M && reinterpret_cast<uintptr_t>(p) % (4 * sizeof(T)) == 0) {
+    V4 w;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) put(&w.e[e], v[e]);
+    *reinterpret_cast<V4*>(p) = w;
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (m + e < M) put(p + e, o.accumulate ? v[e] + to_f32(p[e]) : v[e]);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Small products (few rows, or too few tiles for the pairs): one CTA per 128
+// columns by R rows and per share of the contraction, a cluster of up to 8
+// CTAs per tile.  Bound by reading A once (few rows) or by latency, so the
+// shares fill the SMs, two CTAs each; their integer partial sums meet in
+// shared memory, each CTA of the cluster finishing R / cluster rows (exact,
+// so the split changes no result).  Same roles as above, warps 2..5 finish.
+template <bool A_MN_, int R_, int ND_, int STAGES_>
+struct SmallCfg {
+  static constexpr int KIND = kI8, R = R_, ND = ND_, CG = 1, STAGES = STAGES_;
+  static constexpr bool A_MN = A_MN_, B_MN = false;
+  static constexpr int kK = 128, kN = ND * R, kBRows = R;
+  static constexpr int kATile = kLanes * kRowBytes;
+  static constexpr int kBTile = kN * kRowBytes;
+  static constexpr int kStage = kATile + kBTile;
+  static constexpr int kCols = (kN + 31) / 32 * 32;            // columns drained
+  static constexpr int kTmemCols = kCols <= 32 ? 32 : (kCols <= 64 ? 64 : (kCols <= 128 ? 128 : 256));
+  static constexpr int kSmem = STAGES * kStage + 1024;
+  static_assert(kN % 16 == 0 && kN <= 256 && kBTile % 1024 == 0, "tile shape");
+  static_assert(kCols * kLanes * 4 <= STAGES * kStage, "the partial sums reuse the stages");
+  static_assert(2 * (kSmem + 1024 + 256) <= 228 * 1024, "two CTAs per SM");
+};
+
+template <class C>
+__global__ void __launch_bounds__(kSmallThreads, 2) k_act8_small(const __grid_constant__ GemmArgs g) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  __shared__ uint64_t full_bar[C::STAGES], empty_bar[C::STAGES], done_bar;
+  __shared__ uint32_t tmem_slot;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int shares = gridDim.y, share = blockIdx.y;           // the cluster lies along y
+  const int kb0 = int(int64_t(g.kblocks) * share / shares), kb1 = int(int64_t(g.kblocks) * (share + 1) / shares);
+  const int m0 = int(blockIdx.x % unsigned(g.tiles_m)) * kLanes, r0 = int(blockIdx.x / unsigned(g.tiles_m)) * C::R;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::STAGES; ++s) {
+      mbar_init(&full_bar[s], 1);
+      mbar_init(&empty_bar[s], 1);
+    }
+    mbar_init(&done_bar, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_slot)),
+                 "r"(C::kTmemCols) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  fence_before_sync();
+  __syncthreads();
+  fence_after_sync();
+  const uint32_t tmem = tmem_slot;
+
+  if (warp == 0) {
+    if (lane == 0) {                                        // ---- loads
+      bool ok = true;
+      int it = 0;
+      auto load_a = [&](int s) {
+        mbar_expect_tx(&full_bar[s], C::kStage);
+        load_tile<C, C::A_MN, kLanes>(&g.a, m0, (kb0 + it) * C::kK, 0, smem_u32(smem + s * C::kStage),
+                                      smem_u32(&full_bar[s]));
+      };
+      auto load_b = [&](int s) {
+#pragma unroll
+        for (int d = 0; d < C::ND; ++d)
+          load_tile<C, false, C::R>(&g.b, r0, (kb0 + it) * C::kK, d,
+                                    smem_u32(smem + s * C::kStage) + C::kATile + d * C::R * kRowBytes,
+                                    smem_u32(&full_bar[s]));
+      };
+      const int n = kb1 - kb0, lead = min(n, C::STAGES);
+      for (it = 0; it < lead; ++it) load_a(it);
+      wait_previous();
+      for (it = 0; it < lead; ++it) load_b(it);
+      for (; it < n; ++it) {
+        const int s = it % C::STAGES;
+        if (!mbar_wait(&empty_bar[s], ((it / C::STAGES) & 1) ^ 1)) { ok = false; break; }
+        load_a(s);
+        load_b(s);
+      }
+      for (int i = max(0, it - C::STAGES); i < it; ++i)     // everything loaded has landed before the CTA leaves
+        if (!mbar_wait(&full_bar[i % C::STAGES], (i / C::STAGES) & 1)) ok = false;
+      if (!ok && g.flags) atomicOr(g.flags, SHAMPOO4_FLAG_TIMEOUT);
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {                                        // ---- products
+      constexpr uint32_t id = (2u << 4) | (1u << 7) | (1u << 10) | (uint32_t(C::A_MN) << 15) |
+                              (uint32_t(C::kN >> 3) << 17) | (uint32_t(kLanes >> 4) << 24);
+      bool ok = true;
+      for (int it = 0; it < kb1 - kb0; ++it) {
+        const int s = it % C::STAGES;
+        if (!mbar_wait(&full_bar[s], (it / C::STAGES) & 1)) { ok = false; break; }
+        fence_after_sync();
+        const uint32_t a0 = smem_u32(smem + s * C::kStage), b0 = a0 + C::kATile;
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+          mma<kI8, 1>(tmem, tile_desc<C, C::A_MN>(a0, kk), tile_desc<C, false>(b0, kk), id, (it | kk) != 0);
+        mma_commit(&empty_bar[s]);
+      }
+      mma_commit(&done_bar);
+      if (!mbar_wait(&done_bar, 0)) ok = false;
+      if (!ok && g.flags) atomicOr(g.flags, SHAMPOO4_FLAG_TIMEOUT);
+    }
+  }
+  // Every load has landed and every MMA is done (or timed out).
+  __syncthreads();
+  const int q = warp & 3;
+  const bool any = kb1 > kb0;
+  if (warp >= 2) {
+    wait_previous();
+    fence_after_sync();
+  }
+  if (shares == 1) {                                        // straight from tensor memory
+    if (warp >= 2) {
+      const int m = m0 + 32 * q + lane;
+      const float cs = g.out.col_scale && m < g.M ? __ldg(g.out.col_scale + m) : 1.0f;
+      const float bias = g.out.bias && m < g.M ? __ldg(g.out.bias + m) : 0.0f;
+#pragma unroll 1
+      for (int c = 0; c < C::R && r0 + c < g.R; c += 32) {
+        float v[32];
+        const uint32_t at = tmem + uint32_t(c) + (uint32_t(32 * q) << 16);
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] = 0.0f;
+        if (any) {
+#pragma unroll
+          for (int d = 0; d < C::ND; ++d) {
+            uint32_t r[32];
+            tmem_ld32(at + uint32_t(d * C::R), r);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = fmaf(v[j], 256.0f, __int2float_rn(int(r[j])));
+          }
+        }
+        store_any(g.out, min(g.R, r0 + C::R), g.M, r0 + c, m, cs, bias, row_scale(g.out, g.R, r0 + c + lane), v);
+      }
+      fence_before_sync();
+    }
+  } else {
+    // the stages become the partial sums, columns of 128 integers; a warp then
+    // finishes a row at a time, four columns per lane
+    int32_t* part = reinterpret_cast<int32_t*>(smem);
+    if (warp >= 2) {
+#pragma unroll 1
+      for (int c = 0; c < C::kCols; c += 32) {
+        uint32_t r[32];
+        tmem_ld32(tmem + uint32_t(c) + (uint32_t(32 * q) << 16), r);
+#pragma unroll
+        for (int j = 0; j < 32; ++j) part[(c + j) * kLanes + 32 * q + lane] = any ? int32_t(r[j]) : 0;
+      }
+      fence_before_sync();
+    }
+    __syncthreads();
+    cluster_sync();
+    if (warp >= 2) {
+      const int per = C::R / shares, j_end = min((share + 1) * per, g.R - r0);
+      const uint32_t base = smem_u32(part) + uint32_t(lane) * 16u;
+      const int m = m0 + 4 * lane;
+#pragma unroll 4
+      for (int j = share * per + q; j < j_end; j += 4) {
+        float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int d = 0; d < C::ND; ++d) {
+          int sum[4] = {0, 0, 0, 0};
+          const uint32_t at = base + uint32_t((d * C::R + j) * kLanes) * 4u;
+#pragma unroll 4
+          for (int k = 0; k < shares; ++k) {
+            int x[4];
+            asm volatile("ld.shared::cluster.v4.s32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]) : "r"(in_cta(at, uint32_t(k))) : "memory");
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sum[e] += x[e];
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[e] = fmaf(v[e], 256.0f, __int2float_rn(sum[e]));
+        }
+        const float rs = g.out.row_scale ? __ldg(g.out.row_scale + r0 + j) : 1.0f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float cs = g.out.col_scale && m + e < g.M ? __ldg(g.out.col_scale + m + e) : 1.0f;
+          const float bias = g.out.bias && m + e < g.M ? __ldg(g.out.bias + m + e) : 0.0f;
+          v[e] = fmaf(v[e] * rs, cs, bias);
+        }
+        if (g.out.dtype == ACT8_FP32) store_row4<float>(g.out, r0 + j, m, g.M, v);
+        else if (g.out.dtype == ACT8_BF16) store_row4<__nv_bfloat16>(g.out, r0 + j, m, g.M, v);
+        else store_row4<__half>(g.out, r0 + j, m, g.M, v);
+      }
+    }
+  }
+  if (shares > 1) cluster_sync();                           // nobody leaves while its sums are read
+  else __syncthreads();
+  __syncwarp();
+  if (warp == 1) {
+    fence_after_sync();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::kTmemCols) : "memory");
   }
 }
 
@@ -469,43 +698,121 @@ shampoo4_status encode(CUtensorMap* out, int kind, const Act8Operand& x, int64_t
   return r == CUDA_SUCCESS ? SHAMPOO4_OK : SHAMPOO4_ERR_CUDA;
 }
 
+// Per-device facts, looked up once.
+constexpr int kMaxDevices = 64;
+shampoo4_status device_sms(int* dev, int* sms) {
+  static std::atomic<int> known[kMaxDevices];
+  S4_CUDA(cudaGetDevice(dev));
+  if (*dev < 0 || *dev >= kMaxDevices) return SHAMPOO4_ERR_UNSUPPORTED;
+  *sms = known[*dev].load(std::memory_order_relaxed);
+  if (*sms == 0) {
+    S4_CUDA(cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, *dev));
+    known[*dev].store(*sms, std::memory_order_relaxed);
+  }
+  return SHAMPOO4_OK;
+}
 template <class C>
-shampoo4_status launch(const Act8Operand& a, const Act8Operand& b, int64_t M, int64_t R, int64_t K,
-                       const Act8Out& out, uint32_t* flags, cudaStream_t st) {
-  GemmArgs g{};
+shampoo4_status allow_smem(const void* kern, int dev) {
+  static std::atomic<bool> done[kMaxDevices];
+  if (!done[dev].load(std::memory_order_acquire)) {
+    S4_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem));
+    done[dev].store(true, std::memory_order_release);
+  }
+  return SHAMPOO4_OK;
+}
+
+template <class C>
+shampoo4_status fill_args(GemmArgs& g, const Act8Operand& a, int a_planes, const Act8Operand& b, int b_planes,
+                          int64_t M, int64_t R, int64_t K, const Act8Out& out, uint32_t* flags) {
   g.out = out;
   g.flags = flags;
   g.M = int32_t(M);
   g.R = int32_t(R);
   g.kblocks = int32_t((K + C::kK - 1) / C::kK);
   if (K > 0) {
-    S4_TRY(C::A_MN ? encode(&g.a, C::KIND, a, K, M, C::PA, C::kK) : encode(&g.a, C::KIND, a, M, K, C::PA, kLanes));
-    S4_TRY(C::B_MN ? encode(&g.b, C::KIND, b, K, R, C::PB * C::ND, C::kK)
-                   : encode(&g.b, C::KIND, b, R, K, C::PB * C::ND, C::kBRows));
+    S4_TRY(C::A_MN ? encode(&g.a, C::KIND, a, K, M, a_planes, C::kK) : encode(&g.a, C::KIND, a, M, K, a_planes, kLanes));
+    S4_TRY(C::B_MN ? encode(&g.b, C::KIND, b, K, R, b_planes, C::kK)
+                   : encode(&g.b, C::KIND, b, R, K, b_planes, C::kBRows));
   }
   const int64_t tm = (M + C::CG * kLanes - 1) / (C::CG * kLanes), tr = (R + C::R - 1) / C::R;
   if (tm * tr > INT_MAX / 16) return SHAMPOO4_ERR_INVALID_ARG;
   g.tiles_m = int32_t(tm);
   g.tiles_r = int32_t(tr);
-  auto kern = k_act8_gemm<C>;
-  int dev = 0, sms = 0;
-  S4_CUDA(cudaGetDevice(&dev));
-  S4_CUDA(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
-  S4_CUDA(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem));
+  return SHAMPOO4_OK;
+}
+
+// after_pass: the kernel enqueued just before on this stream is this call's
+// own operand pass, so the launch may overlap its end.
+template <class K>
+shampoo4_status start(K kern, int threads, dim3 grid, dim3 cluster, int smem, bool after_pass, const GemmArgs& g, cudaStream_t st) {
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(unsigned(C::CG * std::min<int64_t>(tm * tr, sms / C::CG)));
-  cfg.blockDim = dim3(192);
-  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(unsigned(threads));
+  cfg.dynamicSmemBytes = size_t(smem);
   cfg.stream = st;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = C::CG;
-  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.x = cluster.x;
+  attr[0].val.clusterDim.y = cluster.y;
   attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = after_pass ? 2 : 1;
   S4_CUDA(cudaLaunchKernelEx(&cfg, kern, g));
   return SHAMPOO4_OK;
+}
+
+template <class C>
+shampoo4_status launch(const Act8Operand& a, const Act8Operand& b, int64_t M, int64_t R, int64_t K,
+                       const Act8Out& out, bool after_pass, uint32_t* flags, cudaStream_t st) {
+  GemmArgs g{};
+  S4_TRY(fill_args<C>(g, a, C::PA, b, C::PB * C::ND, M, R, K, out, flags));
+  int dev = 0, sms = 0;
+  S4_TRY(device_sms(&dev, &sms));
+  auto kern = k_act8_gemm<C>;
+  S4_TRY(allow_smem<C>(reinterpret_cast<const void*>(kern), dev));
+  const int tiles = g.tiles_m * g.tiles_r;
+  return start(kern, kPairThreads, dim3(unsigned(C::CG * std::min(tiles, sms / C::CG))), dim3(C::CG), C::kSmem, after_pass, g, st);
+}
+
+template <class C>
+shampoo4_status launch_small(const Act8Operand& a, const Act8Operand& b, int64_t M, int64_t R, int64_t K, int shares,
+                             const Act8Out& out, bool after_pass, uint32_t* flags, cudaStream_t st) {
+  GemmArgs g{};
+  S4_TRY(fill_args<C>(g, a, 1, b, C::ND, M, R, K, out, flags));
+  int dev = 0, sms = 0;
+  S4_TRY(device_sms(&dev, &sms));
+  auto kern = k_act8_small<C>;
+  S4_TRY(allow_smem<C>(reinterpret_cast<const void*>(kern), dev));
+  return start(kern, kSmallThreads, dim3(unsigned(g.tiles_m * g.tiles_r), unsigned(shares)), dim3(1, unsigned(shares)), C::kSmem,
+               after_pass, g, st);
+}
+
+// Which form an integer product takes: the estimated time (us) of each,
+// fitted to measurements on a B200 (1 to 1024 rows, 768 to 11008 columns,
+// 6 to 86 k-blocks; within 15% of most).  The pairs cost 7.5 and, per wave of
+// tiles, 0.36 per k-block or the results' stores; a small tile 4.5 (and 0.01
+// per row) and 0.29 per k-block, up to 1.4 times that when two CTAs share an
+// SM; joining a split contraction 1.5 and 0.09 per row and digit a CTA
+// finishes; each further wave starts anew.
+struct Form { int rows, shares; };                          // rows 0: the pairs
+Form choose_form(int64_t M, int64_t R, int64_t K, int pair_rows, int digits, const int* tile_rows, int n) {
+  const double kb = double((K + 127) / 128);
+  const double pair_tiles = double((M + 255) / 256) * double((R + pair_rows - 1) / pair_rows);
+  double best = 7.5 + std::max(0.36 * kb, 1.6) * std::ceil(pair_tiles / 74);
+  Form f{0, 1};
+  for (int i = 0; i < n; ++i)
+    for (int s = 1; s <= 8 && s <= std::max(kb, 1.0); s *= 2) {
+      const int rows = tile_rows[i];
+      const double ctas = double((M + 127) / 128) * double((R + rows - 1) / rows) * s;
+      const double waves = std::ceil(ctas / 296), share = ctas <= 148 ? 1.0 : (rows * digits <= 64 ? 1.1 : 1.4);
+      const double cost = 1.5 + waves * (3.0 + 0.01 * rows * digits +
+                                         share * (0.29 * std::ceil(kb / s) +
+                                                  (s > 1 ? 1.5 + 0.09 * digits * rows / s : 0.0)));
+      if (cost < best) best = cost, f = Form{rows, s};
+    }
+  return f;
 }
 
 }  // namespace
@@ -518,25 +825,38 @@ template <bool B_MN, int PA, int PB, int STAGES>
 using PartsCfg = Cfg<            kBf16, true,  B_MN,  128, PA, PB, 1, 2, STAGES, 4>;
 
 shampoo4_status launch_act8_codes(const Act8Operand& a, const Act8Operand& b, int64_t M, int64_t R, int64_t K,
-                                  const Act8Out& out, uint32_t* flags, cudaStream_t st) {
-  return launch<CodesCfg>(a, b, M, R, K, out, flags, st);
+                                  const Act8Out& out, bool after_pass, uint32_t* flags, cudaStream_t st) {
+  const int rows[] = {16, 64, 128};
+  const Form f = choose_form(M, R, K, CodesCfg::R, 1, rows, 3);
+  if (f.rows == 16) return launch_small<SmallCfg<false, 16, 1, 5>>(a, b, M, R, K, f.shares, out, after_pass, flags, st);
+  if (f.rows == 64) return launch_small<SmallCfg<false, 64, 1, 4>>(a, b, M, R, K, f.shares, out, after_pass, flags, st);
+  if (f.rows == 128)
+    return launch_small<SmallCfg<false, 128, 1, 3>>(a, b, M, R, K, f.shares, out, after_pass, flags, st);
+  return launch<CodesCfg>(a, b, M, R, K, out, after_pass, flags, st);
 }
 
 shampoo4_status launch_act8_digits(const Act8Operand& a, const Act8Operand& b, int64_t M, int64_t R, int64_t K,
                                    const Act8Out& out, uint32_t* flags, cudaStream_t st) {
-  return launch<DigitsCfg>(a, b, M, R, K, out, flags, st);
+  const int rows[] = {16, 32};
+  // the small form keeps its integer sums whole
+  const Form f = K <= kAct8MaxInner ? choose_form(M, R, K, DigitsCfg::R, kAct8Digits, rows, 2) : Form{0, 1};
+  if (f.rows == 16)
+    return launch_small<SmallCfg<true, 16, kAct8Digits, 4>>(a, b, M, R, K, f.shares, out, true, flags, st);
+  if (f.rows == 32)
+    return launch_small<SmallCfg<true, 32, kAct8Digits, 3>>(a, b, M, R, K, f.shares, out, true, flags, st);
+  return launch<DigitsCfg>(a, b, M, R, K, out, true, flags, st);
 }
 
 shampoo4_status launch_act8_bf16(const Act8Operand& a, int a_parts, const Act8Operand& b, int b_parts, int b_mn,
                                  int64_t M, int64_t R, int64_t K, const Act8Out& out, uint32_t* flags,
                                  cudaStream_t st) {
   if (a_parts == 1 && b_parts == 1)
-    return b_mn ? launch<Bf16Cfg<true>>(a, b, M, R, K, out, flags, st)
-                : launch<Bf16Cfg<false>>(a, b, M, R, K, out, flags, st);
+    return b_mn ? launch<Bf16Cfg<true>>(a, b, M, R, K, out, true, flags, st)
+                : launch<Bf16Cfg<false>>(a, b, M, R, K, out, true, flags, st);
   if (!b_mn || a_parts != 3) return SHAMPOO4_ERR_INVALID_ARG;    // only the weight gradient splits, its codes always in 3
-  if (b_parts == 1) return launch<PartsCfg<true, 3, 1, 3>>(a, b, M, R, K, out, flags, st);
-  if (b_parts == 2) return launch<PartsCfg<true, 3, 2, 3>>(a, b, M, R, K, out, flags, st);
-  return launch<PartsCfg<true, 3, 3, 3>>(a, b, M, R, K, out, flags, st);
+  if (b_parts == 1) return launch<PartsCfg<true, 3, 1, 3>>(a, b, M, R, K, out, true, flags, st);
+  if (b_parts == 2) return launch<PartsCfg<true, 3, 2, 3>>(a, b, M, R, K, out, true, flags, st);
+  return launch<PartsCfg<true, 3, 3, 3>>(a, b, M, R, K, out, true, flags, st);
 }
 
 }  // namespace s4

@@ -14,7 +14,7 @@
 //          rounding (half of max|F| / 2^23 per element) and a few fp32
 //          roundings at the end.  1.5 times a bfloat16 product's tensor-core
 //          time, against three times for operands split into bfloat16 parts.
-//  bf16    dY and the result bfloat16: the codes' values rounded to one
+//  bf16    dY and the result bfloat16, and enough rows: the codes' values rounded to one
 //          bfloat16 (2^-8 at most, no more than the result's own rounding),
 //          dY as it is.  One bfloat16 product.
 //  parts   Scales per group of columns (no common factor per row): values and
@@ -62,6 +62,7 @@ template <class T>
 __global__ void __launch_bounds__(kThreads)
 k_act8_digit_rows(Mat dy, const float* __restrict__ scale, int8_t* digits, int64_t ld, float* row_scale, int64_t rows,
                   int64_t cols) {
+  let_next_start();
   __shared__ uint32_t slots[kThreads / 32];
   const int64_t row = blockIdx.x;
   const T* x = static_cast<const T*>(dy.p) + row * dy.ld;
@@ -89,17 +90,18 @@ k_act8_digit_rows(Mat dy, const float* __restrict__ scale, int8_t* digits, int64
   }
 }
 
-// Columns of dY as rows of digits (act8_weight_grad): a cluster of 8 CTAs per
-// 64 columns, tiles of 128 tokens dealt round robin.  The first sweep finds
+// Columns of dY as rows of digits (act8_weight_grad): a cluster of up to 8
+// CTAs (gridDim.y) per 64 columns, tiles of 128 tokens dealt round robin.  The first sweep finds
 // the columns' largest magnitudes (joined over distributed shared memory),
 // the second quantizes and transposes through shared memory, so that every
 // digit row is written in pieces of 128 bytes.  A thread holds 4 tokens by 8
 // columns of a tile.
 constexpr int kColTile = 64, kTokTile = 128, kColCluster = 8;
 template <class T>
-__global__ void __launch_bounds__(kThreads) __cluster_dims__(1, kColCluster, 1)
+__global__ void __launch_bounds__(kThreads)
 k_act8_digit_columns(Mat dy, const float* __restrict__ scale, int8_t* digits, int64_t ld, float* row_scale,
                      int64_t tokens, int64_t cols) {
+  let_next_start();
   constexpr int kPitch = kTokTile / 4 + 1;              // words
   __shared__ uint32_t colmax[kColTile];
   __shared__ uint32_t tile[kAct8Digits][kColTile][kPitch];
@@ -115,7 +117,7 @@ k_act8_digit_columns(Mat dy, const float* __restrict__ scale, int8_t* digits, in
   uint32_t m[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) m[i] = 0;
-  for (int64_t tt = blockIdx.y; tt < ntiles; tt += kColCluster) {
+  for (int64_t tt = blockIdx.y; tt < ntiles; tt += gridDim.y) {
     Raw8<T> r[4];
     float s[4];
 #pragma unroll
@@ -135,11 +137,16 @@ k_act8_digit_columns(Mat dy, const float* __restrict__ scale, int8_t* digits, in
     m[i] = max(m[i], __shfl_xor_sync(0xffffffffu, m[i], 16));
     if ((threadIdx.x & 24) == 0) atomicMax(&colmax[cgrp * 8 + i], m[i]);
   }
-  cluster.sync();
   uint32_t all = 0;
-  if (threadIdx.x < kColTile)
-    for (int k = 0; k < kColCluster; ++k) all = max(all, *cluster.map_shared_rank(&colmax[threadIdx.x], k));
-  cluster.sync();                                       // everyone has read before anyone overwrites or leaves
+  if (gridDim.y > 1) {
+    cluster.sync();
+    if (threadIdx.x < kColTile)
+      for (unsigned k = 0; k < gridDim.y; ++k) all = max(all, *cluster.map_shared_rank(&colmax[threadIdx.x], k));
+    cluster.sync();                                     // everyone has read before anyone overwrites or leaves
+  } else {
+    __syncthreads();
+    if (threadIdx.x < kColTile) all = colmax[threadIdx.x];
+  }
   if (threadIdx.x < kColTile) {
     colmax[threadIdx.x] = all;
     if (blockIdx.y == 0 && n0 + threadIdx.x < cols) row_scale[n0 + threadIdx.x] = Fixed(all).scale;
@@ -149,7 +156,7 @@ k_act8_digit_columns(Mat dy, const float* __restrict__ scale, int8_t* digits, in
 #pragma unroll
   for (int i = 0; i < 8; ++i) inv[i] = Fixed(colmax[cgrp * 8 + i]).inv;
 
-  for (int64_t tt = blockIdx.y; tt < ntiles; tt += kColCluster) {
+  for (int64_t tt = blockIdx.y; tt < ntiles; tt += gridDim.y) {
     uint32_t q[8][4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -212,6 +219,7 @@ __device__ __forceinline__ void store_parts(const float (&v)[8], __nv_bfloat16* 
 template <int PARTS>
 __global__ void __launch_bounds__(kThreads) k_act8_expand(Ckpt k, __nv_bfloat16* o, int64_t ld, int64_t rows,
                                                           int64_t cols, int group, int64_t groups) {
+  let_next_start();
   const Piece p;
   if (p.row >= rows || p.c >= cols) return;
   uint2 w;
@@ -226,6 +234,7 @@ __global__ void __launch_bounds__(kThreads) k_act8_expand(Ckpt k, __nv_bfloat16*
 template <class T, int PARTS>
 __global__ void __launch_bounds__(kThreads) k_act8_split(Mat x, __nv_bfloat16* o, int64_t ld, int64_t rows,
                                                          int64_t cols) {
+  let_next_start();
   const Piece p;
   if (p.row >= rows || p.c >= cols) return;
   Raw8<T> r;
@@ -239,8 +248,16 @@ __global__ void __launch_bounds__(kThreads) k_act8_split(Mat x, __nv_bfloat16* o
 // ------------------------------------------------------------------ host
 
 enum GradPath { kDigits, kBf16, kParts };
-GradPath grad_path(int32_t dtype, int32_t result, int32_t group) {
-  if (dtype == ACT8_BF16 && result == ACT8_BF16) return kBf16;
+// The result is rows x inner.  The bfloat16 path writes the codes out in
+// bfloat16 once (3 bytes a code, 25 us for 45M codes) where digits take half
+// as long again per row of the result (485 us for 8192 rows of the same
+// codes): even at about 420 rows.  It also has one form only, pairs of CTAs on
+// 256 x 256 tiles, so it wants tiles for most of them (512 x 768 and 2304 of
+// contraction: 20 against 16 us; 1024 x 4096: 40 against 61).
+constexpr int64_t kDigitRows = 420;
+GradPath grad_path(int32_t dtype, int32_t result, int32_t group, int64_t rows, int64_t inner) {
+  const bool many = rows > kDigitRows && ((rows + 255) / 256) * ((inner + 255) / 256) >= 48;
+  if (dtype == ACT8_BF16 && result == ACT8_BF16 && (group != 0 || many)) return kBf16;
   return group == 0 ? kDigits : kParts;
 }
 
@@ -258,7 +275,7 @@ struct GradPlan {
 GradPlan grad_plan(bool weight, int32_t dtype, int32_t result, int32_t group, int64_t tokens, int64_t out,
                    int64_t inner) {
   GradPlan p{};
-  p.path = grad_path(dtype, result, group);
+  p.path = grad_path(dtype, result, group, weight ? out : tokens, inner);
   if (p.path == kDigits) {
     const int64_t rows = weight ? out : tokens, k = weight ? tokens : out;
     p.ld_dy = int64_t(round_up(size_t(k), 16));
@@ -283,12 +300,25 @@ shampoo4_status digit_pass(bool weight, const void* dy, int32_t dtype, int64_t l
   const int64_t strips = (out + kColTile - 1) / kColTile;
   return by_dtype(dtype, [&](auto* tag) -> shampoo4_status {
     using T = std::remove_pointer_t<decltype(tag)>;
-    if (weight)
-      k_act8_digit_columns<T><<<dim3(unsigned(strips), kColCluster), kThreads, 0, st>>>(m, scale, digits, ld,
-                                                                                       row_scale, tokens, out);
-    else
+    if (weight) {
+      unsigned ctas = 1;                                // per strip: no more than it has tiles
+      while (ctas < kColCluster && int64_t(ctas) * kTokTile < tokens) ctas *= 2;
+      cudaLaunchConfig_t cfg{};
+      cfg.gridDim = dim3(unsigned(strips), ctas);
+      cfg.blockDim = dim3(kThreads);
+      cfg.stream = st;
+      cudaLaunchAttribute attr[1];
+      attr[0].id = cudaLaunchAttributeClusterDimension;
+      attr[0].val.clusterDim.x = 1;
+      attr[0].val.clusterDim.y = ctas;
+      attr[0].val.clusterDim.z = 1;
+      cfg.attrs = attr;
+      cfg.numAttrs = 1;
+      S4_CUDA(cudaLaunchKernelEx(&cfg, k_act8_digit_columns<T>, m, scale, digits, ld, row_scale, tokens, out));
+    } else {
       k_act8_digit_rows<T><<<unsigned(tokens), kThreads, 0, st>>>(m, scale, digits, ld, row_scale, tokens, out);
-    S4_CUDA(cudaGetLastError());
+      S4_CUDA(cudaGetLastError());
+    }
     return SHAMPOO4_OK;
   });
 }

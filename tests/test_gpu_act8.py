@@ -181,7 +181,7 @@ def check_product(y, xc, xs, wc, ws, bias, dtype):
 
 @pytest.mark.parametrize("tokens,out,inner", [
     (1, 1, 1), (1, 64, 64), (2, 7, 15), (3, 257, 127), (16, 300, 128), (17, 128, 129), (31, 255, 640), (33, 1000, 96),
-    (64, 512, 1000), (127, 256, 256), (128, 256, 385), (129, 257, 768), (300, 513, 1111), (700, 40, 2304)])
+    (64, 512, 1000), (65, 130, 4096), (48, 4100, 2050), (1, 4096, 4096), (13, 11008, 512), (127, 256, 256), (128, 256, 385), (129, 257, 768), (300, 513, 1111), (700, 40, 2304)])
 @pytest.mark.parametrize("dtype", list(DT))
 def test_matmul(tokens, out, inner, dtype):
     api = _api()
@@ -257,7 +257,9 @@ def grad_tolerance(dy, codes, scales, group, dtype, result, weight):
     a, b = np.abs(dy), np.abs(A.values64(codes, scales, group))
     K = codes.shape[0]
     S = (a.T if weight else a) @ b
-    if dtype == "bf16" and result == "bf16":
+    # bfloat16 with one scale per row and few result tiles goes through fixed point
+    tiles = -(-S.shape[0] // 256) * -(-S.shape[1] // 256)
+    if dtype == "bf16" and result == "bf16" and (group or (S.shape[0] > 420 and tiles >= 48)):
         return S * (1.01 * 2.0 ** -8 + (-(-K // 16) + 1) * 2.0 ** -22)
     if group == 0:
         s = scales.astype(np.float64)
@@ -270,7 +272,8 @@ def grad_tolerance(dy, codes, scales, group, dtype, result, weight):
 
 
 SHAPES = [(1, 1, 1), (1, 64, 300), (2, 7, 17), (63, 130, 65), (64, 128, 256), (65, 256, 257), (200, 129, 520),
-          (513, 300, 96), (1100, 64, 128), (30, 1500, 700), (3000, 140, 260)]
+          (513, 300, 96), (1100, 64, 128), (30, 1500, 700), (3000, 140, 260), (16, 500, 2900), (17, 2500, 130), (70, 1800, 1700),
+          (1800, 90, 1700)]
 TYPES = [("bf16", "bf16"), ("bf16", "fp32"), ("fp16", "fp16"), ("fp32", "fp32"), ("bf16", "fp16"), ("fp32", "bf16")]
 
 
