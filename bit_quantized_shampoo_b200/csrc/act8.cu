@@ -4,14 +4,30 @@
 //
 // A group of columns of a row (or the whole row) holds a = max |x|, the
 // scale s = fp32(a / 127) and, per element, the integer nearest to 127 x / a
-// (ties to even).  The code is that of the exact quotient: the fast path
-// multiplies by RN(127 / a), whose product is within 127 2^-23 < 2^-15 of
-// the quotient, and an element that close to a border between two codes is
-// decided by one double division (of two fp32 numbers a quotient that is not
-// a tie lies at least 2^-26 away from it, far above a double's rounding).
+// (ties to even), the code of the exact quotient.
 //
-// All kernels here stream: the bound is HBM bandwidth.
+// fp32: two factors bracket 127 / a, and one packed fp32 multiply-add each
+// rounds both products to integers; rounding is monotonic, so where the two
+// agree the code is that of the quotient between them.  Where they differ (a
+// border between two codes lies within 2^-20 of the quotient, exact ties
+// included) the sign of 254 |x| - (2 k + 1) a decides, in fp32 with the
+// products' exact remainders.
+//
+// 16-bit types: the factor above 127 / a alone.  With x = mx 2^i and a = ma
+// 2^j, mantissas below 2^11, a quotient q that is not a tie is at least
+// q / (254 mx) > q 2^-19 away from a border, and the factor is off by less
+// than 2^-20 of itself.  A tie, 254 |x| = (2 k + 1) a, needs the prime 127 in
+// 2 k + 1 (then k = 63, and the even code is the larger one, where the factor
+// rounds to) or in ma; groups with 127 in ma (one in 128) go the fp32 way.
+// (Ties are met often: with two factors for all types every fifth warp of
+// normal bfloat16 data held one, 190 against 120 us for 16384 x 11008.)
+//
+// All kernels here stream: the bound is HBM bandwidth, and then instructions
+// (the first form, with an IEEE division per lane and a distance test per
+// element, issued 25 instructions per element and ran at a third of the
+// bandwidth).
 #include "act8_elt.cuh"
+#include "quant4.cuh"
 
 namespace s4 {
 namespace {
@@ -20,208 +36,328 @@ constexpr float kScaleMax = 8454659.0f * 0x1p98f;      // the largest s with 127
 
 // ---- the code rule
 
+__device__ __forceinline__ float rcp_approx(float x) {  // within 1 ulp where the result is normal
+  float r;
+  asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
 struct Group {
-  float a;        // max |x|
-  float r;        // RN(127 / a); 0 where every code is 0
-  float scale;
-  bool fast;      // r normal: the fast path holds
+  float a;          // max |x|
+  uint64_t lo, hi;  // factors below and above 127 / a, twice each; 0 where every code is 0 or decided one by one
+  bool ties;        // 127 divides the mantissa of a
+  bool apart;       // decided one by one: NaN, infinity, or a magnitude that the factors do not fit
   __device__ __forceinline__ explicit Group(uint32_t bits) {
     a = __uint_as_float(bits);
-    const bool finite = bits < 0x7f800000u;
-    scale = finite ? fminf(__fdiv_rn(a, 127.0f), kScaleMax) : (bits > 0x7f800000u ? __uint_as_float(0x7fc00000u) : a);
-    fast = a >= 0x1p-118f || !finite || bits == 0u;
-    r = (finite && bits != 0u && fast) ? __fdiv_rn(127.0f, a) : 0.0f;
+    apart = bits != 0u && !(a >= 0x1p-100f && a <= 0x1p120f);
+    // 127 rcp(a) is within 2^-23 + 2^-24 of 127 / a, at most 3 of its ulps
+    const uint32_t r = __float_as_uint(127.0f * rcp_approx(a));
+    ties = ((bits & 0x7fffffu) | 0x800000u) % 127u == 0u;
+    const bool use = bits != 0u && !apart;
+    const float l = use ? __uint_as_float(r - 4) : 0.0f, h = use ? __uint_as_float(r + 4) : 0.0f;
+    lo = pack2(l, l);
+    hi = pack2(h, h);
+  }
+  // fp32(a / 127), capped: Markstein's correction (IBM J. Res. Dev. 34(1),
+  // 1990) of the product with RN(1/127); a plain division where the residual
+  // could underflow.
+  __device__ __forceinline__ float scale() const {
+    if (!(a < __int_as_float(0x7f800000))) return a > 0.0f ? a : __uint_as_float(0x7fc00000u);
+    if (a < 0x1p-90f) return __fdiv_rn(a, 127.0f);
+    constexpr float kInv = 1.0f / 127.0f;
+    const float q = a * kInv;
+    return fminf(fmaf(fmaf(-q, 127.0f, a), kInv, q), kScaleMax);
   }
 };
 
-__device__ __noinline__ float code_exact(float x, float a) { return float(rint(127.0 * double(x) / double(a))); }
-
-// The code of x as the low byte of the result.  A group without codes (zero
-// or non-finite) has r = 0; x * 0 may be NaN there, hence the select.
-__device__ __forceinline__ uint32_t code_of(float x, const Group& g) {
-  constexpr float kMagic = 12582912.0f;                 // 1.5 2^23: adding it rounds to an integer, ties to even
-  float t = fmaf(x, g.r, kMagic);
-  const float d = fmaf(x, g.r, -(t - kMagic));
-  if (!g.fast || fabsf(fabsf(d) - 0.5f) < 0x1p-15f) t = code_exact(x, g.a) + kMagic;
-  return g.r == 0.0f && g.fast ? 0u : (__float_as_uint(t) & 0xffu);
-}
+// The 8 codes one by one: groups of tiny or huge magnitude, and the zero
+// codes of a group with NaN or infinity.  (Two fp32 numbers' quotient that is
+// not a tie lies at least 2^-26 away from one, far above a double's rounding.)
 template <class T>
-__device__ __forceinline__ uint2 codes8(const Raw8<T>& r, const Group& g) {
+__device__ __noinline__ uint2 codes8_apart(Raw8<T> r, float a) {
   uint32_t b[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) b[i] = code_of(elt(r, i), g);
+  for (int i = 0; i < 8; ++i)
+    b[i] = a < __int_as_float(0x7f800000) ? uint32_t(__double2int_rn(127.0 * double(elt(r, i)) / double(a))) & 0xffu
+                                          : 0u;
   return make_uint2(b[0] | (b[1] << 8) | (b[2] << 16) | (b[3] << 24), b[4] | (b[5] << 8) | (b[6] << 16) | (b[7] << 24));
 }
-template <class T>
-__device__ __forceinline__ uint32_t absmax8(const Raw8<T>& r) {
-  uint32_t m = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) m = max(m, abs_bits(elt(r, i)));
-  return m;
+
+constexpr float kMagic = 12582912.0f;                   // 1.5 2^23: adding it rounds to an integer, ties to even
+
+// The code (plus kMagic) of an x between codes: k or k + 1 of its sign, k the
+// smaller in magnitude of the two candidates.  254 |x| and (2 k + 1) a as
+// rounded products and their exact remainders: the rounded ones are so close
+// that they subtract exactly, and the remainders have at most 9 bits.
+__device__ __forceinline__ uint32_t between(float x, float a, uint32_t t0, uint32_t t1) {
+  const float k = fminf(fabsf(__uint_as_float(t0) - kMagic), fabsf(__uint_as_float(t1) - kMagic));
+  const float odd = fmaf(2.0f, k, 1.0f), y = fabsf(x);
+  const float u = 254.0f * y, w = odd * a;
+  const float d = (u - w) + (fmaf(254.0f, y, -u) - fmaf(odd, a, -w));
+  const float up = d > 0.0f || (d == 0.0f && (int(k) & 1)) ? 1.0f : 0.0f;
+  return __float_as_uint(copysignf(k + up, x) + kMagic);
 }
+
+template <class T>
+__device__ __forceinline__ uint2 codes8(const Raw8<T>& r, const Group& g) {
+  const uint64_t magic = pack2(kMagic, kMagic);
+  if (g.apart) return codes8_apart(r, g.a);
+  uint32_t t[8];
+#pragma unroll
+  for (int i = 0; i < 8; i += 2) {
+    const uint64_t h = fma2(pack2(elt(r, i), elt(r, i + 1)), g.hi, magic);
+    t[i] = uint32_t(h);
+    t[i + 1] = uint32_t(h >> 32);
+  }
+  if (sizeof(T) == 4 || g.ties) {
+    uint32_t q[8];
+    uint32_t differ = 0;
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+      const uint64_t l = fma2(pack2(elt(r, i), elt(r, i + 1)), g.lo, magic);
+      q[i] = uint32_t(l);
+      q[i + 1] = uint32_t(l >> 32);
+      differ |= (t[i] ^ q[i]) | (t[i + 1] ^ q[i + 1]);
+    }
+    if (differ) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (t[i] != q[i]) t[i] = between(elt(r, i), g.a, t[i], q[i]);
+    }
+  }
+  return make_uint2(__byte_perm(__byte_perm(t[0], t[1], 0x0040), __byte_perm(t[2], t[3], 0x0040), 0x5410),
+                    __byte_perm(__byte_perm(t[4], t[5], 0x0040), __byte_perm(t[6], t[7], 0x0040), 0x5410));
+}
+
+// max |x| of 8 elements, as bits; NaN above everything.
+__device__ __forceinline__ uint32_t absmax8(const Raw8<float>& r) {
+  float m = absmax3_nan(elt(r, 0), elt(r, 1), elt(r, 2));
+  m = absmax3_nan(m, elt(r, 3), elt(r, 4));
+  m = absmax3_nan(m, elt(r, 5), elt(r, 6));
+  return abs_bits(max2_nan(m, fabsf(elt(r, 7))));
+}
+__device__ __forceinline__ uint32_t absmax8(const Raw8<__nv_bfloat16>& r) {
+  const __nv_bfloat162* w = reinterpret_cast<const __nv_bfloat162*>(r.v);
+  const __nv_bfloat162 m = __hmax2_nan(__hmax2_nan(__habs2(w[0]), __habs2(w[1])),
+                                       __hmax2_nan(__habs2(w[2]), __habs2(w[3])));
+  return abs_bits(max2_nan(__low2float(m), __high2float(m)));
+}
+__device__ __forceinline__ uint32_t absmax8(const Raw8<__half>& r) {
+  const __half2* w = reinterpret_cast<const __half2*>(r.v);
+  const __half2 m = __hmax2_nan(__hmax2_nan(__habs2(w[0]), __habs2(w[1])),
+                                __hmax2_nan(__habs2(w[2]), __habs2(w[3])));
+  return abs_bits(max2_nan(__low2float(m), __high2float(m)));
+}
+
 // ---- pack
 
-template <class T>
-__global__ void __launch_bounds__(kThreads) k_act8_pack_groups(Mat x, Ckpt o, int64_t rows, int64_t cols, int group) {
-  const Piece p;
+template <class T, int kRows>
+__global__ void __launch_bounds__(kThreads) k_act8_pack_groups(Mat x, Ckpt o, int64_t rows, int cols) {
+  const Piece<kRows> p;
   if (p.row >= rows) return;                             // a whole warp
-  Raw8<T> r;
-  load8(static_cast<const T*>(x.p) + p.row * x.ld, p.c, cols, x.vec, r);
-  const Group g(group_max(absmax8(r), group / 8));
-  if (p.c >= cols) return;
-  store_codes8(o.codes + p.row * o.ldc, p.c, cols, codes8(r, g));
-  if (p.c % group == 0) o.scales[p.row * ((cols + group - 1) / group) + p.c / group] = g.scale;
+  Raw8<T> r[kRows];
+#pragma unroll
+  for (int u = 0; u < kRows; ++u)
+    load8(static_cast<const T*>(x.p) + p.at(u) * x.ld, p.c, p.at(u) < rows ? cols : 0, x.vec, r[u]);
+#pragma unroll
+  for (int u = 0; u < kRows; ++u) {
+    const int64_t row = p.at(u);
+    const Group g(group_max(absmax8(r[u]), 1 << (o.shift - 3)));
+    if (row >= rows || p.c >= cols) continue;
+    store_codes8(o.codes + row * o.ldc, p.c, cols, codes8(r[u], g));
+    if ((p.c & ((1 << o.shift) - 1)) == 0) o.scales[row * o.groups + (p.c >> o.shift)] = g.scale();
+  }
 }
 
-// One scale for the row: a CTA per row.  IT > 0: the row (at most
-// IT * 2048 columns) stays in registers between the maximum and the codes;
-// IT = 0: it is read twice.
-template <class T, int IT>
-__global__ void __launch_bounds__(kThreads) k_act8_pack_rows(Mat x, Ckpt o, int64_t rows, int64_t cols) {
-  __shared__ uint32_t slots[kThreads / 32];
+// One scale for the row.  WARP: a warp per row (up to 1024 columns); else a
+// CTA per row.  IT > 0: a thread's at most IT pieces of 8 columns stay in
+// registers between the maximum and the codes; IT = 0: the row is read twice.
+constexpr int kRowThreads = 768;                         // two such CTAs per SM: 42 registers
+template <class T, int IT, bool WARP>
+__global__ void __launch_bounds__(kRowThreads, 2) k_act8_pack_rows(Mat x, Ckpt o, int64_t rows, int cols) {
+  __shared__ uint32_t slots[32];
   let_next_start();
-  for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
-    const T* xr = static_cast<const T*>(x.p) + row * x.ld;
-    int8_t* cr = o.codes + row * o.ldc;
-    uint32_t m = 0;
-    if (IT > 0) {
-      Raw8<T> r[IT > 0 ? IT : 1];
+  const int64_t row = WARP ? int64_t(blockIdx.x) * blockDim.y + threadIdx.y : int64_t(blockIdx.x);
+  if (row >= rows) return;                               // a whole warp, or nobody
+  const T* xr = static_cast<const T*>(x.p) + row * x.ld;
+  int8_t* cr = o.codes + row * o.ldc;
+  const int step = int(blockDim.x) * 8, first = int(threadIdx.x) * 8;
+  uint32_t m = 0;
+  if (IT > 0) {
+    Raw8<T> r[IT > 0 ? IT : 1];
 #pragma unroll
-      for (int i = 0; i < IT; ++i) load8(xr, (int64_t(i) * kThreads + threadIdx.x) * 8, cols, x.vec, r[i]);
+    for (int i = 0; i < IT; ++i) load8(xr, first + i * step, cols, x.vec, r[i]);
 #pragma unroll
-      for (int i = 0; i < IT; ++i) m = max(m, absmax8(r[i]));
-      const Group g(cta_max(m, slots));
+    for (int i = 0; i < IT; ++i) m = max(m, absmax8(r[i]));
+    m = WARP ? __reduce_max_sync(0xffffffffu, m) : cta_max(m, slots);
+    const Group g(m);
 #pragma unroll
-      for (int i = 0; i < IT; ++i) {
-        const int64_t c = (int64_t(i) * kThreads + threadIdx.x) * 8;
-        if (c < cols) store_codes8(cr, c, cols, codes8(r[i], g));
-      }
-      if (threadIdx.x == 0) o.scales[row] = g.scale;
-    } else {
-      Raw8<T> r;
-      for (int64_t c = threadIdx.x * 8; c < cols; c += kThreads * 8) {
-        load8(xr, c, cols, x.vec, r);
-        m = max(m, absmax8(r));
-      }
-      const Group g(cta_max(m, slots));
-      for (int64_t c = threadIdx.x * 8; c < cols; c += kThreads * 8) {
-        load8(xr, c, cols, x.vec, r);
-        store_codes8(cr, c, cols, codes8(r, g));
-      }
-      if (threadIdx.x == 0) o.scales[row] = g.scale;
+    for (int i = 0; i < IT; ++i) {
+      const int c = first + i * step;
+      if (c < cols) store_codes8(cr, c, cols, codes8(r[i], g));
     }
+    if (threadIdx.x == 0) o.scales[row] = g.scale();
+  } else {
+    Raw8<T> r;
+    for (int c = first; c < cols; c += step) {
+      load8(xr, c, cols, x.vec, r);
+      m = max(m, absmax8(r));
+    }
+    const Group g(cta_max(m, slots));
+    for (int c = first; c < cols; c += step) {
+      load8(xr, c, cols, x.vec, r);
+      store_codes8(cr, c, cols, codes8(r, g));
+    }
+    if (threadIdx.x == 0) o.scales[row] = g.scale();
   }
 }
 
 // ---- unpack
 
-template <class T>
-__global__ void __launch_bounds__(kThreads) k_act8_unpack(Ckpt k, T* x, int64_t ldx, int vec, int64_t rows,
-                                                          int64_t cols, int group, int64_t groups) {
-  const Piece p;
+template <class T, int kRows>
+__global__ void __launch_bounds__(kThreads) k_act8_unpack(Ckpt k, T* x, int64_t ldx, int vec, int64_t rows, int cols) {
+  const Piece<kRows> p;
   if (p.row >= rows || p.c >= cols) return;
-  uint2 w;
-  load_codes8(k.codes + p.row * k.ldc, p.c, cols, w);
-  const float s = __ldg(k.scales + p.row * groups + (group ? p.c / group : 0));
-  float v[8];
+  uint2 w[kRows];
+  float s[kRows];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = code_at(w, i) * s;
-  store8(x + p.row * ldx, p.c, cols, vec, v);
+  for (int u = 0; u < kRows; ++u) {
+    const int64_t row = p.at(u);
+    load_codes8(k.codes + row * k.ldc, p.c, row < rows ? cols : 0, w[u]);
+    s[u] = row < rows ? __ldg(k.scales + row * k.groups + (p.c >> k.shift)) : 0.0f;
+  }
+#pragma unroll
+  for (int u = 0; u < kRows; ++u) {
+    float v[8];
+    values8(w[u], s[u], v);
+    store8(x + p.at(u) * ldx, p.c, p.at(u) < rows ? cols : 0, vec, v);
+  }
 }
 
 // ---- the gated activation
 
-__device__ __forceinline__ float sigmoid(float x) { return __fdiv_rn(1.0f, 1.0f + expf(-x)); }
+// 1 / (1 + exp(-x)).  fp32: the accurate exponential, then a reciprocal
+// within an ulp (2^-22 in all); 16-bit results: the base-2 exponential unit,
+// off by 2^-22 and by the rounding of its argument (up to 88 log2(e) 2^-24),
+// below 1e-5, against their half step of 2^-11 or 2^-8.
+template <class T>
+__device__ __forceinline__ float sigmoid(float x) {
+  if (sizeof(T) == 4) return rcp_approx(1.0f + expf(-x));
+  float e;
+  asm("ex2.approx.f32 %0, %1;" : "=f"(e) : "f"(x * -1.4426950408889634f));
+  return rcp_approx(1.0f + e);
+}
 
 template <class T>
-__device__ __forceinline__ void gated8(const Raw8<T>& g, const Raw8<T>& u, T* h, int64_t c, int64_t n, bool vec) {
+__device__ __forceinline__ void gated8(const Raw8<T>& g, const Raw8<T>& u, T* h, int c, int n, int vec) {
   float v[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const float x = elt(g, i);
-    v[i] = x * sigmoid(x) * elt(u, i);
+    v[i] = x * sigmoid<T>(x) * elt(u, i);
   }
   store8(h, c, n, vec, v);
 }
 
-template <class T>
+template <class T, int kRows>
 __global__ void __launch_bounds__(kThreads)
-k_act8_swiglu_groups(Mat gate, Mat up, T* h, int64_t ldh, int vech, Ckpt kg, Ckpt ku, int64_t rows, int64_t cols,
-                     int group) {
-  const Piece p;
+k_act8_swiglu_groups(Mat gate, Mat up, T* h, int64_t ldh, int vech, Ckpt kg, Ckpt ku, int64_t rows, int cols) {
+  const Piece<kRows> p;
   if (p.row >= rows) return;
-  Raw8<T> g, u;
-  load8(static_cast<const T*>(gate.p) + p.row * gate.ld, p.c, cols, gate.vec, g);
-  load8(static_cast<const T*>(up.p) + p.row * up.ld, p.c, cols, up.vec, u);
-  const Group gg(group_max(absmax8(g), group / 8)), gu(group_max(absmax8(u), group / 8));
-  if (p.c >= cols) return;
-  gated8(g, u, h + p.row * ldh, p.c, cols, vech);
-  store_codes8(kg.codes + p.row * kg.ldc, p.c, cols, codes8(g, gg));
-  store_codes8(ku.codes + p.row * ku.ldc, p.c, cols, codes8(u, gu));
-  if (p.c % group == 0) {
-    const int64_t s = p.row * ((cols + group - 1) / group) + p.c / group;
-    kg.scales[s] = gg.scale;
-    ku.scales[s] = gu.scale;
+  Raw8<T> g[kRows], u[kRows];
+#pragma unroll
+  for (int k = 0; k < kRows; ++k) {
+    const int64_t row = p.at(k);
+    const int n = row < rows ? cols : 0;
+    load8(static_cast<const T*>(gate.p) + row * gate.ld, p.c, n, gate.vec, g[k]);
+    load8(static_cast<const T*>(up.p) + row * up.ld, p.c, n, up.vec, u[k]);
+  }
+#pragma unroll
+  for (int k = 0; k < kRows; ++k) {
+    const int64_t row = p.at(k);
+    const int lanes = 1 << (kg.shift - 3);
+    const Group gg(group_max(absmax8(g[k]), lanes)), gu(group_max(absmax8(u[k]), lanes));
+    if (row >= rows || p.c >= cols) continue;
+    store_codes8(kg.codes + row * kg.ldc, p.c, cols, codes8(g[k], gg));
+    store_codes8(ku.codes + row * ku.ldc, p.c, cols, codes8(u[k], gu));
+    if ((p.c & ((1 << kg.shift) - 1)) == 0) {
+      const int64_t s = row * kg.groups + (p.c >> kg.shift);
+      kg.scales[s] = gg.scale();
+      ku.scales[s] = gu.scale();
+    }
+    gated8(g[k], u[k], h + row * ldh, p.c, cols, vech);
   }
 }
 
-// One scale per row: the row is read twice (the second time from L2).
+// One scale per row: the row is read twice (the second time from cache).
 template <class T>
 __global__ void __launch_bounds__(kThreads)
-k_act8_swiglu_rows(Mat gate, Mat up, T* h, int64_t ldh, int vech, Ckpt kg, Ckpt ku, int64_t rows, int64_t cols) {
+k_act8_swiglu_rows(Mat gate, Mat up, T* h, int64_t ldh, int vech, Ckpt kg, Ckpt ku, int64_t rows, int cols) {
   __shared__ uint32_t slots[kThreads / 32];
-  for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
-    const T* gr = static_cast<const T*>(gate.p) + row * gate.ld;
-    const T* ur = static_cast<const T*>(up.p) + row * up.ld;
-    Raw8<T> g, u;
-    uint32_t mg = 0, mu = 0;
-    for (int64_t c = threadIdx.x * 8; c < cols; c += kThreads * 8) {
-      load8(gr, c, cols, gate.vec, g);
-      load8(ur, c, cols, up.vec, u);
-      mg = max(mg, absmax8(g));
-      mu = max(mu, absmax8(u));
-      gated8(g, u, h + row * ldh, c, cols, vech);
-    }
-    const Group gg(cta_max(mg, slots)), gu(cta_max(mu, slots));
-    for (int64_t c = threadIdx.x * 8; c < cols; c += kThreads * 8) {
-      load8(gr, c, cols, gate.vec, g);
-      load8(ur, c, cols, up.vec, u);
-      store_codes8(kg.codes + row * kg.ldc, c, cols, codes8(g, gg));
-      store_codes8(ku.codes + row * ku.ldc, c, cols, codes8(u, gu));
-    }
-    if (threadIdx.x == 0) {
-      kg.scales[row] = gg.scale;
-      ku.scales[row] = gu.scale;
-    }
+  const int64_t row = blockIdx.x;
+  const T* gr = static_cast<const T*>(gate.p) + row * gate.ld;
+  const T* ur = static_cast<const T*>(up.p) + row * up.ld;
+  Raw8<T> g, u;
+  uint32_t mg = 0, mu = 0;
+#pragma unroll 2
+  for (int c = int(threadIdx.x) * 8; c < cols; c += kThreads * 8) {
+    load8(gr, c, cols, gate.vec, g);
+    load8(ur, c, cols, up.vec, u);
+    mg = max(mg, absmax8(g));
+    mu = max(mu, absmax8(u));
+    gated8(g, u, h + row * ldh, c, cols, vech);
+  }
+  const Group gg(cta_max(mg, slots)), gu(cta_max(mu, slots));
+#pragma unroll 2
+  for (int c = int(threadIdx.x) * 8; c < cols; c += kThreads * 8) {
+    load8(gr, c, cols, gate.vec, g);
+    load8(ur, c, cols, up.vec, u);
+    store_codes8(kg.codes + row * kg.ldc, c, cols, codes8(g, gg));
+    store_codes8(ku.codes + row * ku.ldc, c, cols, codes8(u, gu));
+  }
+  if (threadIdx.x == 0) {
+    kg.scales[row] = gg.scale();
+    ku.scales[row] = gu.scale();
   }
 }
 
-template <class T>
+template <class T, int kRows>
 __global__ void __launch_bounds__(kThreads)
 k_act8_swiglu_backward(Mat dh, Ckpt kg, Ckpt ku, T* dg, int64_t lddg, int vecg, T* du, int64_t lddu, int vecu,
-                       int64_t rows, int64_t cols, int group, int64_t groups) {
-  const Piece p;
+                       int64_t rows, int cols) {
+  const Piece<kRows> p;
   if (p.row >= rows || p.c >= cols) return;
-  Raw8<T> d;
-  uint2 wg, wu;
-  load8(static_cast<const T*>(dh.p) + p.row * dh.ld, p.c, cols, dh.vec, d);
-  load_codes8(kg.codes + p.row * kg.ldc, p.c, cols, wg);
-  load_codes8(ku.codes + p.row * ku.ldc, p.c, cols, wu);
-  const int64_t s = p.row * groups + (group ? p.c / group : 0);
-  const float sg = __ldg(kg.scales + s), su = __ldg(ku.scales + s);
-  float og[8], ou[8];
+  Raw8<T> d[kRows];
+  uint2 wg[kRows], wu[kRows];
+  float sg[kRows], su[kRows];
+  const int gi = p.c >> kg.shift;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float g = code_at(wg, i) * sg, u = code_at(wu, i) * su, x = elt(d, i);
-    const float sig = sigmoid(g);
-    ou[i] = x * (g * sig);
-    og[i] = x * u * (sig * fmaf(g, 1.0f - sig, 1.0f));
+  for (int k = 0; k < kRows; ++k) {
+    const int64_t row = p.at(k);
+    const int n = row < rows ? cols : 0;
+    load8(static_cast<const T*>(dh.p) + row * dh.ld, p.c, n, dh.vec, d[k]);
+    load_codes8(kg.codes + row * kg.ldc, p.c, n, wg[k]);
+    load_codes8(ku.codes + row * ku.ldc, p.c, n, wu[k]);
+    sg[k] = n ? __ldg(kg.scales + row * kg.groups + gi) : 0.0f;
+    su[k] = n ? __ldg(ku.scales + row * ku.groups + gi) : 0.0f;
   }
-  store8(dg + p.row * lddg, p.c, cols, vecg, og);
-  store8(du + p.row * lddu, p.c, cols, vecu, ou);
+#pragma unroll
+  for (int k = 0; k < kRows; ++k) {
+    const int64_t row = p.at(k);
+    const int n = row < rows ? cols : 0;
+    float g[8], u[8], og[8], ou[8];
+    values8(wg[k], sg[k], g);
+    values8(wu[k], su[k], u);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float x = elt(d[k], i), sig = sigmoid<T>(g[i]);
+      ou[i] = x * (g[i] * sig);
+      og[i] = x * u[i] * (sig * fmaf(g[i], 1.0f - sig, 1.0f));
+    }
+    store8(dg + row * lddg, p.c, n, vecg, og);
+    store8(du + row * lddu, p.c, n, vecu, ou);
+  }
 }
-
-// ------------------------------------------------------------------ host
 
 shampoo4_status pack(const void* x, int32_t dtype, int64_t rows, int64_t cols, int64_t ldx, int32_t group, Ckpt o,
                      cudaStream_t st) {
@@ -232,15 +368,28 @@ shampoo4_status pack(const void* x, int32_t dtype, int64_t rows, int64_t cols, i
     if (group) {
       const dim3 b = piece_block(cols);
       dim3 g;
-      if (!piece_grid(rows, cols, b, &g)) return SHAMPOO4_ERR_INVALID_ARG;
-      k_act8_pack_groups<T><<<g, b, 0, st>>>(m, o, rows, cols, group);
+      constexpr int kMany = sizeof(T) == 4 ? 2 : 4;
+      const bool many = many_pieces(rows, cols);
+      if (!piece_grid(rows, cols, b, many ? kMany : 1, &g)) return SHAMPOO4_ERR_INVALID_ARG;
+      if (many) k_act8_pack_groups<T, kMany><<<g, b, 0, st>>>(m, o, rows, int(cols));
+      else k_act8_pack_groups<T, 1><<<g, b, 0, st>>>(m, o, rows, int(cols));
+    } else if (cols <= 1024) {                           // 8 rows per CTA, a warp each
+      const dim3 b(32, 8);
+      const unsigned g = unsigned((rows + 7) / 8);
+      if (cols <= 256) k_act8_pack_rows<T, 1, true><<<g, b, 0, st>>>(m, o, rows, int(cols));
+      else if (cols <= 512) k_act8_pack_rows<T, 2, true><<<g, b, 0, st>>>(m, o, rows, int(cols));
+      else k_act8_pack_rows<T, 4, true><<<g, b, 0, st>>>(m, o, rows, int(cols));
     } else {
-      const unsigned g = unsigned(std::min<int64_t>(rows, 0x7fffffff));
-      if (cols <= 2048) k_act8_pack_rows<T, 1><<<g, kThreads, 0, st>>>(m, o, rows, cols);
-      else if (cols <= 4096) k_act8_pack_rows<T, 2><<<g, kThreads, 0, st>>>(m, o, rows, cols);
-      else if (cols <= 8192) k_act8_pack_rows<T, 4><<<g, kThreads, 0, st>>>(m, o, rows, cols);
-      else if (cols <= 16384) k_act8_pack_rows<T, 8><<<g, kThreads, 0, st>>>(m, o, rows, cols);
-      else k_act8_pack_rows<T, 0><<<g, kThreads, 0, st>>>(m, o, rows, cols);
+      // no more threads than pieces: one each in rows up to 4096, two up to
+      // 12288, four up to 24576
+      const int64_t pieces = (cols + 7) / 8;
+      const int it = pieces <= 512 ? 1 : (pieces <= 2 * kRowThreads ? 2 : 4);
+      const unsigned b = unsigned(std::min<int64_t>(kRowThreads, ((pieces + it - 1) / it + 31) / 32 * 32));
+      const unsigned g = unsigned(rows);
+      if (pieces > 4 * kRowThreads) k_act8_pack_rows<T, 0, false><<<g, b, 0, st>>>(m, o, rows, int(cols));
+      else if (it == 1) k_act8_pack_rows<T, 1, false><<<g, b, 0, st>>>(m, o, rows, int(cols));
+      else if (it == 2) k_act8_pack_rows<T, 2, false><<<g, b, 0, st>>>(m, o, rows, int(cols));
+      else k_act8_pack_rows<T, 4, false><<<g, b, 0, st>>>(m, o, rows, int(cols));
     }
     S4_CUDA(cudaGetLastError());
     return SHAMPOO4_OK;
@@ -260,7 +409,8 @@ extern "C" shampoo4_status act8_pack(const void* d_x, int32_t dtype, int64_t row
   if (!shape_ok(rows, cols) || !dtype_ok(dtype) || !group_ok(group)) return SHAMPOO4_ERR_INVALID_ARG;
   if (rows == 0 || cols == 0) return SHAMPOO4_OK;
   if (!mat_ok(d_x, dtype, rows, cols, ldx) || !codes_ok(d_codes, ldc, cols, d_scales)) return SHAMPOO4_ERR_INVALID_ARG;
-  return pack(d_x, dtype, rows, cols, ldx, group, Ckpt{d_codes, ldc, d_scales}, reinterpret_cast<cudaStream_t>(stream));
+  return pack(d_x, dtype, rows, cols, ldx, group, ckpt(d_codes, ldc, d_scales, cols, group),
+              reinterpret_cast<cudaStream_t>(stream));
 }
 
 extern "C" shampoo4_status act8_unpack(const int8_t* d_codes, int64_t ldc, const float* d_scales, int64_t rows,
@@ -269,14 +419,18 @@ extern "C" shampoo4_status act8_unpack(const int8_t* d_codes, int64_t ldc, const
   if (!shape_ok(rows, cols) || !dtype_ok(dtype) || !group_ok(group)) return SHAMPOO4_ERR_INVALID_ARG;
   if (rows == 0 || cols == 0) return SHAMPOO4_OK;
   if (!mat_ok(d_x, dtype, rows, cols, ldx) || !codes_ok(d_codes, ldc, cols, d_scales)) return SHAMPOO4_ERR_INVALID_ARG;
+  const bool many = many_pieces(rows, cols);
   const dim3 b = piece_block(cols);
   dim3 g;
-  if (!piece_grid(rows, cols, b, &g)) return SHAMPOO4_ERR_INVALID_ARG;
-  const Ckpt k{const_cast<int8_t*>(d_codes), ldc, const_cast<float*>(d_scales)};
+  if (!piece_grid(rows, cols, b, many ? 4 : 1, &g)) return SHAMPOO4_ERR_INVALID_ARG;
+  const Ckpt k = ckpt(d_codes, ldc, d_scales, cols, group);
+  const int vec = vec_of(d_x, ldx, dtype);
+  const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   return by_dtype(dtype, [&](auto* tag) -> shampoo4_status {
     using T = std::remove_pointer_t<decltype(tag)>;
-    k_act8_unpack<T><<<g, b, 0, reinterpret_cast<cudaStream_t>(stream)>>>(
-        k, static_cast<T*>(d_x), ldx, row_aligned(d_x, ldx, dtype), rows, cols, group, group_count(cols, group));
+    T* x = static_cast<T*>(d_x);
+    if (many) k_act8_unpack<T, 4><<<g, b, 0, st>>>(k, x, ldx, vec, rows, int(cols));
+    else k_act8_unpack<T, 1><<<g, b, 0, st>>>(k, x, ldx, vec, rows, int(cols));
     S4_CUDA(cudaGetLastError());
     return SHAMPOO4_OK;
   });
@@ -341,18 +495,23 @@ extern "C" shampoo4_status act8_swiglu(const void* d_gate, int64_t ldg, const vo
     return SHAMPOO4_ERR_INVALID_ARG;
   const dim3 b = piece_block(cols);
   dim3 g;
-  if (!piece_grid(rows, cols, b, &g)) return SHAMPOO4_ERR_INVALID_ARG;
+  const bool many = dtype != ACT8_FP32 && many_pieces(rows, cols);
+  if (!piece_grid(rows, cols, b, many ? 2 : 1, &g)) return SHAMPOO4_ERR_INVALID_ARG;
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  const Ckpt kg{d_gate_codes, ldgc, d_gate_scales}, ku{d_up_codes, lduc, d_up_scales};
-  const int vh = row_aligned(d_h, ldh, dtype);
+  const Ckpt kg = ckpt(d_gate_codes, ldgc, d_gate_scales, cols, group);
+  const Ckpt ku = ckpt(d_up_codes, lduc, d_up_scales, cols, group);
+  const int vh = vec_of(d_h, ldh, dtype);
   return by_dtype(dtype, [&](auto* tag) -> shampoo4_status {
     using T = std::remove_pointer_t<decltype(tag)>;
-    if (group)
-      k_act8_swiglu_groups<T><<<g, b, 0, st>>>(mat(d_gate, ldg, dtype), mat(d_up, ldu, dtype), static_cast<T*>(d_h),
-                                               ldh, vh, kg, ku, rows, cols, group);
+    const Mat mg = mat(d_gate, ldg, dtype), mu = mat(d_up, ldu, dtype);
+    T* h = static_cast<T*>(d_h);
+    if (group && many)
+      k_act8_swiglu_groups<T, 2><<<g, b, 0, st>>>(mg, mu, h, ldh, vh, kg, ku, rows, int(cols));
+    else if (group)
+      k_act8_swiglu_groups<T, 1><<<g, b, 0, st>>>(mg, mu, h, ldh, vh, kg, ku, rows, int(cols));
     else
-      k_act8_swiglu_rows<T><<<unsigned(std::min<int64_t>(rows, 0x7fffffff)), kThreads, 0, st>>>(
-          mat(d_gate, ldg, dtype), mat(d_up, ldu, dtype), static_cast<T*>(d_h), ldh, vh, kg, ku, rows, cols);
+      k_act8_swiglu_rows<T><<<unsigned(rows), kThreads, 0, st>>>(
+          mg, mu, h, ldh, vh, kg, ku, rows, int(cols));
     S4_CUDA(cudaGetLastError());
     return SHAMPOO4_OK;
   });
@@ -371,14 +530,20 @@ extern "C" shampoo4_status act8_swiglu_backward(const void* d_dh, int64_t lddh, 
     return SHAMPOO4_ERR_INVALID_ARG;
   const dim3 b = piece_block(cols);
   dim3 g;
-  if (!piece_grid(rows, cols, b, &g)) return SHAMPOO4_ERR_INVALID_ARG;
-  const Ckpt kg{const_cast<int8_t*>(d_gate_codes), ldgc, const_cast<float*>(d_gate_scales)};
-  const Ckpt ku{const_cast<int8_t*>(d_up_codes), lduc, const_cast<float*>(d_up_scales)};
+  const bool many = dtype != ACT8_FP32 && many_pieces(rows, cols);
+  if (!piece_grid(rows, cols, b, many ? 2 : 1, &g)) return SHAMPOO4_ERR_INVALID_ARG;
+  const Ckpt kg = ckpt(d_gate_codes, ldgc, d_gate_scales, cols, group);
+  const Ckpt ku = ckpt(d_up_codes, lduc, d_up_scales, cols, group);
+  const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   return by_dtype(dtype, [&](auto* tag) -> shampoo4_status {
     using T = std::remove_pointer_t<decltype(tag)>;
-    k_act8_swiglu_backward<T><<<g, b, 0, reinterpret_cast<cudaStream_t>(stream)>>>(
-        mat(d_dh, lddh, dtype), kg, ku, static_cast<T*>(d_dgate), lddg, row_aligned(d_dgate, lddg, dtype),
-        static_cast<T*>(d_dup), lddu, row_aligned(d_dup, lddu, dtype), rows, cols, group, group_count(cols, group));
+    const Mat m = mat(d_dh, lddh, dtype);
+    T *dg = static_cast<T*>(d_dgate), *du = static_cast<T*>(d_dup);
+    const int vg = vec_of(dg, lddg, dtype), vu = vec_of(du, lddu, dtype);
+    if (many)
+      k_act8_swiglu_backward<T, 2><<<g, b, 0, st>>>(m, kg, ku, dg, lddg, vg, du, lddu, vu, rows, int(cols));
+    else
+      k_act8_swiglu_backward<T, 1><<<g, b, 0, st>>>(m, kg, ku, dg, lddg, vg, du, lddu, vu, rows, int(cols));
     S4_CUDA(cudaGetLastError());
     return SHAMPOO4_OK;
   });

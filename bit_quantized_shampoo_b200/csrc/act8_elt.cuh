@@ -30,41 +30,99 @@ __device__ __forceinline__ float elt(const Raw8<__half>& r, int i) {
   const uint32_t w = reinterpret_cast<const uint32_t*>(r.v)[i >> 1];
   return __half2float(__ushort_as_half(uint16_t((i & 1) ? (w >> 16) : w)));
 }
-__device__ __forceinline__ void to_elt(float x, float& o) { o = x; }
-__device__ __forceinline__ void to_elt(float x, __nv_bfloat16& o) { o = __float2bfloat16_rn(x); }
-__device__ __forceinline__ void to_elt(float x, __half& o) { o = __float2half_rn(x); }
 
-// Columns c .. c + 7 of a row of n (zeros past its end).
+// Two floats as the operand of a packed fp32 instruction.
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// Columns c .. c + 7 of a row of n (zeros past its end).  vec: 1 when rows
+// are 16-byte aligned, 2 when they are 32-byte aligned (fp32 then moves its 8
+// elements at once).
 template <class T>
-__device__ __forceinline__ void load8(const T* row, int64_t c, int64_t n, bool vec, Raw8<T>& r) {
+__device__ __forceinline__ void load8(const T* row, int c, int n, int vec, Raw8<T>& r) {
   if (vec && c + 8 <= n) {
-    const uint4* p = reinterpret_cast<const uint4*>(row + c);
+    if (sizeof(T) == 4 && vec == 2) {
+      uint32_t* w = reinterpret_cast<uint32_t*>(r.v);
+      asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                   : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+                   : "l"(row + c));
+    } else {
+      const uint4* p = reinterpret_cast<const uint4*>(row + c);
 #pragma unroll
-    for (int i = 0; i < int(sizeof(T) / 2); ++i) r.v[i] = __ldg(p + i);
+      for (int i = 0; i < int(sizeof(T) / 2); ++i) r.v[i] = __ldg(p + i);
+    }
   } else {
     T* e = reinterpret_cast<T*>(r.v);
 #pragma unroll
     for (int i = 0; i < 8; ++i) e[i] = c + i < n ? row[c + i] : T(0.0f);
   }
 }
+__device__ __forceinline__ void round8(const float (&v)[8], Raw8<float>& r) {
+  uint32_t* w = reinterpret_cast<uint32_t*>(r.v);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(v[i]);
+}
+__device__ __forceinline__ void round8(const float (&v)[8], Raw8<__nv_bfloat16>& r) {
+  uint32_t* w = reinterpret_cast<uint32_t*>(r.v);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 x = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+    w[i] = *reinterpret_cast<const uint32_t*>(&x);
+  }
+}
+__device__ __forceinline__ void round8(const float (&v)[8], Raw8<__half>& r) {
+  uint32_t* w = reinterpret_cast<uint32_t*>(r.v);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __half2 x = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
+    w[i] = *reinterpret_cast<const uint32_t*>(&x);
+  }
+}
 template <class T>
-__device__ __forceinline__ void store8(T* row, int64_t c, int64_t n, bool vec, const float (&v)[8]) {
+__device__ __forceinline__ void store8(T* row, int c, int n, int vec, const float (&v)[8]) {
   Raw8<T> r;
-  T* e = reinterpret_cast<T*>(r.v);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) to_elt(v[i], e[i]);
+  round8(v, r);
   if (vec && c + 8 <= n) {
-    uint4* p = reinterpret_cast<uint4*>(row + c);
+    if (sizeof(T) == 4 && vec == 2) {
+      const uint32_t* w = reinterpret_cast<const uint32_t*>(r.v);
+      asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+                   ::"l"(row + c), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]),
+                     "r"(w[7]) : "memory");
+    } else {
+      uint4* p = reinterpret_cast<uint4*>(row + c);
 #pragma unroll
-    for (int i = 0; i < int(sizeof(T) / 2); ++i) p[i] = r.v[i];
+      for (int i = 0; i < int(sizeof(T) / 2); ++i) p[i] = r.v[i];
+    }
   } else {
+    const T* e = reinterpret_cast<const T*>(r.v);
 #pragma unroll
     for (int i = 0; i < 8; ++i)
       if (c + i < n) row[c + i] = e[i];
   }
 }
 // Code rows are 16-byte aligned, so 8 codes at a multiple of 8 are one word pair.
-__device__ __forceinline__ void load_codes8(const int8_t* row, int64_t c, int64_t n, uint2& w) {
+__device__ __forceinline__ void load_codes8(const int8_t* row, int c, int n, uint2& w) {
   if (c + 8 <= n) {
     w = __ldg(reinterpret_cast<const uint2*>(row + c));
   } else {
@@ -74,7 +132,7 @@ __device__ __forceinline__ void load_codes8(const int8_t* row, int64_t c, int64_
       if (c + i < n) (i < 4 ? w.x : w.y) |= uint32_t(uint8_t(row[c + i])) << (8 * (i & 3));
   }
 }
-__device__ __forceinline__ void store_codes8(int8_t* row, int64_t c, int64_t n, uint2 w) {
+__device__ __forceinline__ void store_codes8(int8_t* row, int c, int n, uint2 w) {
   if (c + 8 <= n) {
     *reinterpret_cast<uint2*>(row + c) = w;
   } else {
@@ -83,8 +141,18 @@ __device__ __forceinline__ void store_codes8(int8_t* row, int64_t c, int64_t n, 
       if (c + i < n) row[c + i] = int8_t((i < 4 ? w.x : w.y) >> (8 * (i & 3)));
   }
 }
-__device__ __forceinline__ float code_at(uint2 w, int i) {
-  return float(int8_t((i < 4 ? w.x : w.y) >> (8 * (i & 3))));
+// The 8 values code * s (one fp32 multiply each).  A code's byte with its
+// sign bit flipped, under the exponent of 2^23, is the float 2^23 + 128 +
+// code: cheaper than an integer conversion, and as exact.
+__device__ __forceinline__ void values8(uint2 w, float s, float (&v)[8]) {
+  const uint64_t s2 = pack2(s, s), off = pack2(-8388736.0f, -8388736.0f);
+#pragma unroll
+  for (int i = 0; i < 8; i += 2) {
+    const uint32_t b = (i < 4 ? w.x : w.y) ^ 0x80808080u;
+    const float x0 = __uint_as_float(__byte_perm(b, 0x4B000000u, 0x7540 | (i & 3)));
+    const float x1 = __uint_as_float(__byte_perm(b, 0x4B000000u, 0x7540 | ((i & 3) + 1)));
+    unpack2(mul2(add2(pack2(x0, x1), off), s2), v[i], v[i + 1]);
+  }
 }
 
 // Bits of |x|: as integers they order NaN above +Inf above every finite
@@ -94,7 +162,9 @@ __device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x
 
 // Over the group's lanes (a power of two, consecutive, aligned).
 __device__ __forceinline__ uint32_t group_max(uint32_t m, int lanes) {
-  for (int o = lanes >> 1; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+#pragma unroll
+  for (int o = 1; o < 32; o *= 2)
+    if (o < lanes) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
   return m;
 }
 // Over the CTA, whatever its shape; slots: one word per warp.
@@ -114,31 +184,38 @@ __device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.
 struct Mat {
   const void* p;
   int64_t ld;
-  int32_t vec;       // rows are 16-byte aligned
+  int32_t vec;       // see load8
 };
 struct Ckpt {
   int8_t* codes;
   int64_t ldc;
   float* scales;     // rows x groups, dense
+  int32_t groups, shift;   // column c is in group c >> shift
 };
 
 // Pieces of rows as warps: blockDim = (32 wx, wy), blockIdx.x over rows,
-// blockIdx.y over column pieces.
+// blockIdx.y over column pieces.  A thread takes ROWS rows, wy apart, whose
+// loads it issues together.
+template <int ROWS>
 struct Piece {
-  int64_t row, c;    // this lane's first column
+  int64_t row;       // the first row
+  int c;             // this lane's first column
   __device__ __forceinline__ Piece() {
-    row = int64_t(blockIdx.x) * blockDim.y + threadIdx.y;
-    c = (int64_t(blockIdx.y) * (blockDim.x >> 5) + (threadIdx.x >> 5)) * kChunk + (threadIdx.x & 31) * 8;
+    row = int64_t(blockIdx.x) * (blockDim.y * ROWS) + threadIdx.y;
+    c = int((blockIdx.y * (blockDim.x >> 5) + (threadIdx.x >> 5)) * kChunk + (threadIdx.x & 31) * 8);
   }
+  __device__ __forceinline__ int64_t at(int u) const { return row + int64_t(u) * blockDim.y; }
 };
 dim3 piece_block(int64_t cols) {
   unsigned wx = 1;
   while (wx < kThreads / 32 && int64_t(wx) * kChunk < cols) wx *= 2;
   return dim3(32 * wx, kThreads / 32 / wx);
 }
-bool piece_grid(int64_t rows, int64_t cols, dim3 b, dim3* g) {
-  const int64_t per = int64_t(b.x / 32) * kChunk;
-  const int64_t gx = (rows + b.y - 1) / b.y, gy = (cols + per - 1) / per;
+// Whether several rows per thread still leave every SM its 2048 threads.
+bool many_pieces(int64_t rows, int64_t cols) { return rows * ((cols + 7) / 8) >= int64_t(4) * 148 * 2048; }
+bool piece_grid(int64_t rows, int64_t cols, dim3 b, int rows_per_thread, dim3* g) {
+  const int64_t per = int64_t(b.x / 32) * kChunk, rp = int64_t(b.y) * rows_per_thread;
+  const int64_t gx = (rows + rp - 1) / rp, gy = (cols + per - 1) / per;
   if (gx > 0x7fffffffLL || gy > 65535) return false;
   *g = dim3(unsigned(gx), unsigned(gy));
   return true;
@@ -149,6 +226,13 @@ bool piece_grid(int64_t rows, int64_t cols, dim3 b, dim3* g) {
 int64_t elt_size(int32_t dtype) { return dtype == ACT8_FP32 ? 4 : 2; }
 bool dtype_ok(int32_t d) { return d == ACT8_FP32 || d == ACT8_BF16 || d == ACT8_FP16; }
 bool group_ok(int32_t g) { return g == 0 || g == 32 || g == 64 || g == 128 || g == 256; }
+// Column c lies in group c >> group_shift (rows have at most 2^30 columns).
+int group_shift(int32_t group) {
+  int s = 31;
+  if (group)
+    for (s = 5; (1 << s) < group; ++s) {}
+  return s;
+}
 int64_t group_count(int64_t cols, int32_t group) { return group ? (cols + group - 1) / group : 1; }
 bool shape_ok(int64_t rows, int64_t cols) {
   return rows >= 0 && cols >= 0 && rows <= kAct8MaxDim && cols <= kAct8MaxDim;
@@ -163,7 +247,17 @@ bool codes_ok(const void* p, int64_t ldc, int64_t cols, const void* scales) {
 bool row_aligned(const void* p, int64_t ld, int32_t dtype) {
   return aligned(p, 16) && (ld * elt_size(dtype)) % 16 == 0;
 }
-Mat mat(const void* p, int64_t ld, int32_t dtype) { return Mat{p, ld, row_aligned(p, ld, dtype) ? 1 : 0}; }
+// 0: element-aligned rows only, 1: 16-byte aligned ones, 2: 32-byte.
+int vec_of(const void* p, int64_t ld, int32_t dtype) {
+  if (!row_aligned(p, ld, dtype)) return 0;
+  return aligned(p, 32) && (ld * elt_size(dtype)) % 32 == 0 ? 2 : 1;
+}
+Mat mat(const void* p, int64_t ld, int32_t dtype) { return Mat{p, ld, vec_of(p, ld, dtype)}; }
+
+Ckpt ckpt(const int8_t* codes, int64_t ldc, const float* scales, int64_t cols, int32_t group) {
+  return Ckpt{const_cast<int8_t*>(codes), ldc, const_cast<float*>(scales), int32_t(group_count(cols, group)),
+              group_shift(group)};
+}
 
 // Call f(T*) with a null pointer of the element type.
 template <class F>

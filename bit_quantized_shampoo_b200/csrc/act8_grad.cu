@@ -61,14 +61,14 @@ __device__ __forceinline__ uint32_t bytes4(uint32_t x0, uint32_t x1, uint32_t x2
 template <class T>
 __global__ void __launch_bounds__(kThreads)
 k_act8_digit_rows(Mat dy, const float* __restrict__ scale, int8_t* digits, int64_t ld, float* row_scale, int64_t rows,
-                  int64_t cols) {
+                  int cols) {
   let_next_start();
   __shared__ uint32_t slots[kThreads / 32];
   const int64_t row = blockIdx.x;
   const T* x = static_cast<const T*>(dy.p) + row * dy.ld;
   Raw8<T> r;
   uint32_t m = 0;
-  for (int64_t c = threadIdx.x * 8; c < cols; c += kThreads * 8) {
+  for (int c = int(threadIdx.x) * 8; c < cols; c += kThreads * 8) {
     load8(x, c, cols, dy.vec, r);
 #pragma unroll
     for (int i = 0; i < 8; ++i)
@@ -76,7 +76,7 @@ k_act8_digit_rows(Mat dy, const float* __restrict__ scale, int8_t* digits, int64
   }
   const Fixed f(cta_max(m, slots));
   if (threadIdx.x == 0) row_scale[row] = f.scale;
-  for (int64_t c = threadIdx.x * 8; c < ld; c += kThreads * 8) {      // ld: the padding gets zeros
+  for (int c = int(threadIdx.x) * 8; c < ld; c += kThreads * 8) {      // ld: the padding gets zeros
     load8(x, c, cols, dy.vec, r);
     uint32_t q[8];
 #pragma unroll
@@ -108,7 +108,7 @@ k_act8_digit_columns(Mat dy, const float* __restrict__ scale, int8_t* digits, in
   cg::cluster_group cluster = cg::this_cluster();
   const int64_t n0 = int64_t(blockIdx.x) * kColTile;
   const int cgrp = threadIdx.x & 7, tgrp = threadIdx.x >> 3;     // 8 columns, 4 tokens
-  const int64_t c = n0 + cgrp * 8;
+  const int c = int(n0) + cgrp * 8;
   const int64_t ntiles = (tokens + kTokTile - 1) / kTokTile;
   const T* x = static_cast<const T*>(dy.p);
   if (threadIdx.x < kColTile) colmax[threadIdx.x] = 0;
@@ -123,7 +123,7 @@ k_act8_digit_columns(Mat dy, const float* __restrict__ scale, int8_t* digits, in
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int64_t t = tt * kTokTile + tgrp * 4 + j;
-      load8(x + t * dy.ld, c, t < tokens ? cols : 0, dy.vec, r[j]);
+      load8(x + t * dy.ld, c, t < tokens ? int(cols) : 0, dy.vec, r[j]);
       s[j] = t < tokens ? __ldg(scale + t) : 0.0f;
     }
 #pragma unroll
@@ -162,7 +162,7 @@ k_act8_digit_columns(Mat dy, const float* __restrict__ scale, int8_t* digits, in
     for (int j = 0; j < 4; ++j) {
       const int64_t t = tt * kTokTile + tgrp * 4 + j;
       Raw8<T> r;
-      load8(x + t * dy.ld, c, t < tokens ? cols : 0, dy.vec, r);
+      load8(x + t * dy.ld, c, t < tokens ? int(cols) : 0, dy.vec, r);
       const float s = t < tokens ? __ldg(scale + t) : 0.0f;
       Fixed f(0u);
 #pragma unroll
@@ -202,8 +202,7 @@ __device__ __forceinline__ void split(float v, float (&p)[3]) {
   }
 }
 template <int PARTS>
-__device__ __forceinline__ void store_parts(const float (&v)[8], __nv_bfloat16* o, int64_t plane, int64_t c,
-                                            int64_t cols) {
+__device__ __forceinline__ void store_parts(const float (&v)[8], __nv_bfloat16* o, int64_t plane, int c, int cols) {
   float p[PARTS][8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
@@ -218,24 +217,23 @@ __device__ __forceinline__ void store_parts(const float (&v)[8], __nv_bfloat16* 
 
 template <int PARTS>
 __global__ void __launch_bounds__(kThreads) k_act8_expand(Ckpt k, __nv_bfloat16* o, int64_t ld, int64_t rows,
-                                                          int64_t cols, int group, int64_t groups) {
+                                                          int cols) {
   let_next_start();
-  const Piece p;
+  const Piece<1> p;
   if (p.row >= rows || p.c >= cols) return;
   uint2 w;
   load_codes8(k.codes + p.row * k.ldc, p.c, cols, w);
-  const float s = __ldg(k.scales + p.row * groups + (group ? p.c / group : 0));
+  const float s = __ldg(k.scales + p.row * k.groups + (p.c >> k.shift));
   float v[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = code_at(w, i) * s;
+  values8(w, s, v);
   store_parts<PARTS>(v, o + p.row * ld, rows * ld, p.c, cols);
 }
 
 template <class T, int PARTS>
 __global__ void __launch_bounds__(kThreads) k_act8_split(Mat x, __nv_bfloat16* o, int64_t ld, int64_t rows,
-                                                         int64_t cols) {
+                                                         int cols) {
   let_next_start();
-  const Piece p;
+  const Piece<1> p;
   if (p.row >= rows || p.c >= cols) return;
   Raw8<T> r;
   load8(static_cast<const T*>(x.p) + p.row * x.ld, p.c, cols, x.vec, r);
@@ -316,21 +314,21 @@ shampoo4_status digit_pass(bool weight, const void* dy, int32_t dtype, int64_t l
       cfg.numAttrs = 1;
       S4_CUDA(cudaLaunchKernelEx(&cfg, k_act8_digit_columns<T>, m, scale, digits, ld, row_scale, tokens, out));
     } else {
-      k_act8_digit_rows<T><<<unsigned(tokens), kThreads, 0, st>>>(m, scale, digits, ld, row_scale, tokens, out);
+      k_act8_digit_rows<T><<<unsigned(tokens), kThreads, 0, st>>>(m, scale, digits, ld, row_scale, tokens, int(out));
       S4_CUDA(cudaGetLastError());
     }
     return SHAMPOO4_OK;
   });
 }
 
-shampoo4_status expand(const Ckpt& k, int64_t rows, int64_t cols, int32_t group, int parts, void* o, int64_t ld,
+shampoo4_status expand(const Ckpt& k, int64_t rows, int64_t cols, int parts, void* o, int64_t ld,
                        cudaStream_t st) {
   const dim3 b = piece_block(cols);
   dim3 g;
-  if (!piece_grid(rows, cols, b, &g)) return SHAMPOO4_ERR_INVALID_ARG;
+  if (!piece_grid(rows, cols, b, 1, &g)) return SHAMPOO4_ERR_INVALID_ARG;
   __nv_bfloat16* p = static_cast<__nv_bfloat16*>(o);
-  if (parts == 1) k_act8_expand<1><<<g, b, 0, st>>>(k, p, ld, rows, cols, group, group_count(cols, group));
-  else k_act8_expand<3><<<g, b, 0, st>>>(k, p, ld, rows, cols, group, group_count(cols, group));
+  if (parts == 1) k_act8_expand<1><<<g, b, 0, st>>>(k, p, ld, rows, int(cols));
+  else k_act8_expand<3><<<g, b, 0, st>>>(k, p, ld, rows, int(cols));
   S4_CUDA(cudaGetLastError());
   return SHAMPOO4_OK;
 }
@@ -339,12 +337,12 @@ shampoo4_status split_dy(const void* x, int32_t dtype, int64_t ldx, int64_t rows
                          cudaStream_t st) {
   const dim3 b = piece_block(cols);
   dim3 g;
-  if (!piece_grid(rows, cols, b, &g)) return SHAMPOO4_ERR_INVALID_ARG;
+  if (!piece_grid(rows, cols, b, 1, &g)) return SHAMPOO4_ERR_INVALID_ARG;
   const Mat m = mat(x, ldx, dtype);
   __nv_bfloat16* p = static_cast<__nv_bfloat16*>(o);
-  if (dtype == ACT8_BF16) k_act8_split<__nv_bfloat16, 1><<<g, b, 0, st>>>(m, p, ld, rows, cols);
-  else if (dtype == ACT8_FP16) k_act8_split<__half, 2><<<g, b, 0, st>>>(m, p, ld, rows, cols);
-  else k_act8_split<float, 3><<<g, b, 0, st>>>(m, p, ld, rows, cols);
+  if (dtype == ACT8_BF16) k_act8_split<__nv_bfloat16, 1><<<g, b, 0, st>>>(m, p, ld, rows, int(cols));
+  else if (dtype == ACT8_FP16) k_act8_split<__half, 2><<<g, b, 0, st>>>(m, p, ld, rows, int(cols));
+  else k_act8_split<float, 3><<<g, b, 0, st>>>(m, p, ld, rows, int(cols));
   S4_CUDA(cudaGetLastError());
   return SHAMPOO4_OK;
 }
@@ -374,7 +372,7 @@ shampoo4_status grad(bool weight, const void* dy, int32_t dtype, int64_t lddy, c
     S4_TRY(split_dy(dy, dtype, lddy, tokens, out, w, p.ld_dy, st));
   }
   const Act8Operand a{w + p.dy_bytes, p.ld_code, K};
-  S4_TRY(expand(k, K, inner, group, p.code_parts, w + p.dy_bytes, p.ld_code, st));
+  S4_TRY(expand(k, K, inner, p.code_parts, w + p.dy_bytes, p.ld_code, st));
   return launch_act8_bf16(a, p.code_parts, b, p.dy_parts, weight ? 1 : 0, inner, R, K, o, flags, st);
 }
 
@@ -405,7 +403,7 @@ static shampoo4_status grad_call(bool weight, const void* d_dy, int32_t dtype, i
   if (K > 0 && (!mat_ok(d_dy, dtype, tokens, out, lddy) || !codes_ok(codes, ldc, inner, scales)))
     return SHAMPOO4_ERR_INVALID_ARG;
   const Act8Out o{d_y, ldy, result, accumulate ? 1 : 0, nullptr, nullptr, nullptr};
-  return grad(weight, d_dy, dtype, lddy, Ckpt{const_cast<int8_t*>(codes), ldc, const_cast<float*>(scales)}, group,
+  return grad(weight, d_dy, dtype, lddy, ckpt(codes, ldc, scales, inner, group), group,
               tokens, out, inner, o, d_ws, ws_bytes, d_flags, reinterpret_cast<cudaStream_t>(stream));
 }
 
