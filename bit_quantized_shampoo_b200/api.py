@@ -322,158 +322,40 @@ def quant4_tables(codebook="linear_square"):
 #
 # Codes are int8 tensors (rows x cols, rows a multiple of 16 bytes apart and
 # 16-byte aligned), scales fp32 (rows x groups); group 0 means one scale per
-# row.  Matrices are 2-D CUDA tensors with unit column stride.  The smallest
-# calls take a few microseconds on the device, so the marshalling here is kept
-# short: plain integers for pointers, one allocation per tensor, no device
-# switch when the tensors' device is the current one.
+# row, else 32, 64, 128 or 256 columns share one.  Matrices are 2-D CUDA
+# tensors with unit column stride.  Results may be given (``out``) or are
+# allocated; ``stream`` defaults to the current stream of the tensors' device.
+# Arguments that do not fit raise TypeError or ValueError before anything is
+# enqueued.  The checks and calls are in csrc/act8_binding.cpp: the smallest
+# of these calls take a few microseconds, less than the same checks in Python.
 
-_ACT8_DTYPES = {torch.float32: L.ACT8_FP32, torch.bfloat16: L.ACT8_BF16, torch.float16: L.ACT8_FP16}
-_ACT8_GROUPS = (0, 32, 64, 128, 256)
-
-
-def _act8_dtype(dtype, name):
-    code = _ACT8_DTYPES.get(dtype)
-    if code is None:
-        raise TypeError(f"{name} must be float32, bfloat16 or float16, not {dtype}")
-    return code
-
-
-def _act8_mat(t, name, shape=None, device=None):
-    """(pointer, dtype code, rows, columns, leading dimension) of a float matrix."""
-    if not (isinstance(t, torch.Tensor) and t.is_cuda):
-        raise TypeError(f"{name} must be a CUDA tensor")
-    code = _act8_dtype(t.dtype, name)
-    if t.dim() != 2:
-        raise ValueError(f"{name} must be 2-D with unit column stride")
-    rows, cols = t.shape
-    ld, step = t.stride()
-    if step != 1 and cols > 1:
-        raise ValueError(f"{name} must be 2-D with unit column stride")
-    if shape is not None and (rows, cols) != tuple(shape):
-        raise ValueError(f"{name}: shape {(rows, cols)} != {tuple(shape)}")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} is on {t.device}, not on {device}")
-    if rows <= 1:                  # a single row has no stride of its own: any that keeps its alignment
-        ld = (cols + 15) // 16 * 16
-    return t.data_ptr(), code, rows, cols, ld
+def _act8():
+    """The binding module; like the library, it has to be built."""
+    global _act8_module
+    if _act8_module is None:
+        L.lib()
+        try:
+            from . import _act8 as module
+        except ImportError as e:
+            raise RuntimeError("the act8 binding is not built: run `python -m bit_quantized_shampoo_b200.build`") from e
+        module.set_check(L.check)
+        _act8_module = module
+    return _act8_module
 
 
-def _act8_codes(codes, scales, group, name, device=None):
-    """(code pointer, leading dimension, scale pointer) of stored codes."""
-    if not (isinstance(codes, torch.Tensor) and codes.is_cuda and codes.dtype == torch.int8 and codes.dim() == 2):
-        raise TypeError(f"{name} codes must be a 2-D CUDA int8 tensor")
-    if not (isinstance(scales, torch.Tensor) and scales.is_cuda and scales.dtype == torch.float32):
-        raise TypeError(f"{name} scales must be a CUDA float32 tensor")
-    rows, cols = codes.shape
-    ld, step = codes.stride()
-    if step != 1 and cols > 1:
-        raise ValueError(f"{name} codes must have unit column stride")
-    groups = _act8_groups(cols, group)
-    if scales.shape != (rows, groups) or not scales.is_contiguous():
-        raise ValueError(f"{name} scales must be a contiguous {rows} x {groups} tensor")
-    dev = codes.device
-    if scales.device != dev or (device is not None and dev != device):
-        raise ValueError(f"{name} codes and scales must be on the other tensors' device")
-    if rows <= 1:
-        ld = (cols + 15) // 16 * 16
-    p = codes.data_ptr()
-    if (ld | p) & 15 and rows and cols:
-        raise ValueError(f"{name} codes must be 16-byte aligned with rows a multiple of 16 bytes apart")
-    return p, ld, scales.data_ptr()
-
-
-def _act8_groups(cols, group):
-    if group not in _ACT8_GROUPS:
-        raise ValueError("group must be 0, 32, 64, 128 or 256")
-    if cols == 0:
-        return 0
-    return 1 if group == 0 else -(-cols // group)
-
-
-def _act8_store(rows, cols, group, device):
-    """Uninitialized codes (rows padded to 16 bytes) and scales, and their
-    (code pointer, leading dimension, scale pointer)."""
-    ld = (cols + 15) // 16 * 16
-    codes = torch.empty_strided((rows, cols), (ld, 1), dtype=torch.int8, device=device)
-    groups = _act8_groups(cols, group)
-    scales = torch.empty_strided((rows, groups), (groups, 1), dtype=torch.float32, device=device)
-    return codes, scales, (codes.data_ptr(), ld, scales.data_ptr())
-
-
-def _act8_out(out, rows, cols, dtype, device, name="out"):
-    """The result tensor and its (pointer, dtype code, leading dimension)."""
-    if out is None:
-        out = torch.empty_strided((rows, cols), (cols, 1), dtype=dtype, device=device)
-        return out, out.data_ptr(), _ACT8_DTYPES[dtype], cols if rows > 1 else (cols + 15) // 16 * 16
-    p, code, _, _, ld = _act8_mat(out, name, (rows, cols), device)
-    return out, p, code, ld
-
-
-def _act8_vec(t, n, dtypes, name, device):
-    """Pointer of an optional contiguous vector (0 when there is none)."""
-    if t is None:
-        return 0
-    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype in dtypes and t.is_contiguous() and t.numel() == n
-            and t.device == device):
-        raise TypeError(f"{name} must be a contiguous {dtypes[0]} tensor of {n} on {device}")
-    return t.data_ptr()
-
-
-_BIAS_TYPES = (torch.float32,)
-_FLAG_TYPES = (torch.int32, torch.uint32)
-
-
-def _act8_call(device, stream, fn, *args):
-    """The call on the tensors' device: ``stream``, or that device's current
-    stream."""
-    if device.index != torch.cuda.current_device():
-        with torch.cuda.device(device):
-            return _act8_call(device, stream, fn, *args)
-    if stream is None:
-        raw = torch._C._cuda_getCurrentRawStream(device.index)
-    else:
-        raw = stream.cuda_stream
-    st = getattr(L.lib(), fn)(*args, raw)
-    if st:
-        L.check(fn, st)
+_act8_module = None
 
 
 def act8_pack(x, group=0, codes=None, scales=None, stream=None):
     """8-bit codes and scales of a matrix: per group of columns of a row (or
     per row, group 0) the scale is fp32(max|x| / 127) and a code the integer
     nearest to 127 x / max|x|.  Returns (codes, scales)."""
-    p, dt, rows, cols, ld = _act8_mat(x, "x")
-    if (codes is None) != (scales is None):
-        raise ValueError("give both codes and scales, or neither")
-    if codes is None:
-        codes, scales, (cp, ldc, sp) = _act8_store(rows, cols, group, x.device)
-    else:
-        cp, ldc, sp = _act8_codes(codes, scales, group, "x", x.device)
-        if codes.shape != x.shape:
-            raise ValueError(f"codes: shape {tuple(codes.shape)} != {(rows, cols)}")
-    _act8_call(x.device, stream, "act8_pack", p, dt, rows, cols, ld, group, cp, ldc, sp)
-    return codes, scales
+    return (_act8_module or _act8()).pack(x, group, codes, scales, stream)
 
 
 def act8_unpack(codes, scales, group=0, dtype=torch.float32, out=None, stream=None):
     """code * scale as ``dtype`` (``out``'s type when given)."""
-    cp, ldc, sp = _act8_codes(codes, scales, group, "x")
-    _act8_dtype(dtype, "dtype")
-    rows, cols = codes.shape
-    dev = codes.device
-    out, op, dt, ldo = _act8_out(out, rows, cols, dtype, dev)
-    _act8_call(dev, stream, "act8_unpack", cp, ldc, sp, rows, cols, group, op, dt, ldo)
-    return out
-
-
-def _act8_inner(inner, w_codes, what):
-    """The output size of a product over ``inner`` columns."""
-    n, wi = w_codes.shape
-    if inner != wi:
-        raise ValueError(f"{what}: inner sizes {inner} and {wi} differ")
-    if inner > 1 << 17:
-        raise ValueError(f"{what}: inner size {inner} > 2^17")
-    return n
+    return (_act8_module or _act8()).unpack(codes, scales, group, dtype, out, stream)
 
 
 def act8_matmul(x_codes, x_scales, w_codes, w_scales, bias=None, dtype=torch.bfloat16, out=None, flags=None,
@@ -481,67 +363,14 @@ def act8_matmul(x_codes, x_scales, w_codes, w_scales, bias=None, dtype=torch.bfl
     """Y = X W^T (+ bias) from codes with one scale per row of X (token) and
     of W (output channel): exact integer sums, scaled in fp32, rounded once
     to ``dtype`` (``out``'s type when given)."""
-    xp, ldx, xs = _act8_codes(x_codes, x_scales, 0, "x")
-    dev = x_codes.device
-    wp, ldw, ws = _act8_codes(w_codes, w_scales, 0, "w", dev)
-    tokens, inner = x_codes.shape
-    n = _act8_inner(inner, w_codes, "act8_matmul")
-    _act8_dtype(dtype, "dtype")
-    out, op, dt, ldo = _act8_out(out, tokens, n, dtype, dev)
-    _act8_call(dev, stream, "act8_matmul", xp, ldx, xs, wp, ldw, ws, _act8_vec(bias, n, _BIAS_TYPES, "bias", dev),
-               tokens, n, inner, op, dt, ldo, _act8_vec(flags, 1, _FLAG_TYPES, "flags", dev))
-    return out
-
-
-def _act8_on(stream, make):
-    """make(), under ``stream`` when one is given, so that the caching allocator keeps the
-    scratch it allocates for the work enqueued there."""
-    if stream is None:
-        return make()
-    with torch.cuda.stream(stream):
-        return make()
+    return (_act8_module or _act8()).matmul(x_codes, x_scales, w_codes, w_scales, bias, dtype, out, flags, stream)
 
 
 def act8_linear(x, w_codes, w_scales, bias=None, out=None, checkpoint=False, flags=None, stream=None):
     """A linear layer on 8-bit codes: x quantized per token, then
     act8_matmul; the result has x's type (or ``out``'s).  With ``checkpoint``
     returns (y, x_codes, x_scales) for act8_weight_grad, else y."""
-    xp, xdt, tokens, inner, ldx = _act8_mat(x, "x")
-    dev = x.device
-    wp, ldw, ws = _act8_codes(w_codes, w_scales, 0, "w", dev)
-    n = _act8_inner(inner, w_codes, "act8_linear")
-    out, op, dt, ldo = _act8_out(out, tokens, n, x.dtype, dev)
-    if checkpoint:
-        codes, scales, (cp, ldc, sp) = _act8_store(tokens, inner, 0, dev)
-    else:                          # scratch of this call: codes, then scales, in one buffer
-        ldc = (inner + 15) // 16 * 16
-        size = tokens * ldc + 4 * tokens
-        work = _act8_on(stream, lambda: torch.empty_strided((size,), (1,), dtype=torch.int8, device=dev))
-        cp = work.data_ptr()
-        sp = cp + tokens * ldc
-    _act8_call(dev, stream, "act8_linear", xp, xdt, ldx, wp, ldw, ws, _act8_vec(bias, n, _BIAS_TYPES, "bias", dev),
-               tokens, n, inner, cp, ldc, sp, op, dt, ldo, _act8_vec(flags, 1, _FLAG_TYPES, "flags", dev))
-    return (out, codes, scales) if checkpoint else out
-
-
-def _act8_grad(fn, dy, codes, scales, group, rows, dtype, out, accumulate, flags, stream):
-    """Either gradient: dy (tokens x out) against stored codes, result rows x
-    the codes' columns."""
-    dp, ddt, tokens, n, ldd = _act8_mat(dy, "dy")
-    dev = dy.device
-    weight = fn == "act8_weight_grad"
-    cp, ldc, sp = _act8_codes(codes, scales, group, "x" if weight else "w", dev)
-    if out is None and accumulate:
-        raise ValueError("accumulate needs out")
-    inner = codes.shape[1]
-    out, op, odt, ldo = _act8_out(out, rows, inner, dtype, dev)
-    need = C.c_size_t()
-    L.call("act8_grad_workspace", int(weight), ddt, odt, tokens, n, inner, group, need)
-    work = _act8_on(stream, lambda: torch.empty_strided((need.value,), (1,), dtype=torch.int8, device=dev))
-    given = (dp, ddt, ldd, cp, ldc, sp) + ((group,) if weight else ())
-    _act8_call(dev, stream, fn, *given, tokens, n, inner, op, odt, ldo, int(bool(accumulate)), work.data_ptr(),
-               need.value, _act8_vec(flags, 1, _FLAG_TYPES, "flags", dev))
-    return out
+    return (_act8_module or _act8()).linear(x, w_codes, w_scales, bias, out, checkpoint, flags, stream)
 
 
 def act8_weight_grad(dy, x_codes, x_scales, group=0, dtype=torch.float32, out=None, accumulate=False, flags=None,
@@ -549,51 +378,22 @@ def act8_weight_grad(dy, x_codes, x_scales, group=0, dtype=torch.float32, out=No
     """dW = dY^T X from the layer input's 8-bit checkpoint: dy is tokens x
     out, the codes tokens x inner; the result out x inner in ``dtype`` (or
     ``out``'s type), added to ``out`` with ``accumulate``."""
-    if dy.dim() != 2 or x_codes.dim() != 2 or dy.shape[0] != x_codes.shape[0]:
-        raise ValueError("dy and x must be 2-D with the same number of rows")
-    _act8_dtype(dtype, "dtype")
-    return _act8_grad("act8_weight_grad", dy, x_codes, x_scales, group, dy.shape[1], dtype, out, accumulate, flags,
-                      stream)
+    return (_act8_module or _act8()).grad(True, dy, x_codes, x_scales, group, dtype, out, accumulate, flags, stream)
 
 
 def act8_input_grad(dy, w_codes, w_scales, dtype=None, out=None, accumulate=False, flags=None, stream=None):
     """dX = dY W from the 8-bit weight (one scale per row): dy is tokens x
     out, the codes out x inner; the result tokens x inner in ``dtype``
     (default dy's, or ``out``'s), added to ``out`` with ``accumulate``."""
-    if dy.dim() != 2 or w_codes.dim() != 2 or dy.shape[1] != w_codes.shape[0]:
-        raise ValueError("dy and w must be 2-D, dy's columns matching w's rows")
-    dtype = dy.dtype if dtype is None else dtype
-    _act8_dtype(dtype, "dtype")
-    return _act8_grad("act8_input_grad", dy, w_codes, w_scales, 0, dy.shape[0], dtype, out, accumulate, flags, stream)
+    return (_act8_module or _act8()).grad(False, dy, w_codes, w_scales, 0, dtype, out, accumulate, flags, stream)
 
 
 def act8_swiglu(gate, up, group=128, out=None, stream=None):
     """h = gate sigmoid(gate) up, keeping gate and up as 8-bit codes in the
     same pass.  Returns (h, (gate codes, gate scales, up codes, up scales))."""
-    gp, dt, rows, cols, ldg = _act8_mat(gate, "gate")
-    dev = gate.device
-    pu, dtu, _, _, ldu = _act8_mat(up, "up", (rows, cols), dev)
-    out, hp, dth, ldh = _act8_out(out, rows, cols, gate.dtype, dev)
-    if dtu != dt or dth != dt:
-        raise TypeError("gate, up and out must have one type")
-    gc, gs, g3 = _act8_store(rows, cols, group, dev)
-    uc, us, u3 = _act8_store(rows, cols, group, dev)
-    _act8_call(dev, stream, "act8_swiglu", gp, ldg, pu, ldu, dt, rows, cols, group, hp, ldh, *g3, *u3)
-    return out, (gc, gs, uc, us)
+    return (_act8_module or _act8()).swiglu(gate, up, group, out, stream)
 
 
 def act8_swiglu_backward(dh, kept, group=128, dgate=None, dup=None, stream=None):
     """(dgate, dup) of act8_swiglu from dh and the codes it kept."""
-    gate_codes, gate_scales, up_codes, up_scales = kept
-    dp, dt, rows, cols, ldd = _act8_mat(dh, "dh", gate_codes.shape)
-    dev = dh.device
-    if up_codes.shape != gate_codes.shape:
-        raise ValueError("gate and up codes differ in shape")
-    g3 = _act8_codes(gate_codes, gate_scales, group, "gate", dev)
-    u3 = _act8_codes(up_codes, up_scales, group, "up", dev)
-    dgate, gp, dtg, ldg = _act8_out(dgate, rows, cols, dh.dtype, dev, "dgate")
-    dup, pu, dtu, ldu = _act8_out(dup, rows, cols, dh.dtype, dev, "dup")
-    if dtg != dt or dtu != dt:
-        raise TypeError("dh, dgate and dup must have one type")
-    _act8_call(dev, stream, "act8_swiglu_backward", dp, ldd, dt, *g3, *u3, rows, cols, group, gp, ldg, pu, ldu)
-    return dgate, dup
+    return (_act8_module or _act8()).swiglu_backward(dh, kept, group, dgate, dup, stream)

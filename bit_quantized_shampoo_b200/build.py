@@ -1,6 +1,9 @@
-"""Build libshampoo4.so in-tree with nvcc for sm_100a.
+"""Build libshampoo4.so in-tree with nvcc for sm_100a:
 
     python -m bit_quantized_shampoo_b200.build [--force] [-v]
+
+and beside it _act8.so, the Python binding of the 8-bit activation calls
+(g++, against this interpreter and its torch).
 """
 from __future__ import annotations
 
@@ -18,6 +21,7 @@ LIB = os.path.join(PKG, "libshampoo4.so")
 
 SOURCES = ["quant4.cu", "gemm_simt.cu", "gemm_tc.cu", "kernels_misc.cu", "graft.cu", "shampoo4.cu", "noalloc.cu",
            "act8.cu", "act8_grad.cu", "act8_gemm.cu"]
+BINDING = os.path.join(PKG, "_act8.so")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo", "-std=c++17",
          "-Xcompiler", "-fPIC", "-I" + INCLUDE, "-I" + CSRC]
@@ -60,7 +64,25 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if force or jobs or _stale(LIB, objs):
         run([NVCC, "-gencode", "arch=compute_100a,code=sm_100a", "-shared", "-o", LIB, *objs,
              "-lcudart_static", "-lrt", "-ldl", "-lpthread"])
+    src = os.path.join(CSRC, "act8_binding.cpp")
+    if force or _stale(BINDING, [src, os.path.join(INCLUDE, "shampoo4.h")]):
+        run(_binding_command(src))
     return LIB
+
+
+def _binding_command(src):
+    """The g++ command of the binding.  Its C entry points come from
+    libshampoo4.so beside it, the rest from the torch that loads it."""
+    import sysconfig
+    import torch
+    base = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(NVCC))
+    flags = ["-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
+    inc = [INCLUDE, sysconfig.get_paths()["include"], os.path.join(base, "include"),
+           os.path.join(base, "include", "torch", "csrc", "api", "include"), os.path.join(cuda, "include")]
+    return [os.environ.get("CXX", "g++"), *flags, *[f"-I{i}" for i in inc], src, "-o", BINDING,
+            f"-L{PKG}", "-l:libshampoo4.so", "-Wl,-rpath,$ORIGIN", f"-L{os.path.join(base, 'lib')}",
+            "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
 
 
 if __name__ == "__main__":
