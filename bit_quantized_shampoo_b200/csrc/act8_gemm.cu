@@ -505,6 +505,19 @@ __global__ void __launch_bounds__(kSmallThreads, 2) k_act8_small(const __grid_co
   const int shares = gridDim.y, share = blockIdx.y;           // the cluster lies along y
   const int kb0 = int(int64_t(g.kblocks) * share / shares), kb1 = int(int64_t(g.kblocks) * (share + 1) / shares);
   const int m0 = int(blockIdx.x % unsigned(g.tiles_m)) * kLanes, r0 = int(blockIdx.x / unsigned(g.tiles_m)) * C::R;
+  auto load_a = [&](int it, int s) {
+    mbar_expect_tx(&full_bar[s], C::kStage);
+    load_tile<C, C::A_MN, kLanes>(&g.a, m0, (kb0 + it) * C::kK, 0, smem_u32(smem + s * C::kStage),
+                                  smem_u32(&full_bar[s]));
+  };
+  auto load_b = [&](int it, int s) {
+#pragma unroll
+    for (int d = 0; d < C::ND; ++d)
+      load_tile<C, false, C::R>(&g.b, r0, (kb0 + it) * C::kK, d,
+                                smem_u32(smem + s * C::kStage) + C::kATile + d * C::R * kRowBytes,
+                                smem_u32(&full_bar[s]));
+  };
+  const int n = kb1 - kb0, lead = min(n, C::STAGES);
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::STAGES; ++s) {
       mbar_init(&full_bar[s], 1);
@@ -512,6 +525,8 @@ __global__ void __launch_bounds__(kSmallThreads, 2) k_act8_small(const __grid_co
     }
     mbar_init(&done_bar, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    for (int it = 0; it < lead; ++it) load_a(it, it);       // under the tensor memory allocation
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&g.b)) : "memory");
   }
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_slot)),
@@ -526,28 +541,14 @@ __global__ void __launch_bounds__(kSmallThreads, 2) k_act8_small(const __grid_co
   if (warp == 0) {
     if (lane == 0) {                                        // ---- loads
       bool ok = true;
-      int it = 0;
-      auto load_a = [&](int s) {
-        mbar_expect_tx(&full_bar[s], C::kStage);
-        load_tile<C, C::A_MN, kLanes>(&g.a, m0, (kb0 + it) * C::kK, 0, smem_u32(smem + s * C::kStage),
-                                      smem_u32(&full_bar[s]));
-      };
-      auto load_b = [&](int s) {
-#pragma unroll
-        for (int d = 0; d < C::ND; ++d)
-          load_tile<C, false, C::R>(&g.b, r0, (kb0 + it) * C::kK, d,
-                                    smem_u32(smem + s * C::kStage) + C::kATile + d * C::R * kRowBytes,
-                                    smem_u32(&full_bar[s]));
-      };
-      const int n = kb1 - kb0, lead = min(n, C::STAGES);
-      for (it = 0; it < lead; ++it) load_a(it);
       wait_previous();
-      for (it = 0; it < lead; ++it) load_b(it);
+      int it = 0;
+      for (; it < lead; ++it) load_b(it, it);
       for (; it < n; ++it) {
         const int s = it % C::STAGES;
         if (!mbar_wait(&empty_bar[s], ((it / C::STAGES) & 1) ^ 1)) { ok = false; break; }
-        load_a(s);
-        load_b(s);
+        load_a(it, s);
+        load_b(it, s);
       }
       for (int i = max(0, it - C::STAGES); i < it; ++i)     // everything loaded has landed before the CTA leaves
         if (!mbar_wait(&full_bar[i % C::STAGES], (i / C::STAGES) & 1)) ok = false;
@@ -622,7 +623,7 @@ __global__ void __launch_bounds__(kSmallThreads, 2) k_act8_small(const __grid_co
     __syncthreads();
     cluster_sync();
     if (warp >= 2) {
-      const int per = C::R / shares, j_end = min((share + 1) * per, g.R - r0);
+      const int per = (C::R + shares - 1) / shares, j_end = min(min((share + 1) * per, C::R), g.R - r0);
       const uint32_t base = smem_u32(part) + uint32_t(lane) * 16u;
       const int m = m0 + 4 * lane;
 #pragma unroll 4
@@ -793,7 +794,7 @@ shampoo4_status launch_small(const Act8Operand& a, const Act8Operand& b, int64_t
 // fitted to measurements on a B200 (1 to 1024 rows, 768 to 11008 columns,
 // 6 to 86 k-blocks; within 15% of most).  The pairs cost 7.5 and, per wave of
 // tiles, 0.36 per k-block or the results' stores; a small tile 4.5 (and 0.01
-// per row) and 0.29 per k-block, up to 1.4 times that when two CTAs share an
+// per row) and 0.27 per k-block, up to 1.4 times that when two CTAs share an
 // SM; joining a split contraction 1.5 and 0.09 per row and digit a CTA
 // finishes; each further wave starts anew.
 struct Form { int rows, shares; };                          // rows 0: the pairs
@@ -803,13 +804,13 @@ Form choose_form(int64_t M, int64_t R, int64_t K, int pair_rows, int digits, con
   double best = 7.5 + std::max(0.36 * kb, 1.6) * std::ceil(pair_tiles / 74);
   Form f{0, 1};
   for (int i = 0; i < n; ++i)
-    for (int s = 1; s <= 8 && s <= std::max(kb, 1.0); s *= 2) {
+    for (int s = 1; s <= 8 && s <= std::max(kb, 1.0); ++s) {
       const int rows = tile_rows[i];
       const double ctas = double((M + 127) / 128) * double((R + rows - 1) / rows) * s;
-      const double waves = std::ceil(ctas / 296), share = ctas <= 148 ? 1.0 : (rows * digits <= 64 ? 1.1 : 1.4);
+      const double waves = std::ceil(ctas / 296), share = ctas <= 148 ? 1.0 : (rows * digits <= 64 ? 1.0 : 1.4);
       const double cost = 1.5 + waves * (3.0 + 0.01 * rows * digits +
-                                         share * (0.29 * std::ceil(kb / s) +
-                                                  (s > 1 ? 1.5 + 0.09 * digits * rows / s : 0.0)));
+                                         share * (0.27 * std::ceil(kb / s) +
+                                                  (s > 1 ? 1.5 + 0.09 * digits * std::ceil(double(rows) / s) : 0.0)));
       if (cost < best) best = cost, f = Form{rows, s};
     }
   return f;

@@ -8,8 +8,8 @@
 //
 //  digits  One scale per row of codes.  F = dY * scale in fp32 becomes fixed
 //          point relative to its largest magnitude over the contraction,
-//          q = rint(F * Q / max|F|), Q = 127 (65536 + 256 + 1), in three
-//          signed base-256 digits; the codes stay as they are stored.  Three
+//          q = rint(F * Q / max|F|), Q just below 127 (65536 + 256 + 1), in
+//          three signed base-256 digits; the codes stay as they are stored.  Three
 //          int8 products with exact int32 sums: the only error is q's
 //          rounding (half of max|F| / 2^23 per element) and a few fp32
 //          roundings at the end.  1.5 times a bfloat16 product's tensor-core
@@ -30,7 +30,9 @@ namespace cg = cooperative_groups;
 namespace s4 {
 namespace {
 
-constexpr float kQMax = 8355711.0f;                    // 127 * 65536 + 127 * 256 + 127
+// A little below 127 * 65536 + 127 * 256 + 127 = 8355711, the largest number
+// of three digits: no rounding of F * inv passes it.
+constexpr float kQMax = 8355704.0f;
 constexpr float kTiny = 0x1p-100f;                     // below it the fixed point stays that of kTiny
 
 // Fixed point of a row whose largest magnitude has these bits: the factor to
@@ -43,10 +45,10 @@ struct Fixed {
     inv = finite ? __fdiv_rn(kQMax, a) : 0.0f;
     scale = finite ? __fdiv_rn(a, kQMax) : __uint_as_float(0x7fc00000u);
   }
-  // The three digits as the low bytes, least significant first.
+  // The three digits as the low bytes, least significant first (a NaN, from
+  // inv = 0 and an infinity, converts to 0).
   __device__ __forceinline__ uint32_t digits(float f) const {
-    const int q = inv == 0.0f ? 0 : __float2int_rn(fminf(fmaxf(f * inv, -kQMax), kQMax));
-    return uint32_t(q + 0x808080) ^ 0x808080u;
+    return uint32_t(__float2int_rn(f * inv) + 0x808080) ^ 0x808080u;
   }
 };
 
@@ -98,7 +100,7 @@ k_act8_digit_rows(Mat dy, const float* __restrict__ scale, int8_t* digits, int64
 // columns of a tile.
 constexpr int kColTile = 64, kTokTile = 128, kColCluster = 8;
 template <class T>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 4)
 k_act8_digit_columns(Mat dy, const float* __restrict__ scale, int8_t* digits, int64_t ld, float* row_scale,
                      int64_t tokens, int64_t cols) {
   let_next_start();

@@ -10,7 +10,7 @@ eps / 2 relative to the value: fp32 2^-24, fp16 2^-11, bf16 2^-8):
    tensor core adds 16 products at a time to an fp32 accumulator with
    truncation, at most 2^-22 of S per addition;
    one scale per row: F = dy * scale rounds to fp32 (2^-24) and to fixed
-   point, off by half of max|F| / 8355711 (and by a rounding 2^-24 max|F| of
+   point, off by half of max|F| / 8355704 (and by a rounding 2^-24 max|F| of
    the factor and of the product) per code; the integer sums are exact, and
    joining and scaling them takes 6 fp32 roundings (2^-24 each);
    groups: value and dy are exact to 2^-24 each as bfloat16 parts, what the
@@ -266,7 +266,7 @@ def grad_tolerance(dy, codes, scales, group, dtype, result, weight):
         F = a * (s if weight else s.T)
         top = F.max(axis=0 if weight else 1, initial=0.0).reshape(-1, 1) if F.size else np.zeros((S.shape[0], 1))
         count = np.abs(codes.astype(np.float64)).sum(axis=0, keepdims=True)
-        return top * count * (0.5 / 8355711 + 2 * 2.0 ** -24) + S * 7 * 2.0 ** -24
+        return top * count * (0.5 / 8355704 + 2 * 2.0 ** -24) + S * 7 * 2.0 ** -24
     kinds = {"bf16": 3, "fp16": 5, "fp32": 6}[dtype]
     return S * (5 * 2.0 ** -24 + kinds * 17 * 2.0 ** -22 + (K // 256 + 1) * 2.0 ** -24)
 
