@@ -2,7 +2,8 @@
 
 PyTorch provides the device memory (state, workspace, outputs) and the CUDA
 stream; every arithmetic step runs in libshampoo4.so.  Tensors must be CUDA
-float32 (gradients, outputs) or uint8 (codes).
+float32 (gradients, outputs) or uint8 (codes); the 8-bit activation calls
+(act8_*) also take bfloat16 and float16 matrices and int8 codes.
 """
 from __future__ import annotations
 
@@ -90,6 +91,27 @@ class Shampoo4:
     def update_stats(self, grads, stream=None):
         p, ld = self._ptrs(grads, "grads")
         L.call("shampoo4_update_stats", self._h, p, ld, _stream(stream))
+
+    def weight_grads(self, dys, inputs, group=0, grads=None, accumulate=False, stream=None):
+        """The fp32 gradients of this handle's parameters, as update_stats
+        takes them, from 8-bit checkpoints of the layers' inputs: parameter p
+        of shape (out, inner) gets dys[p]^T X_p, dys[p] (tokens x out, fp32,
+        bf16 or fp16) the gradient of its layer's output and inputs[p] =
+        (codes, scales) the layer input as act8_pack or act8_linear stored it.
+        ``grads`` (fp32, given or allocated) are overwritten, or added to with
+        ``accumulate`` (micro-batches).  Returns the list of gradients."""
+        if len(dys) != len(self.shapes) or len(inputs) != len(self.shapes):
+            raise ValueError(f"expected {len(self.shapes)} dys and inputs")
+        if grads is None:
+            if accumulate:
+                raise ValueError("accumulate needs grads")
+            grads = [torch.empty(s, dtype=torch.float32, device=self.device) for s in self.shapes]
+        self._ptrs(grads, "grads")
+        for (r, c), dy, (codes, scales), g in zip(self.shapes, dys, inputs, grads):
+            if dy.dim() != 2 or codes.dim() != 2 or dy.shape[1] != r or codes.shape[1] != c:
+                raise ValueError(f"dy and codes must be tokens x {r} and tokens x {c}")
+            act8_weight_grad(dy, codes, scales, group=group, out=g, accumulate=accumulate, stream=stream)
+        return grads
 
     def refresh_roots(self, stream=None):
         L.call("shampoo4_refresh_roots", self._h, _stream(stream))

@@ -496,6 +496,29 @@ def test_layer_gradients_feed_the_optimizer_step():
     assert sh.status_flags() & ~L.FLAG_QR_FALLBACK == 0 and all(torch.isfinite(o).all() for o in out)
 
 
+def test_weight_grads_of_a_handle():
+    """The handle's gradients: those of the calls one by one, micro-batches
+    added up, and refusals."""
+    api = _api()
+    shapes = [(130, 70), (64, 200)]
+    sh = api.Shampoo4(shapes)
+    dys = [data(50, r, "bf16", 200 + r, scale=0.01) for r, _ in shapes]
+    xs = [stored(50, c, 201 + c)[0] for _, c in shapes]
+    grads = sh.weight_grads(dys, xs)
+    for g, d, k in zip(grads, dys, xs):
+        assert torch.equal(g, api.act8_weight_grad(d, *k))
+    twice = sh.weight_grads(dys, xs, grads=[g.clone() for g in grads], accumulate=True)
+    for a, b in zip(twice, grads):
+        assert torch.equal(a, 2 * b)               # g + g rounds to nothing
+    sh.update_stats(grads)
+    assert sh.status_flags() == 0
+    for f in (lambda: sh.weight_grads(dys[:1], xs), lambda: sh.weight_grads(dys, xs[::-1]),
+              lambda: sh.weight_grads(dys, xs, accumulate=True), lambda: sh.weight_grads(dys[::-1], xs),
+              lambda: sh.weight_grads(dys, xs, grads=[g.t() for g in grads]), lambda: sh.weight_grads(dys, xs, group=32)):
+        with pytest.raises((TypeError, ValueError)):
+            f()
+
+
 def test_other_stream_and_graph_replay_match():
     api = _api()
     x, ws, dy = _layer_inputs(dtype="bf16")
