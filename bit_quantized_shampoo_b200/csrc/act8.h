@@ -27,6 +27,7 @@ struct Act8Out {
   const float* row_scale;                              // of R, optional
   const float* col_scale;                              // of M, optional
   const float* bias;                                   // of M, optional
+  const float* factor;                                 // one number, optional, where col_scale is not given
 };
 
 // All products: Y[r, m] = row_scale[r] col_scale[m] sum_k B[r, k] A[m, k] + bias[m].
@@ -41,11 +42,12 @@ shampoo4_status launch_act8_codes(const Act8Operand& a, const Act8Operand& b, in
 // significant first: B = 65536 d0 + 256 d1 + d2.
 shampoo4_status launch_act8_digits(const Act8Operand& a, const Act8Operand& b, int64_t M, int64_t R, int64_t K,
                                    const Act8Out& out, uint32_t* flags, cudaStream_t st);
-// bfloat16 both: a is K x M in a_parts planes (A = their sum), b is R x K
-// (b_mn = 0) or K x R (b_mn = 1) in b_parts planes.  The products of parts i
-// and j with i + j < max(a_parts, b_parts) are taken.
-shampoo4_status launch_act8_bf16(const Act8Operand& a, int a_parts, const Act8Operand& b, int b_parts, int b_mn,
-                                 int64_t M, int64_t R, int64_t K, const Act8Out& out, uint32_t* flags,
-                                 cudaStream_t st);
+// bfloat16 both: a is K x M, b is R x K (b_mn = 0) or K x R (b_mn = 1).
+shampoo4_status launch_act8_bf16(const Act8Operand& a, const Act8Operand& b, int b_mn, int64_t M, int64_t R, int64_t K,
+                                 const Act8Out& out, uint32_t* flags, cudaStream_t st);
+// Halves both, operands the sums of their planes: a is K x M in two, b is
+// K x R in b_parts (1 or 2).  The product of the second planes is left out.
+shampoo4_status launch_act8_halves(const Act8Operand& a, const Act8Operand& b, int b_parts, int64_t M, int64_t R,
+                                   int64_t K, const Act8Out& out, uint32_t* flags, cudaStream_t st);
 
 }  // namespace s4

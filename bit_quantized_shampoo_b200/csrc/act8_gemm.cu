@@ -8,9 +8,9 @@
 //                               the gradient in three signed base-256 digits
 //                               of fixed point: three int8 products with
 //                               exact int32 sums, joined in the epilogue
-//   the same in bfloat16        A = the codes' values in one to three
-//                               bfloat16 parts, B = the gradient in one to
-//                               three (kind::f16, fp32 sums)
+//   the same in 16 bits         A = the codes' values, B = the gradient, each
+//                               as one bfloat16 or as one or two scaled
+//                               halves (kind::f16, fp32 sums)
 //
 // A pair of CTAs (cta_group::2) owns a tile of 256 columns m by R rows: each
 // CTA stages its 128 columns of A and half of the rows of B, and the leader's
@@ -40,27 +40,32 @@
 namespace s4 {
 namespace {
 
-enum { kI8 = 0, kBf16 = 1 };
+enum { kI8 = 0, kBf16 = 1, kHalf = 2 };
 constexpr int kLanes = 128;               // columns m per CTA: the TMEM lanes
 constexpr int kPairThreads = 320, kSmallThreads = 192;
 constexpr int kRowBytes = 128;            // bytes of a swizzle atom row
 
 // KIND; A_MN/B_MN: the operand's row index (not k) is contiguous; R: rows of
-// a tile; PA, PB: bfloat16 parts; ND: digit planes of B (stacked along N);
-// CG: CTAs per tile; CHUNK: k-blocks per accumulation into registers (0: the
+// a tile; PA, PB: 16-bit parts; ND: digit planes of B (stacked along N);
+// CG: CTAs per tile; SUB: k-blocks per stage; CHUNK: stages per accumulation into registers (0: the
 // whole sum in tensor memory).
-template <int KIND_, bool A_MN_, bool B_MN_, int R_, int PA_, int PB_, int ND_, int CG_, int STAGES_, int CHUNK_>
+template <int KIND_, bool A_MN_, bool B_MN_, int R_, int PA_, int PB_, int ND_, int CG_, int SUB_, int STAGES_,
+          int CHUNK_>
 struct Cfg {
-  static constexpr int KIND = KIND_, R = R_, PA = PA_, PB = PB_, ND = ND_, CG = CG_, STAGES = STAGES_, CHUNK = CHUNK_;
+  static constexpr int KIND = KIND_, R = R_, PA = PA_, PB = PB_, ND = ND_, CG = CG_, SUB = SUB_, STAGES = STAGES_,
+                       CHUNK = CHUNK_;
   static constexpr bool A_MN = A_MN_, B_MN = B_MN_;
-  static constexpr int kK = KIND == kI8 ? 128 : 64;            // k per stage
+  static constexpr int kK = KIND == kI8 ? 128 : 64;            // k of a block: a swizzle atom's row
   static constexpr int kN = ND * R;                            // MMA N
   static constexpr int kBRows = R / CG;                        // rows of each digit plane a CTA stages
   static constexpr int kATile = kLanes * kRowBytes;
   static constexpr int kBTile = ND * kBRows * kRowBytes;
-  static constexpr int kStage = PA * kATile + PB * kBTile;
+  static constexpr int kAPart = A_MN ? kK * kRowBytes : kATile;        // from one part to the next
+  static constexpr int kBPart = B_MN ? kK * kRowBytes : kBTile;
+  static constexpr int kBlock = PA * kATile + PB * kBTile;
+  static constexpr int kStage = SUB * kBlock;
   static constexpr int kSmem = STAGES * kStage + 1024;
-  // with several parts the products of lower parts (2^-8 of the first and
+  // with several parts the products of lower parts (2^-11 of the first and
   // less) have columns of their own: the tensor core truncates each addition
   // at the accumulator's magnitude
   static constexpr bool kSmallApart = PA > 1 || PB > 1;
@@ -69,8 +74,8 @@ struct Cfg {
   static constexpr int kTmemCols = 2 * kAccCols;
   static_assert(kSmem <= 227 * 1024, "stages fit in shared memory");
   static_assert(R % 64 == 0 && kN <= 256 && kN % 32 == 0 && kBRows % 8 == 0 && kBTile % 1024 == 0, "tile shape");
-  static_assert(KIND == kBf16 || (PA == 1 && PB == 1 && !B_MN), "integer operands");
-  static_assert(KIND == kI8 || (ND == 1 && A_MN), "bfloat16 operands");
+  static_assert(KIND != kI8 || (PA == 1 && PB == 1 && !B_MN), "integer operands");
+  static_assert(KIND == kI8 || (ND == 1 && A_MN), "16-bit operands");
 };
 
 struct GemmArgs {
@@ -80,12 +85,11 @@ struct GemmArgs {
   Act8Out out;
 };
 
-// Instruction descriptor: fp32 sums of bfloat16 (type code 1, accumulator
-// code 1) or int32 sums of signed 8-bit integers (type code 1, accumulator
-// code 2).
+// Instruction descriptor: fp32 sums (accumulator code 1) of half (type code 0)
+// or bfloat16 (1), or int32 sums (code 2) of signed 8-bit integers (1).
 template <class C>
 __host__ __device__ constexpr uint32_t idesc() {
-  return ((C::KIND == kI8 ? 2u : 1u) << 4) | (1u << 7) | (1u << 10) | (uint32_t(C::A_MN) << 15) |
+  return ((C::KIND == kI8 ? 2u : 1u) << 4) | ((C::KIND == kHalf ? 0u : 1u) * ((1u << 7) | (1u << 10))) | (uint32_t(C::A_MN) << 15) |
          (uint32_t(C::B_MN) << 16) | (uint32_t(C::kN >> 3) << 17) | (uint32_t((C::CG * kLanes) >> 4) << 24);
 }
 
@@ -135,6 +139,14 @@ __device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap* map, i
         "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
         ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(plane), "r"(bar) : "memory");
 }
+// Whether the barrier's phase is complete, without waiting for it.
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity) : "memory");
+  return ok != 0;
+}
 // Arrive on the barrier (of every CTA of the pair) once the MMAs issued so far are done.
 template <int CG>
 __device__ __forceinline__ void commit(uint64_t* bar) {
@@ -147,26 +159,37 @@ __device__ __forceinline__ void commit(uint64_t* bar) {
 }
 
 // K-major (128-byte swizzle): rows of 128 B, 8-row groups 1024 B apart; an
-// MMA's k (32 bytes) lies along the row.  MN-major: boxes of 128 bytes of
-// rows by kK k's, one box per 128 bytes of rows; 8-k groups 1024 B apart,
-// an MMA's k is 32 (int8) or 16 (bfloat16) box rows.
-template <class C, bool MN>
-__device__ __forceinline__ uint64_t tile_desc(uint32_t base, int kk) {
-  constexpr int kStep = C::KIND == kI8 ? 4096 : 2048;
-  return MN ? smem_desc(base + kk * kStep, C::kK * kRowBytes, 1024, 2) : smem_desc(base + kk * 32, 16, 1024, 2);
+// MMA's k (32 bytes) lies along the row; the planes of a box follow one
+// another.  MN-major: boxes of 128 bytes of rows by kK k's by all planes, one
+// box per 128 bytes of rows; 8-k groups 1024 B apart, an MMA's k is 32 (int8)
+// or 16 (16-bit) box rows.  addr: the tile's shared address / 16 (below 2^14,
+// so offsets add without a carry); only the low word depends on it.
+template <class C, bool MN, int PLANES>
+__device__ __forceinline__ uint64_t tile_desc(uint32_t addr, int kk) {
+  constexpr uint32_t kStep = MN ? (C::KIND == kI8 ? 4096 : 2048) : 32, kLead = MN ? PLANES * C::kK * kRowBytes : 16;
+  constexpr uint32_t hi = (1024u >> 4) | (1u << 14) | (2u << 29);   // group stride, version, 128-byte swizzle
+  const uint32_t lo = (addr + uint32_t(kk) * (kStep >> 4)) | ((kLead >> 4) << 16);
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo), "r"(hi));
+  return d;
+}
+// One lane of a converged warp.
+__device__ __forceinline__ bool elected() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
 }
 
-// Rows mn0 .. mn0 + rows - 1 by k0 .. k0 + kK - 1 of one operand plane.
-template <class C, bool MN, int ROWS>
-__device__ __forceinline__ void load_tile(const CUtensorMap* map, int mn0, int k0, int plane, uint32_t dst,
-                                          uint32_t bar) {
+// Rows mn0 .. mn0 + rows - 1 by k0 .. k0 + kK - 1 of every plane of an operand.
+template <class C, bool MN, int ROWS, int PLANES>
+__device__ __forceinline__ void load_tile(const CUtensorMap* map, int mn0, int k0, uint32_t dst, uint32_t bar) {
   if (!MN) {
-    load_box<C::CG>(dst, map, k0, mn0, plane, bar);
+    load_box<C::CG>(dst, map, k0, mn0, 0, bar);
   } else {
     constexpr int kWide = C::KIND == kI8 ? 128 : 64;                // elements of 128 bytes
 #pragma unroll
     for (int g = 0; g < (ROWS + kWide - 1) / kWide; ++g)
-      load_box<C::CG>(dst + g * C::kK * kRowBytes, map, mn0 + kWide * g, k0, plane, bar);
+      load_box<C::CG>(dst + g * PLANES * C::kK * kRowBytes, map, mn0 + kWide * g, k0, 0, bar);
   }
 }
 
@@ -292,82 +315,123 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_act8_gemm(const __grid_cons
   const int chunk = C::CHUNK ? C::CHUNK : max(kblocks, 1);
 
   if (warp == 0) {
-    if (lane == 0) {                                        // ---- loads
-      int it = 0;
-      bool ok = true;
-      wait_previous();
-      for (int t = first; ok && t < tiles; t += step) {
-        int tm, tr;
-        tile_of(g, t, tm, tr);
-        const int m0 = (tm * C::CG + int(rank)) * kLanes, r0 = tr * C::R + int(rank) * C::kBRows;
-        for (int kb = 0; kb < kblocks; ++kb, ++it) {
-          const int s = it % C::STAGES;
-          if (!mbar_wait(&empty_bar[s], ((it / C::STAGES) & 1) ^ 1)) { ok = false; break; }
-          uint32_t dst = smem_u32(smem + s * C::kStage);
-          uint32_t bar = smem_u32(&full_bar[s]);
+    // ---- loads (the whole warp walks the loop, one lane issues)
+    const uint32_t base = smem_u32(smem);
+    int s = 0, filled = 0;
+    uint32_t phase = 1;                                     // of the stage's release before this fill
+    bool ok = true, ready = false;
+    wait_previous();
+    for (int t = first; ok && t < tiles; t += step) {
+      int tm, tr;
+      tile_of(g, t, tm, tr);
+      const int m0 = (tm * C::CG + int(rank)) * kLanes, r0 = tr * C::R + int(rank) * C::kBRows;
+      for (int kb = 0; kb < kblocks; ++kb) {
+        if (!__all_sync(0xffffffffu, ready)) {
+          ok = __all_sync(0xffffffffu, mbar_wait(&empty_bar[s], phase));
+          if (!ok) break;
+        }
+        if (elected()) {
+          uint32_t bar = smem_u32(&full_bar[s]), dst = base + uint32_t(s) * C::kStage;
           if (rank == 0) mbar_expect_tx(&full_bar[s], C::CG * C::kStage);
           if (C::CG == 2) bar = in_cta(bar, 0);
-          const int k0 = kb * C::kK;
 #pragma unroll
-          for (int p = 0; p < C::PA; ++p, dst += C::kATile)
-            load_tile<C, C::A_MN, kLanes>(&g.a, m0, k0, p, dst, bar);
-#pragma unroll
-          for (int p = 0; p < C::PB * C::ND; ++p, dst += C::kBRows * kRowBytes)
-            load_tile<C, C::B_MN, C::kBRows>(&g.b, r0, k0, p, dst, bar);
+          for (int sub = 0; sub < C::SUB; ++sub, dst += C::kBlock) {          // past the last column: zeros
+            const int k0 = (kb * C::SUB + sub) * C::kK;
+            load_tile<C, C::A_MN, kLanes, C::PA>(&g.a, m0, k0, dst, bar);
+            load_tile<C, C::B_MN, C::kBRows, C::PB * C::ND>(&g.b, r0, k0, dst + C::PA * C::kATile, bar);
+          }
         }
+        __syncwarp();
+        filled = min(filled + 1, C::STAGES);
+        if (++s == C::STAGES) {
+          s = 0;
+          phase ^= 1u;
+        }
+        ready = mbar_test(&empty_bar[s], phase);
       }
-      // every stage this CTA filled has been read before it leaves
-      for (int i = max(0, it - C::STAGES); i < it; ++i)
-        if (!mbar_wait(&empty_bar[i % C::STAGES], (i / C::STAGES) & 1)) { ok = false; break; }
-      if (!ok && g.flags) atomicOr(g.flags, SHAMPOO4_FLAG_TIMEOUT);
     }
+    // every stage this CTA filled has been read before it leaves
+    for (; filled > 0 && ok; --filled) {
+      int last = s - filled;
+      uint32_t ph = phase;
+      if (last < 0) {
+        last += C::STAGES;
+        ph ^= 1u;
+      }
+      ok = mbar_wait(&empty_bar[last], ph ^ 1u);
+    }
+    if (!ok && lane == 0 && g.flags) atomicOr(g.flags, SHAMPOO4_FLAG_TIMEOUT);
   } else if (warp == 1) {
-    if (lane == 0 && rank == 0) {                           // ---- products
+    // ---- products.  The whole warp walks the loop, so that descriptors stay
+    // in uniform registers, and one lane issues; the next stage's barrier is
+    // tried under the MMAs just issued.  (With the loop inside one lane's
+    // branch the issue, about 600 clocks a stage, was the bound: 266 against
+    // ZZ us at 8192 x 11008 x 4096.)
+    if (rank == 0) {
       constexpr uint32_t id = idesc<C>();
       constexpr int kParts = C::PA > C::PB ? C::PA : C::PB;
-      int it = 0, i = 0;
-      bool ok = true;
+      const uint32_t base = smem_u32(smem) >> 4;
+      int s = 0, i = 0;
+      uint32_t phase = 0;
+      bool ok = true, ready = false;                        // ready: the next stage's loads have landed already
       for (int t = first; ok && t < tiles; t += step) {
         for (int kb = 0; ok && (kb < kblocks || kb == 0); ++i) {
           const int ab = i & 1;
-          if (!mbar_wait(&acc_empty[ab], ((i >> 1) & 1) ^ 1)) { ok = false; break; }
+          ok = __all_sync(0xffffffffu, mbar_wait(&acc_empty[ab], ((i >> 1) & 1) ^ 1));
+          if (!ok) break;
           fence_after_sync();
           const uint32_t d = tmem + uint32_t(ab * C::kAccCols);
           const int k_end = min(kb + chunk, kblocks);
           const int k_first = kb;
-          for (; kb < k_end; ++kb, ++it) {
-            const int s = it % C::STAGES;
-            if (!mbar_wait(&full_bar[s], (it / C::STAGES) & 1)) { ok = false; break; }
+          for (; kb < k_end; ++kb) {
+            if (!__all_sync(0xffffffffu, ready)) {
+              ok = __all_sync(0xffffffffu, mbar_wait(&full_bar[s], phase));
+              if (!ok) break;
+            }
             fence_after_sync();
-            const uint32_t a0 = smem_u32(smem + s * C::kStage), b0 = a0 + C::PA * C::kATile;
+            const uint32_t a0 = base + uint32_t(s) * (C::kStage >> 4), b0 = a0 + ((C::PA * C::kATile) >> 4);
+            if (elected()) {
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
+              for (int sk = 0; sk < 4 * C::SUB; ++sk)
 #pragma unroll
-              for (int pa = 0; pa < C::PA; ++pa)
+                for (int pa = 0; pa < C::PA; ++pa)
 #pragma unroll
-                for (int pb = 0; pb < C::PB; ++pb)
-                  if (pa + pb < kParts) {
-                    // the first product into each of the two sums overwrites it
-                    const bool opens = pa + pb == 0 || (C::PB > 1 ? pa == 0 && pb == 1 : pa == 1);
-                    mma<C::KIND, C::CG>(d + (pa + pb > 0 ? C::kN : 0),
-                                        tile_desc<C, C::A_MN>(a0 + pa * C::kATile, kk),
-                                        tile_desc<C, C::B_MN>(b0 + pb * C::kBTile, kk), id,
-                                        !(opens && kb == k_first && kk == 0));
-                  }
-            commit<C::CG>(&empty_bar[s]);
+                  for (int pb = 0; pb < C::PB; ++pb)
+                    if (pa + pb < kParts) {
+                      // the first product into each of the two sums overwrites it
+                      const bool opens = pa + pb == 0 || (C::PB > 1 ? pa == 0 && pb == 1 : pa == 1);
+                      const uint32_t block = uint32_t(sk / 4 * C::kBlock) >> 4;
+                      mma<C::KIND, C::CG>(d + (pa + pb > 0 ? C::kN : 0),
+                                          tile_desc<C, C::A_MN, C::PA>(a0 + block + ((pa * C::kAPart) >> 4), sk % 4),
+                                          tile_desc<C, C::B_MN, C::PB>(b0 + block + ((pb * C::kBPart) >> 4), sk % 4),
+                                          id,
+                                          !(opens && kb == k_first && sk == 0));
+                    }
+              commit<C::CG>(&empty_bar[s]);
+            }
+            __syncwarp();
+            if (++s == C::STAGES) {
+              s = 0;
+              phase ^= 1u;
+            }
+            ready = mbar_test(&full_bar[s], phase);         // under the MMAs just issued
           }
-          if (ok) commit<C::CG>(&acc_full[ab]);
+          if (ok && elected()) commit<C::CG>(&acc_full[ab]);
+          __syncwarp();
           if (kblocks == 0) { ++i; break; }
         }
       }
       // all MMAs issued are finished before tensor memory is freed
-      if (C::CG == 2)
-        asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-            smem_u32(&done_bar)) : "memory");
-      else
-        mma_commit(&done_bar);
+      if (elected()) {
+        if (C::CG == 2)
+          asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+              smem_u32(&done_bar)) : "memory");
+        else
+          mma_commit(&done_bar);
+      }
+      __syncwarp();
       if (!mbar_wait(&done_bar, 0)) ok = false;
-      if (!ok && g.flags) atomicOr(g.flags, SHAMPOO4_FLAG_TIMEOUT);
+      if (!ok && lane == 0 && g.flags) atomicOr(g.flags, SHAMPOO4_FLAG_TIMEOUT);
     }
   } else {                                                  // ---- epilogue, warps 2..9
     const int q = warp & 3;                                 // TMEM lane quarter
@@ -376,11 +440,12 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_act8_gemm(const __grid_cons
     int i = 0;
     bool ok = true;
     wait_previous();
+    const float factor = g.out.factor ? __ldg(g.out.factor) : 1.0f;
     for (int t = first; ok && t < tiles; t += step) {
       int tm, tr;
       tile_of(g, t, tm, tr);
       const int m = (tm * C::CG + int(rank)) * kLanes + 32 * q + lane, r0 = tr * C::R + 32 * c0;
-      const float cs = g.out.col_scale && m < g.M ? __ldg(g.out.col_scale + m) : 1.0f;
+      const float cs = g.out.col_scale && m < g.M ? __ldg(g.out.col_scale + m) : factor;
       const float bias = g.out.bias && m < g.M ? __ldg(g.out.bias + m) : 0.0f;
       float rs[kChunks];                                    // fetched under the products
 #pragma unroll
@@ -480,7 +545,7 @@ __device__ __forceinline__ void store_row4(const Act8Out& o, int r, int m, int M
 // so the split changes no result).  Same roles as above, warps 2..5 finish.
 template <bool A_MN_, int R_, int ND_, int STAGES_>
 struct SmallCfg {
-  static constexpr int KIND = kI8, R = R_, ND = ND_, CG = 1, STAGES = STAGES_;
+  static constexpr int KIND = kI8, R = R_, ND = ND_, CG = 1, SUB = 1, STAGES = STAGES_;
   static constexpr bool A_MN = A_MN_, B_MN = false;
   static constexpr int kK = 128, kN = ND * R, kBRows = R;
   static constexpr int kATile = kLanes * kRowBytes;
@@ -507,15 +572,12 @@ __global__ void __launch_bounds__(kSmallThreads, 2) k_act8_small(const __grid_co
   const int m0 = int(blockIdx.x % unsigned(g.tiles_m)) * kLanes, r0 = int(blockIdx.x / unsigned(g.tiles_m)) * C::R;
   auto load_a = [&](int it, int s) {
     mbar_expect_tx(&full_bar[s], C::kStage);
-    load_tile<C, C::A_MN, kLanes>(&g.a, m0, (kb0 + it) * C::kK, 0, smem_u32(smem + s * C::kStage),
-                                  smem_u32(&full_bar[s]));
+    load_tile<C, C::A_MN, kLanes, 1>(&g.a, m0, (kb0 + it) * C::kK, smem_u32(smem + s * C::kStage),
+                                     smem_u32(&full_bar[s]));
   };
   auto load_b = [&](int it, int s) {
-#pragma unroll
-    for (int d = 0; d < C::ND; ++d)
-      load_tile<C, false, C::R>(&g.b, r0, (kb0 + it) * C::kK, d,
-                                smem_u32(smem + s * C::kStage) + C::kATile + d * C::R * kRowBytes,
-                                smem_u32(&full_bar[s]));
+    load_tile<C, false, C::R, C::ND>(&g.b, r0, (kb0 + it) * C::kK, smem_u32(smem + s * C::kStage) + C::kATile,
+                                     smem_u32(&full_bar[s]));
   };
   const int n = kb1 - kb0, lead = min(n, C::STAGES);
   if (threadIdx.x == 0) {
@@ -554,25 +616,29 @@ __global__ void __launch_bounds__(kSmallThreads, 2) k_act8_small(const __grid_co
         if (!mbar_wait(&full_bar[i % C::STAGES], (i / C::STAGES) & 1)) ok = false;
       if (!ok && g.flags) atomicOr(g.flags, SHAMPOO4_FLAG_TIMEOUT);
     }
-  } else if (warp == 1) {
-    if (lane == 0) {                                        // ---- products
-      constexpr uint32_t id = (2u << 4) | (1u << 7) | (1u << 10) | (uint32_t(C::A_MN) << 15) |
-                              (uint32_t(C::kN >> 3) << 17) | (uint32_t(kLanes >> 4) << 24);
-      bool ok = true;
-      for (int it = 0; it < kb1 - kb0; ++it) {
-        const int s = it % C::STAGES;
-        if (!mbar_wait(&full_bar[s], (it / C::STAGES) & 1)) { ok = false; break; }
-        fence_after_sync();
-        const uint32_t a0 = smem_u32(smem + s * C::kStage), b0 = a0 + C::kATile;
+  } else if (warp == 1) {                                   // ---- products (the whole warp, as above)
+    constexpr uint32_t id = (2u << 4) | (1u << 7) | (1u << 10) | (uint32_t(C::A_MN) << 15) |
+                            (uint32_t(C::kN >> 3) << 17) | (uint32_t(kLanes >> 4) << 24);
+    const uint32_t base = smem_u32(smem) >> 4;
+    bool ok = true;
+    for (int it = 0; it < kb1 - kb0; ++it) {
+      const int s = it % C::STAGES;
+      ok = __all_sync(0xffffffffu, mbar_wait(&full_bar[s], (it / C::STAGES) & 1));
+      if (!ok) break;
+      fence_after_sync();
+      const uint32_t a0 = base + uint32_t(s) * (C::kStage >> 4), b0 = a0 + (C::kATile >> 4);
+      if (elected()) {
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)
-          mma<kI8, 1>(tmem, tile_desc<C, C::A_MN>(a0, kk), tile_desc<C, false>(b0, kk), id, (it | kk) != 0);
+          mma<kI8, 1>(tmem, tile_desc<C, C::A_MN, 1>(a0, kk), tile_desc<C, false, 1>(b0, kk), id, (it | kk) != 0);
         mma_commit(&empty_bar[s]);
       }
-      mma_commit(&done_bar);
-      if (!mbar_wait(&done_bar, 0)) ok = false;
-      if (!ok && g.flags) atomicOr(g.flags, SHAMPOO4_FLAG_TIMEOUT);
+      __syncwarp();
     }
+    if (elected()) mma_commit(&done_bar);
+    __syncwarp();
+    if (!mbar_wait(&done_bar, 0)) ok = false;
+    if (!ok && lane == 0 && g.flags) atomicOr(g.flags, SHAMPOO4_FLAG_TIMEOUT);
   }
   // Every load has landed and every MMA is done (or timed out).
   __syncthreads();
@@ -681,7 +747,8 @@ PFN_cuTensorMapEncodeTiled_v12000 encoder() {
 }
 
 // Tensor map of an operand's planes (rows x cols each, row-major), box of
-// 128 bytes of a row by box_rows, 128-byte swizzle, zeros outside a plane.
+// 128 bytes of a row by box_rows by all planes, 128-byte swizzle, zeros
+// outside a plane.
 shampoo4_status encode(CUtensorMap* out, int kind, const Act8Operand& x, int64_t rows, int64_t cols, int planes,
                        int box_rows) {
   auto fn = encoder();
@@ -690,7 +757,7 @@ shampoo4_status encode(CUtensorMap* out, int kind, const Act8Operand& x, int64_t
   if ((x.ld * esize) % 16 != 0 || reinterpret_cast<uintptr_t>(x.p) % 16 != 0) return SHAMPOO4_ERR_INVALID_ARG;
   cuuint64_t dims[3] = {cuuint64_t(cols), cuuint64_t(rows), cuuint64_t(planes)};
   cuuint64_t strides[2] = {cuuint64_t(x.ld * esize), cuuint64_t(planes > 1 ? x.plane * x.ld * esize : x.ld * esize)};
-  cuuint32_t box[3] = {cuuint32_t(128 / esize), cuuint32_t(box_rows), 1u};
+  cuuint32_t box[3] = {cuuint32_t(128 / esize), cuuint32_t(box_rows), cuuint32_t(planes)};
   cuuint32_t estr[3] = {1u, 1u, 1u};
   const CUresult r = fn(out, kind == kI8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
                         const_cast<void*>(x.p), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
@@ -729,7 +796,7 @@ shampoo4_status fill_args(GemmArgs& g, const Act8Operand& a, int a_planes, const
   g.flags = flags;
   g.M = int32_t(M);
   g.R = int32_t(R);
-  g.kblocks = int32_t((K + C::kK - 1) / C::kK);
+  g.kblocks = int32_t((K + C::SUB * C::kK - 1) / (C::SUB * C::kK));             // stages
   if (K > 0) {
     S4_TRY(C::A_MN ? encode(&g.a, C::KIND, a, K, M, a_planes, C::kK) : encode(&g.a, C::KIND, a, M, K, a_planes, kLanes));
     S4_TRY(C::B_MN ? encode(&g.b, C::KIND, b, K, R, b_planes, C::kK)
@@ -818,12 +885,12 @@ Form choose_form(int64_t M, int64_t R, int64_t K, int pair_rows, int digits, con
 
 }  // namespace
 
-//                               kind   A_MN   B_MN   R   PA PB ND CG stages chunk
-using CodesCfg = Cfg<            kI8,   false, false, 256, 1, 1, 1, 2, 6, 0>;
-using DigitsCfg = Cfg<           kI8,   true,  false, 64,  1, 1, kAct8Digits, 2, 7, 1024>;
-template <bool B_MN> using Bf16Cfg = Cfg<kBf16, true, B_MN, 256, 1, 1, 1, 2, 6, 0>;
-template <bool B_MN, int PA, int PB, int STAGES>
-using PartsCfg = Cfg<            kBf16, true,  B_MN,  128, PA, PB, 1, 2, STAGES, 4>;
+//                               kind   A_MN   B_MN   R   PA PB ND CG SUB stages chunk
+using CodesCfg = Cfg<            kI8,   false, false, 256, 1, 1, 1, 2, 1, 6, 0>;
+using DigitsCfg = Cfg<           kI8,   true,  false, 64,  1, 1, kAct8Digits, 2, 2, 4, 512>;
+template <bool B_MN> using Bf16Cfg = Cfg<kBf16, true, B_MN, 256, 1, 1, 1, 2, 1, 6, 0>;
+template <int PB, int STAGES>
+using HalvesCfg = Cfg<           kHalf, true,  true,  128, 2, PB, 1, 2, 1, STAGES, 4>;
 
 shampoo4_status launch_act8_codes(const Act8Operand& a, const Act8Operand& b, int64_t M, int64_t R, int64_t K,
                                   const Act8Out& out, bool after_pass, uint32_t* flags, cudaStream_t st) {
@@ -848,16 +915,16 @@ shampoo4_status launch_act8_digits(const Act8Operand& a, const Act8Operand& b, i
   return launch<DigitsCfg>(a, b, M, R, K, out, true, flags, st);
 }
 
-shampoo4_status launch_act8_bf16(const Act8Operand& a, int a_parts, const Act8Operand& b, int b_parts, int b_mn,
-                                 int64_t M, int64_t R, int64_t K, const Act8Out& out, uint32_t* flags,
-                                 cudaStream_t st) {
-  if (a_parts == 1 && b_parts == 1)
-    return b_mn ? launch<Bf16Cfg<true>>(a, b, M, R, K, out, true, flags, st)
-                : launch<Bf16Cfg<false>>(a, b, M, R, K, out, true, flags, st);
-  if (!b_mn || a_parts != 3) return SHAMPOO4_ERR_INVALID_ARG;    // only the weight gradient splits, its codes always in 3
-  if (b_parts == 1) return launch<PartsCfg<true, 3, 1, 3>>(a, b, M, R, K, out, true, flags, st);
-  if (b_parts == 2) return launch<PartsCfg<true, 3, 2, 3>>(a, b, M, R, K, out, true, flags, st);
-  return launch<PartsCfg<true, 3, 3, 3>>(a, b, M, R, K, out, true, flags, st);
+shampoo4_status launch_act8_bf16(const Act8Operand& a, const Act8Operand& b, int b_mn, int64_t M, int64_t R, int64_t K,
+                                 const Act8Out& out, uint32_t* flags, cudaStream_t st) {
+  return b_mn ? launch<Bf16Cfg<true>>(a, b, M, R, K, out, true, flags, st)
+              : launch<Bf16Cfg<false>>(a, b, M, R, K, out, true, flags, st);
+}
+
+shampoo4_status launch_act8_halves(const Act8Operand& a, const Act8Operand& b, int b_parts, int64_t M, int64_t R,
+                                   int64_t K, const Act8Out& out, uint32_t* flags, cudaStream_t st) {
+  return b_parts == 1 ? launch<HalvesCfg<1, 5>>(a, b, M, R, K, out, true, flags, st)
+                      : launch<HalvesCfg<2, 4>>(a, b, M, R, K, out, true, flags, st);
 }
 
 }  // namespace s4

@@ -17,9 +17,13 @@
 //  bf16    dY and the result bfloat16, and enough rows: the codes' values rounded to one
 //          bfloat16 (2^-8 at most, no more than the result's own rounding),
 //          dY as it is.  One bfloat16 product.
-//  parts   Scales per group of columns (no common factor per row): values and
-//          dY as exact-to-fp32 sums of bfloat16 parts (three for fp32, two
-//          for fp16, one for bfloat16), all products above 2^-24.
+//  halves  Scales per group of columns (no common factor per row): values and
+//          dY scaled by powers of two (their largest to about 2^14) and taken
+//          as a half and a half of what is left, 22 bits and never coarser
+//          than 2^-39 of the largest; a 16-bit dY is one half.  Three products
+//          (two for a 16-bit dY), summed in fp32 outside the tensor core
+//          every 256 k.  (Three bfloat16 parts each, six products, measured
+//          47 us where this takes XX at 1537 x 768 x 2305 fp32.)
 //
 // The operand passes of this file stream; their bound is HBM bandwidth.
 #include <cooperative_groups.h>
@@ -190,34 +194,7 @@ k_act8_digit_columns(Mat dy, const float* __restrict__ scale, int8_t* digits, in
   }
 }
 
-// v in up to three bfloat16 parts: each the nearest to what is left.  The
-// first stays finite when v is (the remainder of an infinite one would be
-// infinite too).
-template <int PARTS>
-__device__ __forceinline__ void split(float v, float (&p)[3]) {
-  constexpr float kMax = 3.38953139e38f;                 // the largest finite bfloat16
-#pragma unroll
-  for (int k = 0; k < PARTS; ++k) {
-    p[k] = __bfloat162float(__float2bfloat16_rn(v));
-    if (k == 0 && PARTS > 1 && fabsf(p[0]) > kMax && fabsf(v) <= 3.402823466e38f) p[0] = copysignf(kMax, v);
-    v -= p[k];
-  }
-}
-template <int PARTS>
-__device__ __forceinline__ void store_parts(const float (&v)[8], __nv_bfloat16* o, int64_t plane, int c, int cols) {
-  float p[PARTS][8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    float s[3];
-    split<PARTS>(v[i], s);
-#pragma unroll
-    for (int k = 0; k < PARTS; ++k) p[k][i] = s[k];
-  }
-#pragma unroll
-  for (int k = 0; k < PARTS; ++k) store8(o + k * plane, c, cols, true, p[k]);
-}
-
-template <int PARTS>
+// The codes' values in bfloat16.
 __global__ void __launch_bounds__(kThreads) k_act8_expand(Ckpt k, __nv_bfloat16* o, int64_t ld, int64_t rows,
                                                           int cols) {
   let_next_start();
@@ -225,16 +202,97 @@ __global__ void __launch_bounds__(kThreads) k_act8_expand(Ckpt k, __nv_bfloat16*
   if (p.row >= rows || p.c >= cols) return;
   uint2 w;
   load_codes8(k.codes + p.row * k.ldc, p.c, cols, w);
-  const float s = __ldg(k.scales + p.row * k.groups + (p.c >> k.shift));
   float v[8];
-  values8(w, s, v);
-  store_parts<PARTS>(v, o + p.row * ld, rows * ld, p.c, cols);
+  values8(w, __ldg(k.scales + p.row * k.groups + (p.c >> k.shift)), v);
+  store8(o + p.row * ld, p.c, cols, 1, v);
+}
+// A bfloat16 dY with rows that are not 16-byte aligned, copied to rows that are.
+__global__ void __launch_bounds__(kThreads) k_act8_align(Mat x, __nv_bfloat16* o, int64_t ld, int64_t rows, int cols) {
+  let_next_start();
+  const Piece<1> p;
+  if (p.row >= rows || p.c >= cols) return;
+  Raw8<__nv_bfloat16> r;
+  load8(static_cast<const __nv_bfloat16*>(x.p) + p.row * x.ld, p.c, cols, x.vec, r);
+  float v[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = elt(r, i);
+  store8(o + p.row * ld, p.c, cols, 1, v);
+}
+
+// ---- halves
+
+// Bits of the largest finite magnitudes, for both operands, zeroed by the
+// caller: [0] of the scales, [1] of dY (elements that are not finite do not
+// count: they stay so whatever the factor).
+struct Largest { uint32_t scale, dy; };
+__device__ __forceinline__ uint32_t finite_bits(float x) {
+  const uint32_t b = abs_bits(x);
+  return b < 0x7f800000u ? b : 0u;
+}
+template <class T>
+__global__ void __launch_bounds__(kThreads) k_act8_largest(Mat dy, const float* __restrict__ scales, int64_t nscales,
+                                                           Largest* out, int64_t rows, int cols) {
+  __shared__ uint32_t slots[kThreads / 32];
+  uint32_t m = 0;
+  for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
+    const T* x = static_cast<const T*>(dy.p) + row * dy.ld;
+    for (int c = int(threadIdx.x) * 8; c < cols; c += kThreads * 8) {
+      Raw8<T> r;
+      load8(x, c, cols, dy.vec, r);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) m = max(m, finite_bits(elt(r, i)));
+    }
+  }
+  m = cta_max(m, slots);
+  if (threadIdx.x == 0) atomicMax(&out->dy, m);
+  uint32_t s = 0;
+  for (int64_t i = int64_t(blockIdx.x) * kThreads + threadIdx.x; i < nscales; i += int64_t(gridDim.x) * kThreads)
+    s = max(s, finite_bits(__ldg(scales + i)));
+  s = cta_max(s, slots);
+  if (threadIdx.x == 0) atomicMax(&out->scale, s);
+}
+
+// 2^e with 2^13 < 2^e x < 2^15 for the x of these bits (1 for zero), within
+// the exponents whose powers and inverses are normal.
+__device__ __forceinline__ float power_to(uint32_t bits) {
+  const int e = bits == 0u ? 0 : min(max(14 + 127 - int(bits >> 23), -126), 126);
+  return __uint_as_float(uint32_t(127 + e) << 23);
+}
+// A value's largest is its scale's 127-fold, 2^7 of it.
+__device__ __forceinline__ float value_power(const Largest* l) { return power_to(l->scale == 0u ? 0u : min(l->scale + (7u << 23), 0x7f000000u)); }
+
+template <int PARTS>
+__device__ __forceinline__ void store_halves(const float (&v)[8], float power, __half* o, int64_t plane, int c,
+                                             int cols) {
+  float hi[8], lo[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float x = v[i] * power;
+    hi[i] = __half2float(__float2half_rn(x));
+    lo[i] = x - hi[i];
+  }
+  store8(o, c, cols, 1, hi);
+  if (PARTS == 2) store8(o + plane, c, cols, 1, lo);
+}
+
+__global__ void __launch_bounds__(kThreads) k_act8_code_halves(Ckpt k, const Largest* largest, __half* o, int64_t ld,
+                                                               int64_t rows, int cols) {
+  const Piece<1> p;
+  if (p.row >= rows || p.c >= cols) return;
+  uint2 w;
+  load_codes8(k.codes + p.row * k.ldc, p.c, cols, w);
+  float v[8];
+  values8(w, __ldg(k.scales + p.row * k.groups + (p.c >> k.shift)), v);
+  store_halves<2>(v, value_power(largest), o + p.row * ld, rows * ld, p.c, cols);
 }
 
 template <class T, int PARTS>
-__global__ void __launch_bounds__(kThreads) k_act8_split(Mat x, __nv_bfloat16* o, int64_t ld, int64_t rows,
-                                                         int cols) {
+__global__ void __launch_bounds__(kThreads) k_act8_dy_halves(Mat x, const Largest* largest, float* factor, __half* o,
+                                                             int64_t ld, int64_t rows, int cols) {
   let_next_start();
+  const float power = power_to(largest->dy);
+  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0 && threadIdx.y == 0)
+    *factor = (1.0f / power) * (1.0f / value_power(largest));
   const Piece<1> p;
   if (p.row >= rows || p.c >= cols) return;
   Raw8<T> r;
@@ -242,12 +300,12 @@ __global__ void __launch_bounds__(kThreads) k_act8_split(Mat x, __nv_bfloat16* o
   float v[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) v[i] = elt(r, i);
-  store_parts<PARTS>(v, o + p.row * ld, rows * ld, p.c, cols);
+  store_halves<PARTS>(v, power, o + p.row * ld, rows * ld, p.c, cols);
 }
 
 // ------------------------------------------------------------------ host
 
-enum GradPath { kDigits, kBf16, kParts };
+enum GradPath { kDigits, kBf16, kHalves };
 // The result is rows x inner.  The bfloat16 path writes the codes out in
 // bfloat16 once (3 bytes a code, 25 us for 45M codes) where digits take half
 // as long again per row of the result (485 us for 8192 rows of the same
@@ -258,13 +316,14 @@ constexpr int64_t kDigitRows = 420;
 GradPath grad_path(int32_t dtype, int32_t result, int32_t group, int64_t rows, int64_t inner) {
   const bool many = rows > kDigitRows && ((rows + 255) / 256) * ((inner + 255) / 256) >= 48;
   if (dtype == ACT8_BF16 && result == ACT8_BF16 && (group != 0 || many)) return kBf16;
-  return group == 0 ? kDigits : kParts;
+  return group == 0 ? kDigits : kHalves;
 }
 
 size_t round_up(size_t n, size_t a) { return (n + a - 1) / a * a; }
 
-// Workspace of a gradient: dY (tokens x out) in the form its product takes,
-// then, but for digits, the codes' values (code_rows x inner) in bfloat16.
+// Workspace of a gradient: scales (digits) or the largest magnitudes and the
+// result's factor (halves), dY (tokens x out) in the form its product takes,
+// then, but for digits, the codes' values (code_rows x inner) in 16 bits.
 struct GradPlan {
   GradPath path;
   int dy_parts, code_parts;
@@ -283,8 +342,9 @@ GradPlan grad_plan(bool weight, int32_t dtype, int32_t result, int32_t group, in
     p.dy_bytes = round_up(size_t(rows) * p.ld_dy * kAct8Digits, 256);
     return p;
   }
-  p.dy_parts = dtype == ACT8_BF16 ? 1 : (dtype == ACT8_FP16 ? 2 : 3);
-  p.code_parts = p.path == kBf16 ? 1 : 3;
+  p.dy_parts = dtype == ACT8_FP32 ? 2 : 1;
+  p.code_parts = p.path == kBf16 ? 1 : 2;
+  p.scale_bytes = p.path == kBf16 ? 0 : 256;
   p.ld_dy = int64_t(round_up(size_t(out), 8));
   p.ld_code = int64_t(round_up(size_t(inner), 8));
   // room for a copy of a bfloat16 dY whatever its alignment turns out to be
@@ -323,30 +383,47 @@ shampoo4_status digit_pass(bool weight, const void* dy, int32_t dtype, int64_t l
   });
 }
 
-shampoo4_status expand(const Ckpt& k, int64_t rows, int64_t cols, int parts, void* o, int64_t ld,
-                       cudaStream_t st) {
+shampoo4_status expand(const Ckpt& k, int64_t rows, int64_t cols, void* o, int64_t ld, cudaStream_t st) {
   const dim3 b = piece_block(cols);
   dim3 g;
   if (!piece_grid(rows, cols, b, 1, &g)) return SHAMPOO4_ERR_INVALID_ARG;
-  __nv_bfloat16* p = static_cast<__nv_bfloat16*>(o);
-  if (parts == 1) k_act8_expand<1><<<g, b, 0, st>>>(k, p, ld, rows, int(cols));
-  else k_act8_expand<3><<<g, b, 0, st>>>(k, p, ld, rows, int(cols));
+  k_act8_expand<<<g, b, 0, st>>>(k, static_cast<__nv_bfloat16*>(o), ld, rows, int(cols));
   S4_CUDA(cudaGetLastError());
   return SHAMPOO4_OK;
 }
 
-shampoo4_status split_dy(const void* x, int32_t dtype, int64_t ldx, int64_t rows, int64_t cols, void* o, int64_t ld,
+shampoo4_status align_dy(const void* x, int64_t ldx, int64_t rows, int64_t cols, void* o, int64_t ld,
                          cudaStream_t st) {
   const dim3 b = piece_block(cols);
   dim3 g;
   if (!piece_grid(rows, cols, b, 1, &g)) return SHAMPOO4_ERR_INVALID_ARG;
-  const Mat m = mat(x, ldx, dtype);
-  __nv_bfloat16* p = static_cast<__nv_bfloat16*>(o);
-  if (dtype == ACT8_BF16) k_act8_split<__nv_bfloat16, 1><<<g, b, 0, st>>>(m, p, ld, rows, int(cols));
-  else if (dtype == ACT8_FP16) k_act8_split<__half, 2><<<g, b, 0, st>>>(m, p, ld, rows, int(cols));
-  else k_act8_split<float, 3><<<g, b, 0, st>>>(m, p, ld, rows, int(cols));
+  k_act8_align<<<g, b, 0, st>>>(mat(x, ldx, ACT8_BF16), static_cast<__nv_bfloat16*>(o), ld, rows, int(cols));
   S4_CUDA(cudaGetLastError());
   return SHAMPOO4_OK;
+}
+
+// Both operands as halves at dyp and cp; the result's factor next to the
+// largest magnitudes at `largest`.
+shampoo4_status halves_pass(const void* dy, int32_t dtype, int64_t lddy, const Ckpt& k, int64_t tokens, int64_t out,
+                            int64_t inner, Largest* largest, float* factor, void* dyp, int64_t ld_dy, void* cp,
+                            int64_t ld_code, cudaStream_t st) {
+  const Mat m = mat(dy, lddy, dtype);
+  const dim3 bd = piece_block(out), bc = piece_block(inner);
+  dim3 gd, gc;
+  if (!piece_grid(tokens, out, bd, 1, &gd) || !piece_grid(tokens, inner, bc, 1, &gc)) return SHAMPOO4_ERR_INVALID_ARG;
+  S4_CUDA(cudaMemsetAsync(largest, 0, sizeof(Largest), st));
+  return by_dtype(dtype, [&](auto* tag) -> shampoo4_status {
+    using T = std::remove_pointer_t<decltype(tag)>;
+    k_act8_largest<T><<<unsigned(std::min<int64_t>(tokens, 148 * 4)), kThreads, 0, st>>>(
+        m, k.scales, tokens * k.groups, largest, tokens, int(out));
+    S4_CUDA(cudaGetLastError());
+    k_act8_code_halves<<<gc, bc, 0, st>>>(k, largest, static_cast<__half*>(cp), ld_code, tokens, int(inner));
+    S4_CUDA(cudaGetLastError());
+    k_act8_dy_halves<T, sizeof(T) == 4 ? 2 : 1><<<gd, bd, 0, st>>>(m, largest, factor, static_cast<__half*>(dyp), ld_dy,
+                                                                  tokens, int(out));
+    S4_CUDA(cudaGetLastError());
+    return SHAMPOO4_OK;
+  });
 }
 
 // Both gradients: weight: Y[out, inner] = dY^T X; else Y[tokens, inner] = dY W.
@@ -356,7 +433,7 @@ shampoo4_status grad(bool weight, const void* dy, int32_t dtype, int64_t lddy, c
   const int64_t K = weight ? tokens : out, R = weight ? out : tokens;
   if (K == 0 && o.accumulate) return SHAMPOO4_OK;
   const GradPlan p = grad_plan(weight, dtype, o.dtype, group, tokens, out, inner);
-  if (K == 0) return launch_act8_bf16(Act8Operand{}, 1, Act8Operand{}, 1, 0, inner, R, 0, o, flags, st);
+  if (K == 0) return launch_act8_bf16(Act8Operand{}, Act8Operand{}, 0, inner, R, 0, o, flags, st);
   if (!ws || !aligned(ws, 256)) return SHAMPOO4_ERR_INVALID_ARG;
   if (ws_bytes < p.total()) return SHAMPOO4_ERR_WORKSPACE;
   char* w = static_cast<char*>(ws);
@@ -368,14 +445,22 @@ shampoo4_status grad(bool weight, const void* dy, int32_t dtype, int64_t lddy, c
     return launch_act8_digits(Act8Operand{k.codes, k.ldc, 0}, Act8Operand{digits, p.ld_dy, R}, inner, R, K, o, flags,
                               st);
   }
-  Act8Operand b{dy, lddy, 0};
-  if (dtype != ACT8_BF16 || !row_aligned(dy, lddy, dtype)) {
-    b = Act8Operand{w, p.ld_dy, tokens};
-    S4_TRY(split_dy(dy, dtype, lddy, tokens, out, w, p.ld_dy, st));
+  char *dyp = w + p.scale_bytes, *cp = dyp + p.dy_bytes;
+  if (p.path == kHalves) {                                  // groups: only the weight gradient has them
+    Largest* largest = reinterpret_cast<Largest*>(w);
+    float* factor = reinterpret_cast<float*>(largest + 1);
+    S4_TRY(halves_pass(dy, dtype, lddy, k, tokens, out, inner, largest, factor, dyp, p.ld_dy, cp, p.ld_code, st));
+    o.factor = factor;
+    return launch_act8_halves(Act8Operand{cp, p.ld_code, K}, Act8Operand{dyp, p.ld_dy, tokens}, p.dy_parts, inner, R,
+                              K, o, flags, st);
   }
-  const Act8Operand a{w + p.dy_bytes, p.ld_code, K};
-  S4_TRY(expand(k, K, inner, p.code_parts, w + p.dy_bytes, p.ld_code, st));
-  return launch_act8_bf16(a, p.code_parts, b, p.dy_parts, weight ? 1 : 0, inner, R, K, o, flags, st);
+  Act8Operand b{dy, lddy, 0};
+  if (!row_aligned(dy, lddy, dtype)) {
+    b = Act8Operand{dyp, p.ld_dy, 0};
+    S4_TRY(align_dy(dy, lddy, tokens, out, dyp, p.ld_dy, st));
+  }
+  S4_TRY(expand(k, K, inner, cp, p.ld_code, st));
+  return launch_act8_bf16(Act8Operand{cp, p.ld_code, 0}, b, weight ? 1 : 0, inner, R, K, o, flags, st);
 }
 
 }  // namespace
@@ -404,7 +489,7 @@ static shampoo4_status grad_call(bool weight, const void* d_dy, int32_t dtype, i
   if (!mat_ok(d_y, result, M, inner, ldy) || !aligned(d_flags, 4)) return SHAMPOO4_ERR_INVALID_ARG;
   if (K > 0 && (!mat_ok(d_dy, dtype, tokens, out, lddy) || !codes_ok(codes, ldc, inner, scales)))
     return SHAMPOO4_ERR_INVALID_ARG;
-  const Act8Out o{d_y, ldy, result, accumulate ? 1 : 0, nullptr, nullptr, nullptr};
+  const Act8Out o{d_y, ldy, result, accumulate ? 1 : 0, nullptr, nullptr, nullptr, nullptr};
   return grad(weight, d_dy, dtype, lddy, ckpt(codes, ldc, scales, inner, group), group,
               tokens, out, inner, o, d_ws, ws_bytes, d_flags, reinterpret_cast<cudaStream_t>(stream));
 }

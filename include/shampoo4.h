@@ -570,12 +570,18 @@ shampoo4_status act8_linear(const void* d_x, int32_t xdtype, int64_t ldx, const 
  *   act8_input_grad   dX[t, i] = sum_o dY[t, o] w[o, i],  w = value of wc
  *                     (one scale per row)
  * accumulate != 0 adds the product to the result's contents (in fp32,
- * rounded once).  Arithmetic: tensor-core products of bfloat16 with fp32
- * sums.  A bfloat16 dY enters exactly, fp16 as an exact sum of two bfloat16,
- * fp32 as such a sum to 2^-16.  The code values enter as a sum of two
- * bfloat16, to 2^-16; when both dY and the result are bfloat16 they are
- * rounded to one (off by 2^-8 at most).  A non-finite element of dY, or a
- * non-finite scale, makes every result it enters non-finite.
+ * rounded once).  Arithmetic, by the types and scales (xf: a code's value):
+ *   one scale per row   dY * scale in fp32, then fixed point: 24 bits below
+ *                       its largest magnitude over the contraction; exact
+ *                       integer products and sums with the codes.
+ *   scales per group    dY and xf to 22 bits, and no finer than 2^-39 of the
+ *                       largest in the whole tensor; fp32 sums.
+ *   dY and the result bfloat16, with scales per group or more than 420 rows
+ *                       and at least 48 tiles of 256 x 256 in the result:
+ *                       xf rounded to bfloat16 (off by 2^-8 at most), dY as
+ *                       it is; fp32 sums.
+ * A non-finite element of dY, or a non-finite scale, makes every result it
+ * enters non-finite.
  * d_workspace: act8_grad_workspace bytes, 256-byte aligned (weight != 0 for
  * act8_weight_grad), scratch of the one call; SHAMPOO4_ERR_WORKSPACE when
  * smaller. */

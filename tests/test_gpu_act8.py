@@ -13,10 +13,10 @@ eps / 2 relative to the value: fp32 2^-24, fp16 2^-11, bf16 2^-8):
    point, off by half of max|F| / 8355704 (and by a rounding 2^-24 max|F| of
    the factor and of the product) per code; the integer sums are exact, and
    joining and scaling them takes 6 fp32 roundings (2^-24 each);
-   groups: value and dy are exact to 2^-24 each as bfloat16 parts, what the
-   omitted products add is below 3 * 2^-24, and of K / 16 additions per
-   product kind at most 16 are in one accumulator; its sum is then added in
-   fp32, once per 256 k.
+   groups: value and dy as two halves are off by 2^-22 each and by 2^-39 of
+   the tensor's largest, the omitted product of the lower halves is at most
+   2^-22; of K / 16 additions per product kind at most 16 are in one
+   accumulator; its sum is then added in fp32, once per 256 k.
 """
 import numpy as np
 import pytest
@@ -267,8 +267,10 @@ def grad_tolerance(dy, codes, scales, group, dtype, result, weight):
         top = F.max(axis=0 if weight else 1, initial=0.0).reshape(-1, 1) if F.size else np.zeros((S.shape[0], 1))
         count = np.abs(codes.astype(np.float64)).sum(axis=0, keepdims=True)
         return top * count * (0.5 / 8355704 + 2 * 2.0 ** -24) + S * 7 * 2.0 ** -24
-    kinds = {"bf16": 3, "fp16": 5, "fp32": 6}[dtype]
-    return S * (5 * 2.0 ** -24 + kinds * 17 * 2.0 ** -22 + (K // 256 + 1) * 2.0 ** -24)
+    kinds = 3 if dtype == "fp32" else 2
+    floor = 2.0 ** -39 * (a.max(initial=0.0) * (b.sum(axis=0, keepdims=True) if weight else b.max(initial=0.0) * K)
+                          + b.max(initial=0.0) * a.sum(axis=0).reshape(-1, 1))
+    return S * (4 * 2.0 ** -22 + kinds * 17 * 2.0 ** -22 + (K // 256 + 1) * 2.0 ** -24) + floor
 
 
 SHAPES = [(1, 1, 1), (1, 64, 300), (2, 7, 17), (63, 130, 65), (64, 128, 256), (65, 256, 257), (200, 129, 520),
