@@ -47,13 +47,11 @@ constexpr int kRowBytes = 128;            // bytes of a swizzle atom row
 
 // KIND; A_MN/B_MN: the operand's row index (not k) is contiguous; R: rows of
 // a tile; PA, PB: 16-bit parts; ND: digit planes of B (stacked along N);
-// CG: CTAs per tile; SUB: k-blocks per stage; CHUNK: stages per accumulation into registers (0: the
+// CG: CTAs per tile; CHUNK: k-blocks per accumulation into registers (0: the
 // whole sum in tensor memory).
-template <int KIND_, bool A_MN_, bool B_MN_, int R_, int PA_, int PB_, int ND_, int CG_, int SUB_, int STAGES_,
-          int CHUNK_>
+template <int KIND_, bool A_MN_, bool B_MN_, int R_, int PA_, int PB_, int ND_, int CG_, int STAGES_, int CHUNK_>
 struct Cfg {
-  static constexpr int KIND = KIND_, R = R_, PA = PA_, PB = PB_, ND = ND_, CG = CG_, SUB = SUB_, STAGES = STAGES_,
-                       CHUNK = CHUNK_;
+  static constexpr int KIND = KIND_, R = R_, PA = PA_, PB = PB_, ND = ND_, CG = CG_, STAGES = STAGES_, CHUNK = CHUNK_;
   static constexpr bool A_MN = A_MN_, B_MN = B_MN_;
   static constexpr int kK = KIND == kI8 ? 128 : 64;            // k of a block: a swizzle atom's row
   static constexpr int kN = ND * R;                            // MMA N
@@ -62,8 +60,7 @@ struct Cfg {
   static constexpr int kBTile = ND * kBRows * kRowBytes;
   static constexpr int kAPart = A_MN ? kK * kRowBytes : kATile;        // from one part to the next
   static constexpr int kBPart = B_MN ? kK * kRowBytes : kBTile;
-  static constexpr int kBlock = PA * kATile + PB * kBTile;
-  static constexpr int kStage = SUB * kBlock;
+  static constexpr int kStage = PA * kATile + PB * kBTile;
   static constexpr int kSmem = STAGES * kStage + 1024;
   // with several parts the products of lower parts (2^-11 of the first and
   // less) have columns of their own: the tensor core truncates each addition
@@ -315,7 +312,10 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_act8_gemm(const __grid_cons
   const int chunk = C::CHUNK ? C::CHUNK : max(kblocks, 1);
 
   if (warp == 0) {
-    // ---- loads (the whole warp walks the loop, one lane issues)
+    // ---- loads.  The whole warp walks the loop and one lane issues, a box over
+    // all planes of an operand: four boxes a k-block from one lane's branch
+    // took longer to issue than the digits' products take (903 against 755 us
+    // for the weight gradient of 8192 x 4096 x 11008).
     const uint32_t base = smem_u32(smem);
     int s = 0, filled = 0;
     uint32_t phase = 1;                                     // of the stage's release before this fill
@@ -331,15 +331,12 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_act8_gemm(const __grid_cons
           if (!ok) break;
         }
         if (elected()) {
-          uint32_t bar = smem_u32(&full_bar[s]), dst = base + uint32_t(s) * C::kStage;
+          const uint32_t dst = base + uint32_t(s) * C::kStage;
+          uint32_t bar = smem_u32(&full_bar[s]);
           if (rank == 0) mbar_expect_tx(&full_bar[s], C::CG * C::kStage);
           if (C::CG == 2) bar = in_cta(bar, 0);
-#pragma unroll
-          for (int sub = 0; sub < C::SUB; ++sub, dst += C::kBlock) {          // past the last column: zeros
-            const int k0 = (kb * C::SUB + sub) * C::kK;
-            load_tile<C, C::A_MN, kLanes, C::PA>(&g.a, m0, k0, dst, bar);
-            load_tile<C, C::B_MN, C::kBRows, C::PB * C::ND>(&g.b, r0, k0, dst + C::PA * C::kATile, bar);
-          }
+          load_tile<C, C::A_MN, kLanes, C::PA>(&g.a, m0, kb * C::kK, dst, bar);
+          load_tile<C, C::B_MN, C::kBRows, C::PB * C::ND>(&g.b, r0, kb * C::kK, dst + C::PA * C::kATile, bar);
         }
         __syncwarp();
         filled = min(filled + 1, C::STAGES);
@@ -365,8 +362,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_act8_gemm(const __grid_cons
     // ---- products.  The whole warp walks the loop, so that descriptors stay
     // in uniform registers, and one lane issues; the next stage's barrier is
     // tried under the MMAs just issued.  (With the loop inside one lane's
-    // branch the issue, about 600 clocks a stage, was the bound: 266 against
-    // ZZ us at 8192 x 11008 x 4096.)
+    // branch the issue, about 600 clocks a k-block, was the bound: 266 against
+    // 234 us at 8192 x 11008 x 4096.)
     if (rank == 0) {
       constexpr uint32_t id = idesc<C>();
       constexpr int kParts = C::PA > C::PB ? C::PA : C::PB;
@@ -392,7 +389,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_act8_gemm(const __grid_cons
             const uint32_t a0 = base + uint32_t(s) * (C::kStage >> 4), b0 = a0 + ((C::PA * C::kATile) >> 4);
             if (elected()) {
 #pragma unroll
-              for (int sk = 0; sk < 4 * C::SUB; ++sk)
+              for (int kk = 0; kk < 4; ++kk)
 #pragma unroll
                 for (int pa = 0; pa < C::PA; ++pa)
 #pragma unroll
@@ -400,12 +397,11 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_act8_gemm(const __grid_cons
                     if (pa + pb < kParts) {
                       // the first product into each of the two sums overwrites it
                       const bool opens = pa + pb == 0 || (C::PB > 1 ? pa == 0 && pb == 1 : pa == 1);
-                      const uint32_t block = uint32_t(sk / 4 * C::kBlock) >> 4;
                       mma<C::KIND, C::CG>(d + (pa + pb > 0 ? C::kN : 0),
-                                          tile_desc<C, C::A_MN, C::PA>(a0 + block + ((pa * C::kAPart) >> 4), sk % 4),
-                                          tile_desc<C, C::B_MN, C::PB>(b0 + block + ((pb * C::kBPart) >> 4), sk % 4),
+                                          tile_desc<C, C::A_MN, C::PA>(a0 + ((pa * C::kAPart) >> 4), kk),
+                                          tile_desc<C, C::B_MN, C::PB>(b0 + ((pb * C::kBPart) >> 4), kk),
                                           id,
-                                          !(opens && kb == k_first && sk == 0));
+                                          !(opens && kb == k_first && kk == 0));
                     }
               commit<C::CG>(&empty_bar[s]);
             }
@@ -545,7 +541,7 @@ __device__ __forceinline__ void store_row4(const Act8Out& o, int r, int m, int M
 // so the split changes no result).  Same roles as above, warps 2..5 finish.
 template <bool A_MN_, int R_, int ND_, int STAGES_>
 struct SmallCfg {
-  static constexpr int KIND = kI8, R = R_, ND = ND_, CG = 1, SUB = 1, STAGES = STAGES_;
+  static constexpr int KIND = kI8, R = R_, ND = ND_, CG = 1, STAGES = STAGES_;
   static constexpr bool A_MN = A_MN_, B_MN = false;
   static constexpr int kK = 128, kN = ND * R, kBRows = R;
   static constexpr int kATile = kLanes * kRowBytes;
@@ -796,7 +792,7 @@ shampoo4_status fill_args(GemmArgs& g, const Act8Operand& a, int a_planes, const
   g.flags = flags;
   g.M = int32_t(M);
   g.R = int32_t(R);
-  g.kblocks = int32_t((K + C::SUB * C::kK - 1) / (C::SUB * C::kK));             // stages
+  g.kblocks = int32_t((K + C::kK - 1) / C::kK);
   if (K > 0) {
     S4_TRY(C::A_MN ? encode(&g.a, C::KIND, a, K, M, a_planes, C::kK) : encode(&g.a, C::KIND, a, M, K, a_planes, kLanes));
     S4_TRY(C::B_MN ? encode(&g.b, C::KIND, b, K, R, b_planes, C::kK)
@@ -858,26 +854,26 @@ shampoo4_status launch_small(const Act8Operand& a, const Act8Operand& b, int64_t
 }
 
 // Which form an integer product takes: the estimated time (us) of each,
-// fitted to measurements on a B200 (1 to 1024 rows, 768 to 11008 columns,
-// 6 to 86 k-blocks; within 15% of most).  The pairs cost 7.5 and, per wave of
-// tiles, 0.36 per k-block or the results' stores; a small tile 4.5 (and 0.01
-// per row) and 0.27 per k-block, up to 1.4 times that when two CTAs share an
-// SM; joining a split contraction 1.5 and 0.09 per row and digit a CTA
-// finishes; each further wave starts anew.
+// fitted to measurements on a B200 (1 to 2048 rows, 768 to 11008 columns, 6 to
+// 86 k-blocks; within 15% of most).  The pairs: 8.3 and, per wave of tiles,
+// 0.31 (digits 0.25) per k-block or the results' stores.  A small tile of n =
+// rows x digits columns: 4.9 + 0.004 n, and 0.15 + 0.0006 n per k-block, half
+// as much again or more when two CTAs share an SM; joining a split contraction
+// 1 and 0.07 per row and digit a CTA finishes; each further wave starts anew.
 struct Form { int rows, shares; };                          // rows 0: the pairs
-Form choose_form(int64_t M, int64_t R, int64_t K, int pair_rows, int digits, const int* tile_rows, int n) {
+Form choose_form(int64_t M, int64_t R, int64_t K, int pair_rows, int digits, const int* tile_rows, int forms) {
   const double kb = double((K + 127) / 128);
   const double pair_tiles = double((M + 255) / 256) * double((R + pair_rows - 1) / pair_rows);
-  double best = 7.5 + std::max(0.36 * kb, 1.6) * std::ceil(pair_tiles / 74);
+  double best = 8.3 + std::max((digits == 1 ? 0.31 : 0.25) * kb, 1.6) * std::ceil(pair_tiles / 74);
   Form f{0, 1};
-  for (int i = 0; i < n; ++i)
+  for (int i = 0; i < forms; ++i)
     for (int s = 1; s <= 8 && s <= std::max(kb, 1.0); ++s) {
       const int rows = tile_rows[i];
       const double ctas = double((M + 127) / 128) * double((R + rows - 1) / rows) * s;
-      const double waves = std::ceil(ctas / 296), share = ctas <= 148 ? 1.0 : (rows * digits <= 64 ? 1.0 : 1.4);
-      const double cost = 1.5 + waves * (3.0 + 0.01 * rows * digits +
-                                         share * (0.27 * std::ceil(kb / s) +
-                                                  (s > 1 ? 1.5 + 0.09 * digits * std::ceil(double(rows) / s) : 0.0)));
+      const double n = double(rows) * digits, waves = std::ceil(ctas / 296);
+      const double share = ctas <= 148 ? 1.0 : 1.45 + 0.0025 * n;
+      const double join = s > 1 ? 1.0 + 0.07 * std::ceil(n / s) : 0.0;
+      const double cost = 1.9 + waves * (3.0 + 0.004 * n + share * (0.15 + 0.0006 * n) * std::ceil(kb / s) + join);
       if (cost < best) best = cost, f = Form{rows, s};
     }
   return f;
@@ -885,12 +881,12 @@ Form choose_form(int64_t M, int64_t R, int64_t K, int pair_rows, int digits, con
 
 }  // namespace
 
-//                               kind   A_MN   B_MN   R   PA PB ND CG SUB stages chunk
-using CodesCfg = Cfg<            kI8,   false, false, 256, 1, 1, 1, 2, 1, 6, 0>;
-using DigitsCfg = Cfg<           kI8,   true,  false, 64,  1, 1, kAct8Digits, 2, 2, 4, 512>;
-template <bool B_MN> using Bf16Cfg = Cfg<kBf16, true, B_MN, 256, 1, 1, 1, 2, 1, 6, 0>;
+//                               kind   A_MN   B_MN   R   PA PB ND CG stages chunk
+using CodesCfg = Cfg<            kI8,   false, false, 256, 1, 1, 1, 2, 7, 0>;
+using DigitsCfg = Cfg<           kI8,   true,  false, 64,  1, 1, kAct8Digits, 2, 8, 1024>;
+template <bool B_MN> using Bf16Cfg = Cfg<kBf16, true, B_MN, 256, 1, 1, 1, 2, 7, 0>;
 template <int PB, int STAGES>
-using HalvesCfg = Cfg<           kHalf, true,  true,  128, 2, PB, 1, 2, 1, STAGES, 4>;
+using HalvesCfg = Cfg<           kHalf, true,  true,  128, 2, PB, 1, 2, STAGES, 4>;
 
 shampoo4_status launch_act8_codes(const Act8Operand& a, const Act8Operand& b, int64_t M, int64_t R, int64_t K,
                                   const Act8Out& out, bool after_pass, uint32_t* flags, cudaStream_t st) {

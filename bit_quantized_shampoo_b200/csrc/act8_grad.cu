@@ -23,7 +23,7 @@
 //          than 2^-39 of the largest; a 16-bit dY is one half.  Three products
 //          (two for a 16-bit dY), summed in fp32 outside the tensor core
 //          every 256 k.  (Three bfloat16 parts each, six products, measured
-//          47 us where this takes XX at 1537 x 768 x 2305 fp32.)
+//          47 us where this takes 32 at 1537 x 768 x 2305 fp32.)
 //
 // The operand passes of this file stream; their bound is HBM bandwidth.
 #include <cooperative_groups.h>
@@ -307,12 +307,12 @@ __global__ void __launch_bounds__(kThreads) k_act8_dy_halves(Mat x, const Larges
 
 enum GradPath { kDigits, kBf16, kHalves };
 // The result is rows x inner.  The bfloat16 path writes the codes out in
-// bfloat16 once (3 bytes a code, 25 us for 45M codes) where digits take half
-// as long again per row of the result (485 us for 8192 rows of the same
-// codes): even at about 420 rows.  It also has one form only, pairs of CTAs on
+// bfloat16 once (3 bytes a code, 26 us for 45M codes) where digits take half
+// as long again per row of the result (335 us for 8192 rows of the same
+// codes): even at about 640 rows.  It also has one form only, pairs of CTAs on
 // 256 x 256 tiles, so it wants tiles for most of them (512 x 768 and 2304 of
-// contraction: 20 against 16 us; 1024 x 4096: 40 against 61).
-constexpr int64_t kDigitRows = 420;
+// contraction: 20 against 16 us; 1024 x 4096: 37 against 44).
+constexpr int64_t kDigitRows = 640;
 GradPath grad_path(int32_t dtype, int32_t result, int32_t group, int64_t rows, int64_t inner) {
   const bool many = rows > kDigitRows && ((rows + 255) / 256) * ((inner + 255) / 256) >= 48;
   if (dtype == ACT8_BF16 && result == ACT8_BF16 && (group != 0 || many)) return kBf16;

@@ -576,7 +576,7 @@ shampoo4_status act8_linear(const void* d_x, int32_t xdtype, int64_t ldx, const 
  *                       integer products and sums with the codes.
  *   scales per group    dY and xf to 22 bits, and no finer than 2^-39 of the
  *                       largest in the whole tensor; fp32 sums.
- *   dY and the result bfloat16, with scales per group or more than 420 rows
+ *   dY and the result bfloat16, with scales per group or more than 640 rows
  *                       and at least 48 tiles of 256 x 256 in the result:
  *                       xf rounded to bfloat16 (off by 2^-8 at most), dY as
  *                       it is; fp32 sums.

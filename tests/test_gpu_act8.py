@@ -259,7 +259,7 @@ def grad_tolerance(dy, codes, scales, group, dtype, result, weight):
     S = (a.T if weight else a) @ b
     # bfloat16 with one scale per row and few result tiles goes through fixed point
     tiles = -(-S.shape[0] // 256) * -(-S.shape[1] // 256)
-    if dtype == "bf16" and result == "bf16" and (group or (S.shape[0] > 420 and tiles >= 48)):
+    if dtype == "bf16" and result == "bf16" and (group or (S.shape[0] > 640 and tiles >= 48)):
         return S * (1.01 * 2.0 ** -8 + (-(-K // 16) + 1) * 2.0 ** -22)
     if group == 0:
         s = scales.astype(np.float64)
