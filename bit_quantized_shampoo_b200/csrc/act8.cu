@@ -36,9 +36,11 @@ constexpr float kScaleMax = 8454659.0f * 0x1p98f;      // the largest s with 127
 
 // ---- the code rule
 
-__device__ __forceinline__ float rcp_approx(float x) {  // within 1 ulp where the result is normal
+// Within 1 ulp where x and the result are normal, else 0 or infinity (the form
+// that keeps subnormals takes several instructions more).
+__device__ __forceinline__ float rcp_approx(float x) {
   float r;
-  asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
 
@@ -172,9 +174,8 @@ __global__ void __launch_bounds__(kThreads) k_act8_pack_groups(Mat x, Ckpt o, in
 // One scale for the row.  WARP: a warp per row (up to 1024 columns); else a
 // CTA per row.  IT > 0: a thread's at most IT pieces of 8 columns stay in
 // registers between the maximum and the codes; IT = 0: the row is read twice.
-constexpr int kRowThreads = 768;                         // two such CTAs per SM: 42 registers
 template <class T, int IT, bool WARP>
-__global__ void __launch_bounds__(kRowThreads, 2) k_act8_pack_rows(Mat x, Ckpt o, int64_t rows, int cols) {
+__global__ void __launch_bounds__(512, 2) k_act8_pack_rows(Mat x, Ckpt o, int64_t rows, int cols) {
   __shared__ uint32_t slots[32];
   let_next_start();
   const int64_t row = WARP ? int64_t(blockIdx.x) * blockDim.y + threadIdx.y : int64_t(blockIdx.x);
@@ -244,7 +245,7 @@ template <class T>
 __device__ __forceinline__ float sigmoid(float x) {
   if (sizeof(T) == 4) return rcp_approx(1.0f + expf(-x));
   float e;
-  asm("ex2.approx.f32 %0, %1;" : "=f"(e) : "f"(x * -1.4426950408889634f));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * -1.4426950408889634f));
   return rcp_approx(1.0f + e);
 }
 
@@ -378,18 +379,24 @@ shampoo4_status pack(const void* x, int32_t dtype, int64_t rows, int64_t cols, i
       const unsigned g = unsigned((rows + 7) / 8);
       if (cols <= 256) k_act8_pack_rows<T, 1, true><<<g, b, 0, st>>>(m, o, rows, int(cols));
       else if (cols <= 512) k_act8_pack_rows<T, 2, true><<<g, b, 0, st>>>(m, o, rows, int(cols));
+      else if (cols <= 768) k_act8_pack_rows<T, 3, true><<<g, b, 0, st>>>(m, o, rows, int(cols));
       else k_act8_pack_rows<T, 4, true><<<g, b, 0, st>>>(m, o, rows, int(cols));
     } else {
-      // no more threads than pieces: one each in rows up to 4096, two up to
-      // 12288, four up to 24576
+      // Few threads with many pieces each in flight: 256 with up to 8 (fp32,
+      // whose pieces take twice the registers: 512 with up to 4).  16384 x
+      // 11008 bf16: 99 us, against 128 with 704 threads of two pieces.
       const int64_t pieces = (cols + 7) / 8;
-      const int it = pieces <= 512 ? 1 : (pieces <= 2 * kRowThreads ? 2 : 4);
-      const unsigned b = unsigned(std::min<int64_t>(kRowThreads, ((pieces + it - 1) / it + 31) / 32 * 32));
       const unsigned g = unsigned(rows);
-      if (pieces > 4 * kRowThreads) k_act8_pack_rows<T, 0, false><<<g, b, 0, st>>>(m, o, rows, int(cols));
-      else if (it == 1) k_act8_pack_rows<T, 1, false><<<g, b, 0, st>>>(m, o, rows, int(cols));
+      const int threads = sizeof(T) == 2 || pieces <= 1024 ? 256 : 512;
+      const int it = int(std::min<int64_t>((pieces + threads - 1) / threads, 99));
+      const unsigned b = unsigned(std::min<int64_t>(threads, ((pieces + it - 1) / it + 31) / 32 * 32));
+      if (it == 1) k_act8_pack_rows<T, 1, false><<<g, b, 0, st>>>(m, o, rows, int(cols));
       else if (it == 2) k_act8_pack_rows<T, 2, false><<<g, b, 0, st>>>(m, o, rows, int(cols));
-      else k_act8_pack_rows<T, 4, false><<<g, b, 0, st>>>(m, o, rows, int(cols));
+      else if (it == 3) k_act8_pack_rows<T, 3, false><<<g, b, 0, st>>>(m, o, rows, int(cols));
+      else if (it == 4) k_act8_pack_rows<T, 4, false><<<g, b, 0, st>>>(m, o, rows, int(cols));
+      else if (sizeof(T) == 2 && it <= 6) k_act8_pack_rows<T, 6, false><<<g, b, 0, st>>>(m, o, rows, int(cols));
+      else if (sizeof(T) == 2 && it <= 8) k_act8_pack_rows<T, 8, false><<<g, b, 0, st>>>(m, o, rows, int(cols));
+      else k_act8_pack_rows<T, 0, false><<<g, 512, 0, st>>>(m, o, rows, int(cols));
     }
     S4_CUDA(cudaGetLastError());
     return SHAMPOO4_OK;

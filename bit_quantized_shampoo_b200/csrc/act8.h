@@ -6,7 +6,8 @@
 
 namespace s4 {
 
-constexpr int64_t kAct8MaxDim = int64_t(1) << 30;      // rows or columns of any matrix
+constexpr int64_t kAct8MaxRows = int64_t(1) << 30;     // of any matrix
+constexpr int64_t kAct8MaxCols = int64_t(1) << 26;
 constexpr int64_t kAct8MaxInner = int64_t(1) << 17;    // 128 * 127 * 2^17 < 2^31: an integer sum stays exact
 constexpr int kAct8CodeAlign = 16;                     // bytes, of code rows (TMA)
 constexpr int kAct8Digits = 3;                         // base-256 digits of a fixed-point gradient

@@ -235,7 +235,7 @@ int group_shift(int32_t group) {
 }
 int64_t group_count(int64_t cols, int32_t group) { return group ? (cols + group - 1) / group : 1; }
 bool shape_ok(int64_t rows, int64_t cols) {
-  return rows >= 0 && cols >= 0 && rows <= kAct8MaxDim && cols <= kAct8MaxDim;
+  return rows >= 0 && cols >= 0 && rows <= kAct8MaxRows && cols <= kAct8MaxCols;
 }
 // A float matrix: element-aligned, rows that do not overlap.
 bool mat_ok(const void* p, int32_t dtype, int64_t rows, int64_t cols, int64_t ld) {

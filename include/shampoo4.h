@@ -530,7 +530,7 @@ shampoo4_status shampoo4_graft_update(shampoo4_handle h, const shampoo4_graft_co
  * their element, leading dimension >= cols (16-byte aligned rows take the
  * vector path); scales and biases are fp32.  Bytes between cols and a leading
  * dimension are neither read into a result nor written.  At most 2^30 rows
- * or columns.  Outputs must not overlap inputs.  Bad arguments return
+ * and 2^26 columns.  Outputs must not overlap inputs.  Bad arguments return
  * SHAMPOO4_ERR_INVALID_ARG before anything is enqueued; an empty result does
  * nothing.  Everything is enqueued on `stream` of the current device, which
  * must be the tensors' own; nothing is allocated, and the calls hold no
@@ -572,8 +572,9 @@ shampoo4_status act8_linear(const void* d_x, int32_t xdtype, int64_t ldx, const 
  * accumulate != 0 adds the product to the result's contents (in fp32,
  * rounded once).  Arithmetic, by the types and scales (xf: a code's value):
  *   one scale per row   dY * scale in fp32, then fixed point: 24 bits below
- *                       its largest magnitude over the contraction; exact
- *                       integer products and sums with the codes.
+ *                       its largest magnitude over the contraction (a largest
+ *                       below 2^-100 counts as 2^-100); exact integer
+ *                       products and sums with the codes.
  *   scales per group    dY and xf to 22 bits, and no finer than 2^-39 of the
  *                       largest in the whole tensor; fp32 sums.
  *   dY and the result bfloat16, with scales per group or more than 640 rows

@@ -113,7 +113,7 @@ def _pack(x=OK16, dt=0, rows=4, cols=64, ldx=64, group=0, codes=OK16, ldc=64, sc
 @pytest.mark.parametrize("kw", [
     dict(x=0), dict(codes=0), dict(scales=0), dict(dt=3), dict(dt=-1), dict(rows=-1), dict(cols=-1), dict(ldx=63),
     dict(group=48), dict(group=-1), dict(group=512), dict(codes=OK16 + 8), dict(ldc=72), dict(ldc=48),
-    dict(scales=OK16 + 2), dict(x=OK16 + 2), dict(dt=1, x=OK16 + 1), dict(rows=(1 << 30) + 1), dict(cols=(1 << 30) + 1)])
+    dict(scales=OK16 + 2), dict(x=OK16 + 2), dict(dt=1, x=OK16 + 1), dict(rows=(1 << 30) + 1), dict(cols=(1 << 26) + 1, ldx=1 << 27, ldc=1 << 27)])
 def test_pack_refuses(kw):
     assert _pack(**kw) == INVALID
 

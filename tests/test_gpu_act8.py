@@ -334,6 +334,60 @@ def test_grads_strides_and_accumulation(pad, offset, dtype):
         assert torch.all(room[:, :4] == 2) and torch.all(room[:, 137:] == 2)
 
 
+@pytest.mark.parametrize("group", [0, 64])
+def test_weight_grad_over_a_long_contraction(group):
+    """More tokens than an integer sum can take at once: equal signs, the
+    largest codes and digits, two and a half sums of 2^17."""
+    api = _api()
+    tokens = 5 << 16
+    dy = torch.full((tokens, 3), 0.5, device="cuda")
+    dy[:, 1] = -0.25
+    dy[1::2, 2] = -0.5
+    codes = torch.full((tokens, 16), 127, dtype=torch.int8, device="cuda")
+    scales = torch.full((tokens, 1), 1.0 / 64, device="cuda")
+    dw = f64(api.act8_weight_grad(dy, codes, scales, group=group))
+    per = 127 / 64 * tokens
+    # digits: q = 8355704 for every element but for a few roundings; groups: at most 17 * 3 * 2^-22 of the sum and
+    # one rounding per 256 tokens (1280 of them)
+    bound = per * (8 * 2.0 ** -24 if group == 0 else 51 * 2.0 ** -22 + 1280 * 2.0 ** -24)
+    within(dw, np.tile(np.array([[0.5 * per], [-0.25 * per], [0.0]]), (1, 16)), bound)
+
+
+def test_offsets_past_32_bits():
+    """Matrices of more than 2^32 elements: the last rows against the same
+    rows alone."""
+    api = _api()
+    rows, cols, tail = 66000, 65552, 5
+    x = torch.randn(rows, cols, dtype=torch.bfloat16, device="cuda")
+    for group in (0, 128):
+        codes, scales = api.act8_pack(x, group=group)
+        c, s = api.act8_pack(x[-tail:], group=group)
+        assert torch.equal(codes[-tail:], c) and torch.equal(scales[-tail:], s)
+        back = api.act8_unpack(codes, scales, group=group, dtype=torch.bfloat16)
+        assert torch.equal(back[-tail:], api.act8_unpack(c, s, group=group, dtype=torch.bfloat16))
+        h, kept = api.act8_swiglu(x, back, group=group)
+        h2, kept2 = api.act8_swiglu(x[-tail:], back[-tail:], group=group)
+        assert torch.equal(h[-tail:], h2) and all(torch.equal(a[-tail:], b) for a, b in zip(kept, kept2))
+        dg, du = api.act8_swiglu_backward(x, kept, group=group)
+        dg2, du2 = api.act8_swiglu_backward(x[-tail:], kept2, group=group)
+        assert torch.equal(dg[-tail:], dg2) and torch.equal(du[-tail:], du2)
+        del back, h, kept, dg, du
+    # the result of a product, and each operand of a gradient
+    a, b = api.act8_pack(x[:, :128]), api.act8_pack(x[:cols, 128:256])
+    y = api.act8_matmul(*a, *b)
+    assert torch.equal(y[-tail:], api.act8_matmul(a[0][-tail:], a[1][-tail:], *b))
+    del y
+    w = api.act8_pack(x[:128])
+    dx = api.act8_input_grad(x[:, :128], *w, dtype=torch.float32)
+    assert torch.equal(dx[-tail:], api.act8_input_grad(x[-tail:, :128], *w, dtype=torch.float32))
+    del dx
+    dw = api.act8_weight_grad(x[:128, -300:], *w)
+    dw2 = api.act8_weight_grad(x, *api.act8_pack(x[:, :16]), dtype=torch.float32)
+    part = api.act8_weight_grad(x[:, -7:], *api.act8_pack(x[:, :16]), dtype=torch.float32)
+    assert torch.equal(dw2[-7:], part)
+    assert torch.isfinite(dw).all()
+
+
 def test_grads_empty():
     api = _api()
     x, _, _ = stored(3, 20, 1)
