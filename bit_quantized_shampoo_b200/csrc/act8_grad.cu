@@ -28,6 +28,7 @@
 // The operand passes of this file stream; their bound is HBM bandwidth.
 #include <cooperative_groups.h>
 #include "act8_elt.cuh"
+#include "quant4.cuh"
 
 namespace cg = cooperative_groups;
 
@@ -49,12 +50,12 @@ struct Fixed {
     inv = finite ? __fdiv_rn(kQMax, a) : 0.0f;
     scale = finite ? __fdiv_rn(a, kQMax) : __uint_as_float(0x7fc00000u);
   }
-  // The three digits as the low bytes, least significant first (a NaN, from
-  // inv = 0 and an infinity, converts to 0).
-  __device__ __forceinline__ uint32_t digits(float f) const {
-    return uint32_t(__float2int_rn(f * inv) + 0x808080) ^ 0x808080u;
-  }
 };
+// The three digits of f * inv as the low bytes, least significant first (a
+// NaN, from inv = 0 and an infinity, converts to 0).
+__device__ __forceinline__ uint32_t digits_of(float f, float inv) {
+  return uint32_t(__float2int_rn(f * inv) + 0x808080) ^ 0x808080u;
+}
 
 // Byte `b` of four words, the first word's in the low byte.
 __device__ __forceinline__ uint32_t bytes4(uint32_t x0, uint32_t x1, uint32_t x2, uint32_t x3, int b) {
@@ -86,7 +87,7 @@ k_act8_digit_rows(Mat dy, const float* __restrict__ scale, int8_t* digits, int64
     load8(x, c, cols, dy.vec, r);
     uint32_t q[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) q[i] = c + i < cols ? f.digits(elt(r, i) * __ldg(scale + c + i)) : 0u;
+    for (int i = 0; i < 8; ++i) q[i] = c + i < cols ? digits_of(elt(r, i) * __ldg(scale + c + i), f.inv) : 0u;
 #pragma unroll
     for (int d = 0; d < kAct8Digits; ++d) {
       const int b = kAct8Digits - 1 - d;
@@ -120,22 +121,40 @@ k_act8_digit_columns(Mat dy, const float* __restrict__ scale, int8_t* digits, in
   if (threadIdx.x < kColTile) colmax[threadIdx.x] = 0;
   __syncthreads();
 
+  // This thread's 4 tokens by 8 columns of tile tt, and the tokens' scales.
+  const bool inside = dy.vec && c + 8 <= cols;
+  auto fetch = [&](int64_t tt, Raw8<T> (&r)[4], float (&s)[4]) {
+    const int64_t t0 = tt * kTokTile + tgrp * 4;
+    const T* p = x + t0 * dy.ld;
+    if (inside && t0 + 4 <= tokens) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint4* q = reinterpret_cast<const uint4*>(p + j * dy.ld + c);
+#pragma unroll
+        for (int k = 0; k < int(sizeof(T) / 2); ++k) r[j].v[k] = __ldg(q + k);
+        s[j] = __ldg(scale + t0 + j);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        load8(p + j * dy.ld, c, t0 + j < tokens ? int(cols) : 0, dy.vec, r[j]);
+        s[j] = t0 + j < tokens ? __ldg(scale + t0 + j) : 0.0f;
+      }
+    }
+  };
   uint32_t m[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) m[i] = 0;
   for (int64_t tt = blockIdx.y; tt < ntiles; tt += gridDim.y) {
     Raw8<T> r[4];
     float s[4];
+    fetch(tt, r, s);
+    // the maximum of magnitudes, NaN above all: |dy s| by pairs of tokens
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int64_t t = tt * kTokTile + tgrp * 4 + j;
-      load8(x + t * dy.ld, c, t < tokens ? int(cols) : 0, dy.vec, r[j]);
-      s[j] = t < tokens ? __ldg(scale + t) : 0.0f;
+    for (int i = 0; i < 8; ++i) {
+      const float a = max2_nan(fabsf(elt(r[0], i) * s[0]), fabsf(elt(r[1], i) * s[1]));
+      m[i] = max(m[i], abs_bits(absmax3_nan(a, elt(r[2], i) * s[2], elt(r[3], i) * s[3])));
     }
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) m[i] = max(m[i], abs_bits(elt(r[j], i) * s[j]));
   }
 #pragma unroll
   for (int i = 0; i < 8; ++i) {                         // over the warp's 4 token groups, then the CTA
@@ -163,32 +182,29 @@ k_act8_digit_columns(Mat dy, const float* __restrict__ scale, int8_t* digits, in
   for (int i = 0; i < 8; ++i) inv[i] = Fixed(colmax[cgrp * 8 + i]).inv;
 
   for (int64_t tt = blockIdx.y; tt < ntiles; tt += gridDim.y) {
-    uint32_t q[8][4];
+    Raw8<T> r[4];
+    float s[4];
+    fetch(tt, r, s);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int64_t t = tt * kTokTile + tgrp * 4 + j;
-      Raw8<T> r;
-      load8(x + t * dy.ld, c, t < tokens ? int(cols) : 0, dy.vec, r);
-      const float s = t < tokens ? __ldg(scale + t) : 0.0f;
-      Fixed f(0u);
+    for (int i = 0; i < 8; ++i) {
+      uint32_t q[4];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        f.inv = inv[i];
-        q[i][j] = f.digits(elt(r, i) * s);
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
+      for (int j = 0; j < 4; ++j) q[j] = digits_of(elt(r[j], i) * s[j], inv[i]);
 #pragma unroll
       for (int d = 0; d < kAct8Digits; ++d)
-        tile[d][cgrp * 8 + i][tgrp] = bytes4(q[i][0], q[i][1], q[i][2], q[i][3], kAct8Digits - 1 - d);
+        tile[d][cgrp * 8 + i][tgrp] = bytes4(q[0], q[1], q[2], q[3], kAct8Digits - 1 - d);
+    }
     __syncthreads();
     const int lane = threadIdx.x & 31;
     const int64_t t = tt * kTokTile + lane * 4;
-    for (int w = threadIdx.x >> 5; w < kAct8Digits * kColTile; w += kThreads / 32) {
-      const int d = w / kColTile, n = w % kColTile;
-      if (n0 + n < cols && t < ld)                      // ld is a multiple of 16: a word is inside or outside
-        *reinterpret_cast<uint32_t*>(digits + (d * cols + n0 + n) * ld + t) = tile[d][n][lane];
+    const int rows = int(min(int64_t(kColTile), cols - n0));
+    if (t < ld) {                                       // ld is a multiple of 16: a word is inside or outside
+#pragma unroll
+      for (int d = 0; d < kAct8Digits; ++d) {
+        int8_t* o = digits + (d * cols + n0) * ld + t;
+        for (int n = threadIdx.x >> 5; n < rows; n += kThreads / 32)
+          *reinterpret_cast<uint32_t*>(o + n * ld) = tile[d][n][lane];
+      }
     }
     __syncthreads();
   }
@@ -275,32 +291,33 @@ __device__ __forceinline__ void store_halves(const float (&v)[8], float power, _
   if (PARTS == 2) store8(o + plane, c, cols, 1, lo);
 }
 
-__global__ void __launch_bounds__(kThreads) k_act8_code_halves(Ckpt k, const Largest* largest, __half* o, int64_t ld,
-                                                               int64_t rows, int cols) {
-  const Piece<1> p;
-  if (p.row >= rows || p.c >= cols) return;
-  uint2 w;
-  load_codes8(k.codes + p.row * k.ldc, p.c, cols, w);
-  float v[8];
-  values8(w, __ldg(k.scales + p.row * k.groups + (p.c >> k.shift)), v);
-  store_halves<2>(v, value_power(largest), o + p.row * ld, rows * ld, p.c, cols);
-}
-
+// Both operands in one launch: blockIdx.z 0 the codes' values, 1 dY (the
+// column pieces of the wider one; the other's surplus warps leave).
 template <class T, int PARTS>
-__global__ void __launch_bounds__(kThreads) k_act8_dy_halves(Mat x, const Largest* largest, float* factor, __half* o,
-                                                             int64_t ld, int64_t rows, int cols) {
+__global__ void __launch_bounds__(kThreads)
+k_act8_halves(Ckpt k, __half* co, int64_t ldco, int cols_c, Mat dy, __half* dyo, int64_t lddyo, int cols_dy,
+              const Largest* largest, float* factor, int64_t rows) {
   let_next_start();
-  const float power = power_to(largest->dy);
-  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0 && threadIdx.y == 0)
-    *factor = (1.0f / power) * (1.0f / value_power(largest));
   const Piece<1> p;
-  if (p.row >= rows || p.c >= cols) return;
-  Raw8<T> r;
-  load8(static_cast<const T*>(x.p) + p.row * x.ld, p.c, cols, x.vec, r);
+  const float pc = value_power(largest), pd = power_to(largest->dy);
+  if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0 && threadIdx.x == 0 && threadIdx.y == 0)
+    *factor = (1.0f / pc) * (1.0f / pd);
+  if (p.row >= rows) return;
   float v[8];
+  if (blockIdx.z == 0) {
+    if (p.c >= cols_c) return;
+    uint2 w;
+    load_codes8(k.codes + p.row * k.ldc, p.c, cols_c, w);
+    values8(w, __ldg(k.scales + p.row * k.groups + (p.c >> k.shift)), v);
+    store_halves<2>(v, pc, co + p.row * ldco, rows * ldco, p.c, cols_c);
+  } else {
+    if (p.c >= cols_dy) return;
+    Raw8<T> r;
+    load8(static_cast<const T*>(dy.p) + p.row * dy.ld, p.c, cols_dy, dy.vec, r);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = elt(r, i);
-  store_halves<PARTS>(v, power, o + p.row * ld, rows * ld, p.c, cols);
+    for (int i = 0; i < 8; ++i) v[i] = elt(r, i);
+    store_halves<PARTS>(v, pd, dyo + p.row * lddyo, rows * lddyo, p.c, cols_dy);
+  }
 }
 
 // ------------------------------------------------------------------ host
@@ -408,19 +425,20 @@ shampoo4_status halves_pass(const void* dy, int32_t dtype, int64_t lddy, const C
                             int64_t inner, Largest* largest, float* factor, void* dyp, int64_t ld_dy, void* cp,
                             int64_t ld_code, cudaStream_t st) {
   const Mat m = mat(dy, lddy, dtype);
-  const dim3 bd = piece_block(out), bc = piece_block(inner);
-  dim3 gd, gc;
-  if (!piece_grid(tokens, out, bd, 1, &gd) || !piece_grid(tokens, inner, bc, 1, &gc)) return SHAMPOO4_ERR_INVALID_ARG;
+  const int64_t widest = std::max(out, inner);
+  const dim3 b = piece_block(widest);
+  dim3 g;
+  if (!piece_grid(tokens, widest, b, 1, &g)) return SHAMPOO4_ERR_INVALID_ARG;
+  g.z = 2;
   S4_CUDA(cudaMemsetAsync(largest, 0, sizeof(Largest), st));
   return by_dtype(dtype, [&](auto* tag) -> shampoo4_status {
     using T = std::remove_pointer_t<decltype(tag)>;
     k_act8_largest<T><<<unsigned(std::min<int64_t>(tokens, 148 * 4)), kThreads, 0, st>>>(
         m, k.scales, tokens * k.groups, largest, tokens, int(out));
     S4_CUDA(cudaGetLastError());
-    k_act8_code_halves<<<gc, bc, 0, st>>>(k, largest, static_cast<__half*>(cp), ld_code, tokens, int(inner));
-    S4_CUDA(cudaGetLastError());
-    k_act8_dy_halves<T, sizeof(T) == 4 ? 2 : 1><<<gd, bd, 0, st>>>(m, largest, factor, static_cast<__half*>(dyp), ld_dy,
-                                                                  tokens, int(out));
+    k_act8_halves<T, sizeof(T) == 4 ? 2 : 1><<<g, b, 0, st>>>(k, static_cast<__half*>(cp), ld_code, int(inner), m,
+                                                             static_cast<__half*>(dyp), ld_dy, int(out), largest,
+                                                             factor, tokens);
     S4_CUDA(cudaGetLastError());
     return SHAMPOO4_OK;
   });
