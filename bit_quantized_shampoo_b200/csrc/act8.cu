@@ -153,14 +153,14 @@ __device__ __forceinline__ uint32_t absmax8(const Raw8<__half>& r) {
 
 // ---- pack
 
-template <class T, int kRows>
+template <class T, int kRows, bool A>
 __global__ void __launch_bounds__(kThreads) k_act8_pack_groups(Mat x, Ckpt o, int64_t rows, int cols) {
   const Piece<kRows> p;
   if (p.row >= rows) return;                             // a whole warp
   Raw8<T> r[kRows];
 #pragma unroll
   for (int u = 0; u < kRows; ++u)
-    load8(static_cast<const T*>(x.p) + p.at(u) * x.ld, p.c, p.at(u) < rows ? cols : 0, x.vec, r[u]);
+    load8<A>(static_cast<const T*>(x.p) + p.at(u) * x.ld, p.c, p.at(u) < rows ? cols : 0, x.vec, r[u]);
 #pragma unroll
   for (int u = 0; u < kRows; ++u) {
     const int64_t row = p.at(u);
@@ -174,7 +174,7 @@ __global__ void __launch_bounds__(kThreads) k_act8_pack_groups(Mat x, Ckpt o, in
 // One scale for the row.  WARP: a warp per row (up to 1024 columns); else a
 // CTA per row.  IT > 0: a thread's at most IT pieces of 8 columns stay in
 // registers between the maximum and the codes; IT = 0: the row is read twice.
-template <class T, int IT, bool WARP>
+template <class T, int IT, bool WARP, bool A>
 __global__ void __launch_bounds__(512, 2) k_act8_pack_rows(Mat x, Ckpt o, int64_t rows, int cols) {
   __shared__ uint32_t slots[32];
   let_next_start();
@@ -187,7 +187,7 @@ __global__ void __launch_bounds__(512, 2) k_act8_pack_rows(Mat x, Ckpt o, int64_
   if (IT > 0) {
     Raw8<T> r[IT > 0 ? IT : 1];
 #pragma unroll
-    for (int i = 0; i < IT; ++i) load8(xr, first + i * step, cols, x.vec, r[i]);
+    for (int i = 0; i < IT; ++i) load8<A>(xr, first + i * step, cols, x.vec, r[i]);
 #pragma unroll
     for (int i = 0; i < IT; ++i) m = max(m, absmax8(r[i]));
     m = WARP ? __reduce_max_sync(0xffffffffu, m) : cta_max(m, slots);
@@ -201,12 +201,12 @@ __global__ void __launch_bounds__(512, 2) k_act8_pack_rows(Mat x, Ckpt o, int64_
   } else {
     Raw8<T> r;
     for (int c = first; c < cols; c += step) {
-      load8(xr, c, cols, x.vec, r);
+      load8<A>(xr, c, cols, x.vec, r);
       m = max(m, absmax8(r));
     }
     const Group g(cta_max(m, slots));
     for (int c = first; c < cols; c += step) {
-      load8(xr, c, cols, x.vec, r);
+      load8<A>(xr, c, cols, x.vec, r);
       store_codes8(cr, c, cols, codes8(r, g));
     }
     if (threadIdx.x == 0) o.scales[row] = g.scale();
@@ -215,23 +215,23 @@ __global__ void __launch_bounds__(512, 2) k_act8_pack_rows(Mat x, Ckpt o, int64_
 
 // ---- unpack
 
-template <class T, int kRows>
+template <class T, int kRows, bool A>
 __global__ void __launch_bounds__(kThreads) k_act8_unpack(Ckpt k, T* x, int64_t ldx, int vec, int64_t rows, int cols) {
   const Piece<kRows> p;
-  if (p.row >= rows || p.c >= cols) return;
+  if (p.row >= rows || (A && p.c >= cols)) return;       // unaligned stores are a whole warp's
   uint2 w[kRows];
   float s[kRows];
 #pragma unroll
   for (int u = 0; u < kRows; ++u) {
     const int64_t row = p.at(u);
     load_codes8(k.codes + row * k.ldc, p.c, row < rows ? cols : 0, w[u]);
-    s[u] = row < rows ? __ldg(k.scales + row * k.groups + (p.c >> k.shift)) : 0.0f;
+    s[u] = row < rows && (A || p.c < cols) ? __ldg(k.scales + row * k.groups + (p.c >> k.shift)) : 0.0f;
   }
 #pragma unroll
   for (int u = 0; u < kRows; ++u) {
     float v[8];
     values8(w[u], s[u], v);
-    store8(x + p.at(u) * ldx, p.c, p.at(u) < rows ? cols : 0, vec, v);
+    store8_any<A>(x + p.at(u) * ldx, p.c, p.at(u) < rows ? cols : 0, vec, v);
   }
 }
 
@@ -249,7 +249,7 @@ __device__ __forceinline__ float sigmoid(float x) {
   return rcp_approx(1.0f + e);
 }
 
-template <class T>
+template <bool A, class T>
 __device__ __forceinline__ void gated8(const Raw8<T>& g, const Raw8<T>& u, T* h, int c, int n, int vec) {
   float v[8];
 #pragma unroll
@@ -257,10 +257,10 @@ __device__ __forceinline__ void gated8(const Raw8<T>& g, const Raw8<T>& u, T* h,
     const float x = elt(g, i);
     v[i] = x * sigmoid<T>(x) * elt(u, i);
   }
-  store8(h, c, n, vec, v);
+  store8_any<A>(h, c, n, vec, v);
 }
 
-template <class T, int kRows>
+template <class T, int kRows, bool A>
 __global__ void __launch_bounds__(kThreads)
 k_act8_swiglu_groups(Mat gate, Mat up, T* h, int64_t ldh, int vech, Ckpt kg, Ckpt ku, int64_t rows, int cols) {
   const Piece<kRows> p;
@@ -270,28 +270,30 @@ k_act8_swiglu_groups(Mat gate, Mat up, T* h, int64_t ldh, int vech, Ckpt kg, Ckp
   for (int k = 0; k < kRows; ++k) {
     const int64_t row = p.at(k);
     const int n = row < rows ? cols : 0;
-    load8(static_cast<const T*>(gate.p) + row * gate.ld, p.c, n, gate.vec, g[k]);
-    load8(static_cast<const T*>(up.p) + row * up.ld, p.c, n, up.vec, u[k]);
+    load8<A>(static_cast<const T*>(gate.p) + row * gate.ld, p.c, n, gate.vec, g[k]);
+    load8<A>(static_cast<const T*>(up.p) + row * up.ld, p.c, n, up.vec, u[k]);
   }
 #pragma unroll
   for (int k = 0; k < kRows; ++k) {
     const int64_t row = p.at(k);
     const int lanes = 1 << (kg.shift - 3);
     const Group gg(group_max(absmax8(g[k]), lanes)), gu(group_max(absmax8(u[k]), lanes));
-    if (row >= rows || p.c >= cols) continue;
-    store_codes8(kg.codes + row * kg.ldc, p.c, cols, codes8(g[k], gg));
-    store_codes8(ku.codes + row * ku.ldc, p.c, cols, codes8(u[k], gu));
-    if ((p.c & ((1 << kg.shift) - 1)) == 0) {
-      const int64_t s = row * kg.groups + (p.c >> kg.shift);
-      kg.scales[s] = gg.scale();
-      ku.scales[s] = gu.scale();
+    if (row >= rows) continue;                           // a whole warp
+    if (p.c < cols) {
+      store_codes8(kg.codes + row * kg.ldc, p.c, cols, codes8(g[k], gg));
+      store_codes8(ku.codes + row * ku.ldc, p.c, cols, codes8(u[k], gu));
+      if ((p.c & ((1 << kg.shift) - 1)) == 0) {
+        const int64_t s = row * kg.groups + (p.c >> kg.shift);
+        kg.scales[s] = gg.scale();
+        ku.scales[s] = gu.scale();
+      }
     }
-    gated8(g[k], u[k], h + row * ldh, p.c, cols, vech);
+    gated8<A>(g[k], u[k], h + row * ldh, p.c, cols, vech);
   }
 }
 
 // One scale per row: the row is read twice (the second time from cache).
-template <class T>
+template <class T, bool A>
 __global__ void __launch_bounds__(kThreads)
 k_act8_swiglu_rows(Mat gate, Mat up, T* h, int64_t ldh, int vech, Ckpt kg, Ckpt ku, int64_t rows, int cols) {
   __shared__ uint32_t slots[kThreads / 32];
@@ -301,18 +303,19 @@ k_act8_swiglu_rows(Mat gate, Mat up, T* h, int64_t ldh, int vech, Ckpt kg, Ckpt 
   Raw8<T> g, u;
   uint32_t mg = 0, mu = 0;
 #pragma unroll 2
-  for (int c = int(threadIdx.x) * 8; c < cols; c += kThreads * 8) {
-    load8(gr, c, cols, gate.vec, g);
-    load8(ur, c, cols, up.vec, u);
+  for (int c0 = 0; c0 < cols; c0 += kThreads * 8) {      // all lanes to the end
+    const int c = c0 + int(threadIdx.x) * 8;
+    load8<A>(gr, c, cols, gate.vec, g);
+    load8<A>(ur, c, cols, up.vec, u);
     mg = max(mg, absmax8(g));
     mu = max(mu, absmax8(u));
-    gated8(g, u, h + row * ldh, c, cols, vech);
+    gated8<A>(g, u, h + row * ldh, c, cols, vech);
   }
   const Group gg(cta_max(mg, slots)), gu(cta_max(mu, slots));
 #pragma unroll 2
   for (int c = int(threadIdx.x) * 8; c < cols; c += kThreads * 8) {
-    load8(gr, c, cols, gate.vec, g);
-    load8(ur, c, cols, up.vec, u);
+    load8<A>(gr, c, cols, gate.vec, g);
+    load8<A>(ur, c, cols, up.vec, u);
     store_codes8(kg.codes + row * kg.ldc, c, cols, codes8(g, gg));
     store_codes8(ku.codes + row * ku.ldc, c, cols, codes8(u, gu));
   }
@@ -322,12 +325,12 @@ k_act8_swiglu_rows(Mat gate, Mat up, T* h, int64_t ldh, int vech, Ckpt kg, Ckpt 
   }
 }
 
-template <class T, int kRows>
+template <class T, int kRows, bool A>
 __global__ void __launch_bounds__(kThreads)
 k_act8_swiglu_backward(Mat dh, Ckpt kg, Ckpt ku, T* dg, int64_t lddg, int vecg, T* du, int64_t lddu, int vecu,
                        int64_t rows, int cols) {
   const Piece<kRows> p;
-  if (p.row >= rows || p.c >= cols) return;
+  if (p.row >= rows || (A && p.c >= cols)) return;       // unaligned stores are a whole warp's
   Raw8<T> d[kRows];
   uint2 wg[kRows], wu[kRows];
   float sg[kRows], su[kRows];
@@ -336,11 +339,11 @@ k_act8_swiglu_backward(Mat dh, Ckpt kg, Ckpt ku, T* dg, int64_t lddg, int vecg, 
   for (int k = 0; k < kRows; ++k) {
     const int64_t row = p.at(k);
     const int n = row < rows ? cols : 0;
-    load8(static_cast<const T*>(dh.p) + row * dh.ld, p.c, n, dh.vec, d[k]);
+    load8<A>(static_cast<const T*>(dh.p) + row * dh.ld, p.c, n, dh.vec, d[k]);
     load_codes8(kg.codes + row * kg.ldc, p.c, n, wg[k]);
     load_codes8(ku.codes + row * ku.ldc, p.c, n, wu[k]);
-    sg[k] = n ? __ldg(kg.scales + row * kg.groups + gi) : 0.0f;
-    su[k] = n ? __ldg(ku.scales + row * ku.groups + gi) : 0.0f;
+    sg[k] = n && (A || p.c < n) ? __ldg(kg.scales + row * kg.groups + gi) : 0.0f;
+    su[k] = n && (A || p.c < n) ? __ldg(ku.scales + row * ku.groups + gi) : 0.0f;
   }
 #pragma unroll
   for (int k = 0; k < kRows; ++k) {
@@ -355,8 +358,8 @@ k_act8_swiglu_backward(Mat dh, Ckpt kg, Ckpt ku, T* dg, int64_t lddg, int vecg, 
       ou[i] = x * (g[i] * sig);
       og[i] = x * u[i] * (sig * fmaf(g[i], 1.0f - sig, 1.0f));
     }
-    store8(dg + row * lddg, p.c, n, vecg, og);
-    store8(du + row * lddu, p.c, n, vecu, ou);
+    store8_any<A>(dg + row * lddg, p.c, n, vecg, og);
+    store8_any<A>(du + row * lddu, p.c, n, vecu, ou);
   }
 }
 
@@ -364,23 +367,25 @@ shampoo4_status pack(const void* x, int32_t dtype, int64_t rows, int64_t cols, i
                      cudaStream_t st) {
   if (rows == 0 || cols == 0) return SHAMPOO4_OK;
   const Mat m = mat(x, ldx, dtype);
-  return by_dtype(dtype, [&](auto* tag) -> shampoo4_status {
+  return by_dtype(dtype, [&](auto* tag) { return by_flag(m.vec != 0, [&](auto flag) -> shampoo4_status {
     using T = std::remove_pointer_t<decltype(tag)>;
+    constexpr bool A = decltype(flag)::value;
+    const int n = int(cols);
     if (group) {
       const dim3 b = piece_block(cols);
       dim3 g;
       constexpr int kMany = sizeof(T) == 4 ? 2 : 4;
       const bool many = many_pieces(rows, cols);
       if (!piece_grid(rows, cols, b, many ? kMany : 1, &g)) return SHAMPOO4_ERR_INVALID_ARG;
-      if (many) k_act8_pack_groups<T, kMany><<<g, b, 0, st>>>(m, o, rows, int(cols));
-      else k_act8_pack_groups<T, 1><<<g, b, 0, st>>>(m, o, rows, int(cols));
+      if (many) k_act8_pack_groups<T, kMany, A><<<g, b, 0, st>>>(m, o, rows, n);
+      else k_act8_pack_groups<T, 1, A><<<g, b, 0, st>>>(m, o, rows, n);
     } else if (cols <= 1024) {                           // 8 rows per CTA, a warp each
       const dim3 b(32, 8);
       const unsigned g = unsigned((rows + 7) / 8);
-      if (cols <= 256) k_act8_pack_rows<T, 1, true><<<g, b, 0, st>>>(m, o, rows, int(cols));
-      else if (cols <= 512) k_act8_pack_rows<T, 2, true><<<g, b, 0, st>>>(m, o, rows, int(cols));
-      else if (cols <= 768) k_act8_pack_rows<T, 3, true><<<g, b, 0, st>>>(m, o, rows, int(cols));
-      else k_act8_pack_rows<T, 4, true><<<g, b, 0, st>>>(m, o, rows, int(cols));
+      if (cols <= 256) k_act8_pack_rows<T, 1, true, A><<<g, b, 0, st>>>(m, o, rows, n);
+      else if (cols <= 512) k_act8_pack_rows<T, 2, true, A><<<g, b, 0, st>>>(m, o, rows, n);
+      else if (cols <= 768) k_act8_pack_rows<T, 3, true, A><<<g, b, 0, st>>>(m, o, rows, n);
+      else k_act8_pack_rows<T, 4, true, A><<<g, b, 0, st>>>(m, o, rows, n);
     } else {
       // Few threads with many pieces each in flight: 256 with up to 8 (fp32,
       // whose pieces take twice the registers: 512 with up to 4).  16384 x
@@ -390,17 +395,17 @@ shampoo4_status pack(const void* x, int32_t dtype, int64_t rows, int64_t cols, i
       const int threads = sizeof(T) == 2 || pieces <= 1024 ? 256 : 512;
       const int it = int(std::min<int64_t>((pieces + threads - 1) / threads, 99));
       const unsigned b = unsigned(std::min<int64_t>(threads, ((pieces + it - 1) / it + 31) / 32 * 32));
-      if (it == 1) k_act8_pack_rows<T, 1, false><<<g, b, 0, st>>>(m, o, rows, int(cols));
-      else if (it == 2) k_act8_pack_rows<T, 2, false><<<g, b, 0, st>>>(m, o, rows, int(cols));
-      else if (it == 3) k_act8_pack_rows<T, 3, false><<<g, b, 0, st>>>(m, o, rows, int(cols));
-      else if (it == 4) k_act8_pack_rows<T, 4, false><<<g, b, 0, st>>>(m, o, rows, int(cols));
-      else if (sizeof(T) == 2 && it <= 6) k_act8_pack_rows<T, 6, false><<<g, b, 0, st>>>(m, o, rows, int(cols));
-      else if (sizeof(T) == 2 && it <= 8) k_act8_pack_rows<T, 8, false><<<g, b, 0, st>>>(m, o, rows, int(cols));
-      else k_act8_pack_rows<T, 0, false><<<g, 512, 0, st>>>(m, o, rows, int(cols));
+      if (it == 1) k_act8_pack_rows<T, 1, false, A><<<g, b, 0, st>>>(m, o, rows, n);
+      else if (it == 2) k_act8_pack_rows<T, 2, false, A><<<g, b, 0, st>>>(m, o, rows, n);
+      else if (it == 3) k_act8_pack_rows<T, 3, false, A><<<g, b, 0, st>>>(m, o, rows, n);
+      else if (it == 4) k_act8_pack_rows<T, 4, false, A><<<g, b, 0, st>>>(m, o, rows, n);
+      else if (sizeof(T) == 2 && it <= 6) k_act8_pack_rows<T, 6, false, A><<<g, b, 0, st>>>(m, o, rows, n);
+      else if (sizeof(T) == 2 && it <= 8) k_act8_pack_rows<T, 8, false, A><<<g, b, 0, st>>>(m, o, rows, n);
+      else k_act8_pack_rows<T, 0, false, A><<<g, 512, 0, st>>>(m, o, rows, n);
     }
     S4_CUDA(cudaGetLastError());
     return SHAMPOO4_OK;
-  });
+  }); });
 }
 
 }  // namespace
@@ -433,14 +438,15 @@ extern "C" shampoo4_status act8_unpack(const int8_t* d_codes, int64_t ldc, const
   const Ckpt k = ckpt(d_codes, ldc, d_scales, cols, group);
   const int vec = vec_of(d_x, ldx, dtype);
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  return by_dtype(dtype, [&](auto* tag) -> shampoo4_status {
+  return by_dtype(dtype, [&](auto* tag) { return by_flag(vec != 0, [&](auto flag) -> shampoo4_status {
     using T = std::remove_pointer_t<decltype(tag)>;
+    constexpr bool A = decltype(flag)::value;
     T* x = static_cast<T*>(d_x);
-    if (many) k_act8_unpack<T, 4><<<g, b, 0, st>>>(k, x, ldx, vec, rows, int(cols));
-    else k_act8_unpack<T, 1><<<g, b, 0, st>>>(k, x, ldx, vec, rows, int(cols));
+    if (many) k_act8_unpack<T, 4, A><<<g, b, 0, st>>>(k, x, ldx, vec, rows, int(cols));
+    else k_act8_unpack<T, 1, A><<<g, b, 0, st>>>(k, x, ldx, vec, rows, int(cols));
     S4_CUDA(cudaGetLastError());
     return SHAMPOO4_OK;
-  });
+  }); });
 }
 
 static shampoo4_status check_product(int64_t tokens, int64_t out, int64_t inner) {
@@ -508,20 +514,20 @@ extern "C" shampoo4_status act8_swiglu(const void* d_gate, int64_t ldg, const vo
   const Ckpt kg = ckpt(d_gate_codes, ldgc, d_gate_scales, cols, group);
   const Ckpt ku = ckpt(d_up_codes, lduc, d_up_scales, cols, group);
   const int vh = vec_of(d_h, ldh, dtype);
-  return by_dtype(dtype, [&](auto* tag) -> shampoo4_status {
+  const Mat mg = mat(d_gate, ldg, dtype), mu = mat(d_up, ldu, dtype);
+  return by_dtype(dtype, [&](auto* tag) { return by_flag(mg.vec && mu.vec && vh, [&](auto flag) -> shampoo4_status {
     using T = std::remove_pointer_t<decltype(tag)>;
-    const Mat mg = mat(d_gate, ldg, dtype), mu = mat(d_up, ldu, dtype);
+    constexpr bool A = decltype(flag)::value;
     T* h = static_cast<T*>(d_h);
     if (group && many)
-      k_act8_swiglu_groups<T, 2><<<g, b, 0, st>>>(mg, mu, h, ldh, vh, kg, ku, rows, int(cols));
+      k_act8_swiglu_groups<T, 2, A><<<g, b, 0, st>>>(mg, mu, h, ldh, vh, kg, ku, rows, int(cols));
     else if (group)
-      k_act8_swiglu_groups<T, 1><<<g, b, 0, st>>>(mg, mu, h, ldh, vh, kg, ku, rows, int(cols));
+      k_act8_swiglu_groups<T, 1, A><<<g, b, 0, st>>>(mg, mu, h, ldh, vh, kg, ku, rows, int(cols));
     else
-      k_act8_swiglu_rows<T><<<unsigned(rows), kThreads, 0, st>>>(
-          mg, mu, h, ldh, vh, kg, ku, rows, int(cols));
+      k_act8_swiglu_rows<T, A><<<unsigned(rows), kThreads, 0, st>>>(mg, mu, h, ldh, vh, kg, ku, rows, int(cols));
     S4_CUDA(cudaGetLastError());
     return SHAMPOO4_OK;
-  });
+  }); });
 }
 
 extern "C" shampoo4_status act8_swiglu_backward(const void* d_dh, int64_t lddh, int32_t dtype,
@@ -542,16 +548,17 @@ extern "C" shampoo4_status act8_swiglu_backward(const void* d_dh, int64_t lddh, 
   const Ckpt kg = ckpt(d_gate_codes, ldgc, d_gate_scales, cols, group);
   const Ckpt ku = ckpt(d_up_codes, lduc, d_up_scales, cols, group);
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  return by_dtype(dtype, [&](auto* tag) -> shampoo4_status {
+  const Mat m = mat(d_dh, lddh, dtype);
+  const int vg = vec_of(d_dgate, lddg, dtype), vu = vec_of(d_dup, lddu, dtype);
+  return by_dtype(dtype, [&](auto* tag) { return by_flag(m.vec && vg && vu, [&](auto flag) -> shampoo4_status {
     using T = std::remove_pointer_t<decltype(tag)>;
-    const Mat m = mat(d_dh, lddh, dtype);
+    constexpr bool A = decltype(flag)::value;
     T *dg = static_cast<T*>(d_dgate), *du = static_cast<T*>(d_dup);
-    const int vg = vec_of(dg, lddg, dtype), vu = vec_of(du, lddu, dtype);
     if (many)
-      k_act8_swiglu_backward<T, 2><<<g, b, 0, st>>>(m, kg, ku, dg, lddg, vg, du, lddu, vu, rows, int(cols));
+      k_act8_swiglu_backward<T, 2, A><<<g, b, 0, st>>>(m, kg, ku, dg, lddg, vg, du, lddu, vu, rows, int(cols));
     else
-      k_act8_swiglu_backward<T, 1><<<g, b, 0, st>>>(m, kg, ku, dg, lddg, vg, du, lddu, vu, rows, int(cols));
+      k_act8_swiglu_backward<T, 1, A><<<g, b, 0, st>>>(m, kg, ku, dg, lddg, vg, du, lddu, vu, rows, int(cols));
     S4_CUDA(cudaGetLastError());
     return SHAMPOO4_OK;
-  });
+  }); });
 }

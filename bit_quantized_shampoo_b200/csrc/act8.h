@@ -48,7 +48,11 @@ shampoo4_status launch_act8_bf16(const Act8Operand& a, const Act8Operand& b, int
                                  const Act8Out& out, uint32_t* flags, cudaStream_t st);
 // Halves both, operands the sums of their planes: a is K x M in two, b is
 // K x R in b_parts (1 or 2).  The product of the second planes is left out.
+// shares (act8_halves_shares, one of the least estimated time): with more than
+// one, the contraction is cut in that many and out.y receives their sums, fp32,
+// R x M each, for the caller to add up.
+int act8_halves_shares(int64_t M, int64_t R, int64_t K);
 shampoo4_status launch_act8_halves(const Act8Operand& a, const Act8Operand& b, int b_parts, int64_t M, int64_t R,
-                                   int64_t K, const Act8Out& out, uint32_t* flags, cudaStream_t st);
+                                   int64_t K, int shares, const Act8Out& out, uint32_t* flags, cudaStream_t st);
 
 }  // namespace s4

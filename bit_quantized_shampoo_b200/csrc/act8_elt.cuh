@@ -56,12 +56,38 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   return r;
 }
 
-// Columns c .. c + 7 of a row of n (zeros past its end).  vec: 1 when rows
-// are 16-byte aligned, 2 when they are 32-byte aligned (fp32 then moves its 8
-// elements at once).
-template <class T>
+// Words 0 .. N - 1 of the words w shifted down by `bytes` (0 .. 16): words move by
+// selects (the shift is the same for a whole row), bytes by funnel shifts.
+template <int N, bool SUBWORD>
+__device__ __forceinline__ void shift_down(uint32_t (&w)[N + 5], uint32_t bytes) {
+  if (bytes & 16u) {
+#pragma unroll
+    for (int i = 0; i < N + 1; ++i) w[i] = w[i + 4];
+  }
+  if (bytes & 8u) {
+#pragma unroll
+    for (int i = 0; i < N + 3; ++i) w[i] = w[i + 2];
+  }
+  if (bytes & 4u) {
+#pragma unroll
+    for (int i = 0; i < N + 4; ++i) w[i] = w[i + 1];
+  }
+  if (SUBWORD) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 8u * (bytes & 3u));
+  }
+}
+
+// Columns c .. c + 7 of a row of n (zeros past its end).  A: rows are 16-byte
+// aligned (vec 2: 32-byte, fp32 then moves its 8 elements at once).  Else, of
+// any alignment: the aligned 16-byte pieces around the elements, shifted,
+// inside the row, and one by one at its ends, so that nothing outside the row
+// is read.  (Kernels are built for each: with both in one, the registers of
+// the shifts cost aligned data a quarter of its bandwidth.)
+template <bool A, class T>
 __device__ __forceinline__ void load8(const T* row, int c, int n, int vec, Raw8<T>& r) {
-  if (vec && c + 8 <= n) {
+  constexpr int kWords = 2 * int(sizeof(T));            // of 8 elements
+  if (A && c + 8 <= n) {
     if (sizeof(T) == 4 && vec == 2) {
       uint32_t* w = reinterpret_cast<uint32_t*>(r.v);
       asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
@@ -72,6 +98,22 @@ __device__ __forceinline__ void load8(const T* row, int c, int n, int vec, Raw8<
 #pragma unroll
       for (int i = 0; i < int(sizeof(T) / 2); ++i) r.v[i] = __ldg(p + i);
     }
+  } else if (!A && c >= 8 && c + 16 <= n) {
+    const uintptr_t at = reinterpret_cast<uintptr_t>(row + c);
+    const uint4* p = reinterpret_cast<const uint4*>(at & ~uintptr_t(15));
+    uint32_t w[kWords + 5];
+#pragma unroll
+    for (int i = 0; i < kWords / 4 + 1; ++i) {
+      const uint4 x = __ldg(p + i);
+      w[4 * i] = x.x;
+      w[4 * i + 1] = x.y;
+      w[4 * i + 2] = x.z;
+      w[4 * i + 3] = x.w;
+    }
+    w[kWords + 4] = 0u;
+    shift_down<kWords, sizeof(T) == 2>(w, uint32_t(at) & 15u);
+#pragma unroll
+    for (int i = 0; i < kWords / 4; ++i) r.v[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
   } else {
     T* e = reinterpret_cast<T*>(r.v);
 #pragma unroll
@@ -99,11 +141,12 @@ __device__ __forceinline__ void round8(const float (&v)[8], Raw8<__half>& r) {
     w[i] = *reinterpret_cast<const uint32_t*>(&x);
   }
 }
+// To rows that are 16-byte aligned (vec 2: 32-byte).
 template <class T>
 __device__ __forceinline__ void store8(T* row, int c, int n, int vec, const float (&v)[8]) {
   Raw8<T> r;
   round8(v, r);
-  if (vec && c + 8 <= n) {
+  if (c + 8 <= n) {
     if (sizeof(T) == 4 && vec == 2) {
       const uint32_t* w = reinterpret_cast<const uint32_t*>(r.v);
       asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
@@ -119,6 +162,55 @@ __device__ __forceinline__ void store8(T* row, int c, int n, int vec, const floa
 #pragma unroll
     for (int i = 0; i < 8; ++i)
       if (c + i < n) row[c + i] = e[i];
+  }
+}
+// The same, and without A for rows of any alignment, by a whole warp whose lanes hold
+// consecutive pieces of 8 columns (lanes without columns pass n <= c).  Lane l
+// stores the aligned 16-byte pieces that begin in its predecessor's elements
+// and end in its own; the row's (and the warp's) first and last elements go
+// one by one.
+template <bool A, class T>
+__device__ __forceinline__ void store8_any(T* row, int c, int n, int vec, const float (&v)[8]) {
+  if (A) {
+    store8(row, c, n, vec, v);
+    return;
+  }
+  constexpr int kWords = 2 * int(sizeof(T)), kPer = 16 / int(sizeof(T));
+  Raw8<T> r;
+  round8(v, r);
+  const uint32_t* own = reinterpret_cast<const uint32_t*>(r.v);
+  uint32_t w[kWords + 5];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[i] = __shfl_up_sync(0xffffffffu, own[kWords - 4 + i], 1);
+#pragma unroll
+  for (int i = 0; i < kWords; ++i) w[4 + i] = own[i];
+  w[kWords + 4] = 0u;
+  const int lane = threadIdx.x & 31;
+  const uintptr_t at = reinterpret_cast<uintptr_t>(row + c);
+  const uint32_t lead = uint32_t(at) & 15u;             // bytes from an aligned address to the first element
+  const T* e = reinterpret_cast<const T*>(r.v);
+  if (c + 8 > n) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (c + i < n) row[c + i] = e[i];
+    return;
+  }
+  shift_down<kWords, sizeof(T) == 2>(w, 16u - lead);
+  uint4* p = reinterpret_cast<uint4*>(at & ~uintptr_t(15));
+#pragma unroll
+  for (int i = 0; i < kWords / 4; ++i)
+    if (i > 0 || lane > 0 || lead == 0)
+      p[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+  const int head = kPer - int(lead / sizeof(T));        // own elements in the first aligned piece
+  if (lane == 0 && lead != 0) {
+#pragma unroll
+    for (int i = 0; i < kPer && i < 8; ++i)
+      if (i < head) row[c + i] = e[i];
+  }
+  if (lane == 31 || c + 16 > n) {                       // no successor stores this lane's last elements
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i >= 8 - int(lead / sizeof(T))) row[c + i] = e[i];
   }
 }
 // Code rows are 16-byte aligned, so 8 codes at a multiple of 8 are one word pair.
@@ -258,6 +350,10 @@ Ckpt ckpt(const int8_t* codes, int64_t ldc, const float* scales, int64_t cols, i
   return Ckpt{const_cast<int8_t*>(codes), ldc, const_cast<float*>(scales), int32_t(group_count(cols, group)),
               group_shift(group)};
 }
+
+// Call f(std::true_type) or f(std::false_type).
+template <class F>
+shampoo4_status by_flag(bool b, F f) { return b ? f(std::true_type{}) : f(std::false_type{}); }
 
 // Call f(T*) with a null pointer of the element type.
 template <class F>

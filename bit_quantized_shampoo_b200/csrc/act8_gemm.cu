@@ -78,6 +78,8 @@ struct Cfg {
 struct GemmArgs {
   CUtensorMap a, b;
   int32_t M, R, kblocks, tiles_m, tiles_r;
+  int32_t shares, share_blocks;            // pairs: parts of the contraction, k-blocks of each
+  int64_t share_stride;                    // and elements of Y from one part's sums to the next
   uint32_t* flags;
   Act8Out out;
 };
@@ -307,7 +309,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_act8_gemm(const __grid_cons
   if (C::CG == 2) cluster_sync();
   fence_after_sync();
   const uint32_t tmem = tmem_slot;
-  const int tiles = g.tiles_m * g.tiles_r, kblocks = g.kblocks;
+  const int shares = C::CHUNK ? g.shares : 1, items = g.tiles_m * g.tiles_r * shares, kblocks = g.kblocks;
   const int first = blockIdx.x / C::CG, step = gridDim.x / C::CG;
   const int chunk = C::CHUNK ? C::CHUNK : max(kblocks, 1);
 
@@ -321,11 +323,12 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_act8_gemm(const __grid_cons
     uint32_t phase = 1;                                     // of the stage's release before this fill
     bool ok = true, ready = false;
     wait_previous();
-    for (int t = first; ok && t < tiles; t += step) {
+    for (int t = first; ok && t < items; t += step) {
       int tm, tr;
-      tile_of(g, t, tm, tr);
+      tile_of(g, t / shares, tm, tr);
       const int m0 = (tm * C::CG + int(rank)) * kLanes, r0 = tr * C::R + int(rank) * C::kBRows;
-      for (int kb = 0; kb < kblocks; ++kb) {
+      const int kb_end = min(kblocks, (t % shares + 1) * g.share_blocks);
+      for (int kb = t % shares * g.share_blocks; kb < kb_end; ++kb) {
         if (!__all_sync(0xffffffffu, ready)) {
           ok = __all_sync(0xffffffffu, mbar_wait(&empty_bar[s], phase));
           if (!ok) break;
@@ -371,14 +374,16 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_act8_gemm(const __grid_cons
       int s = 0, i = 0;
       uint32_t phase = 0;
       bool ok = true, ready = false;                        // ready: the next stage's loads have landed already
-      for (int t = first; ok && t < tiles; t += step) {
-        for (int kb = 0; ok && (kb < kblocks || kb == 0); ++i) {
+      for (int t = first; ok && t < items; t += step) {
+        const int kb_end = min(kblocks, (t % shares + 1) * g.share_blocks);
+        bool some = true;                                   // no k-blocks at all: an empty sum
+        for (int kb = t % shares * g.share_blocks; ok && some; ++i) {
           const int ab = i & 1;
           ok = __all_sync(0xffffffffu, mbar_wait(&acc_empty[ab], ((i >> 1) & 1) ^ 1));
           if (!ok) break;
           fence_after_sync();
           const uint32_t d = tmem + uint32_t(ab * C::kAccCols);
-          const int k_end = min(kb + chunk, kblocks);
+          const int k_end = min(kb + chunk, kb_end);
           const int k_first = kb;
           for (; kb < k_end; ++kb) {
             if (!__all_sync(0xffffffffu, ready)) {
@@ -414,7 +419,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_act8_gemm(const __grid_cons
           }
           if (ok && elected()) commit<C::CG>(&acc_full[ab]);
           __syncwarp();
-          if (kblocks == 0) { ++i; break; }
+          some = kb < kb_end;
         }
       }
       // all MMAs issued are finished before tensor memory is freed
@@ -437,16 +442,19 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_act8_gemm(const __grid_cons
     bool ok = true;
     wait_previous();
     const float factor = g.out.factor ? __ldg(g.out.factor) : 1.0f;
-    for (int t = first; ok && t < tiles; t += step) {
+    for (int t = first; ok && t < items; t += step) {
       int tm, tr;
-      tile_of(g, t, tm, tr);
+      tile_of(g, t / shares, tm, tr);
       const int m = (tm * C::CG + int(rank)) * kLanes + 32 * q + lane, r0 = tr * C::R + 32 * c0;
       const float cs = g.out.col_scale && m < g.M ? __ldg(g.out.col_scale + m) : factor;
       const float bias = g.out.bias && m < g.M ? __ldg(g.out.bias + m) : 0.0f;
       float rs[kChunks];                                    // fetched under the products
 #pragma unroll
       for (int c = 0; c < kChunks; ++c) rs[c] = row_scale(g.out, g.R, r0 + 32 * c + lane);
-      const int passes = max(1, (kblocks + chunk - 1) / chunk);
+      const int share = t % shares, blocks = min(kblocks - share * g.share_blocks, g.share_blocks);
+      const int passes = max(1, (blocks + chunk - 1) / chunk);
+      Act8Out out = g.out;
+      if (C::CHUNK) out.y = static_cast<float*>(out.y) + (shares > 1 ? share * g.share_stride : 0);
       float sum[C::CHUNK ? kChunks : 1][32];
       for (int pass = 0; pass < passes; ++pass, ++i) {
         const int ab = i & 1;
@@ -498,7 +506,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_act8_gemm(const __grid_cons
 #pragma unroll
         for (int c = 0; c < kChunks; ++c)
           if (r0 + 32 * c < g.R)
-            store_any(g.out, g.R, g.M, r0 + 32 * c, m, cs, bias, rs[c], sum[c]);
+            store_any(out, g.R, g.M, r0 + 32 * c, m, cs, bias, rs[c], sum[c]);
       }
     }
   }
@@ -802,6 +810,8 @@ shampoo4_status fill_args(GemmArgs& g, const Act8Operand& a, int a_planes, const
   if (tm * tr > INT_MAX / 16) return SHAMPOO4_ERR_INVALID_ARG;
   g.tiles_m = int32_t(tm);
   g.tiles_r = int32_t(tr);
+  g.shares = 1;
+  g.share_blocks = g.kblocks;
   return SHAMPOO4_OK;
 }
 
@@ -827,16 +837,22 @@ shampoo4_status start(K kern, int threads, dim3 grid, dim3 cluster, int smem, bo
   return SHAMPOO4_OK;
 }
 
+// shares > 1: Y receives that many fp32 sums of R x M, one after the other.
 template <class C>
 shampoo4_status launch(const Act8Operand& a, const Act8Operand& b, int64_t M, int64_t R, int64_t K,
-                       const Act8Out& out, bool after_pass, uint32_t* flags, cudaStream_t st) {
+                       const Act8Out& out, bool after_pass, uint32_t* flags, cudaStream_t st, int shares = 1) {
   GemmArgs g{};
   S4_TRY(fill_args<C>(g, a, C::PA, b, C::PB * C::ND, M, R, K, out, flags));
+  if (shares > 1) {
+    g.share_blocks = (g.kblocks + shares - 1) / shares;
+    g.shares = shares;
+    g.share_stride = M * R;
+  }
   int dev = 0, sms = 0;
   S4_TRY(device_sms(&dev, &sms));
   auto kern = k_act8_gemm<C>;
   S4_TRY(allow_smem<C>(reinterpret_cast<const void*>(kern), dev));
-  const int tiles = g.tiles_m * g.tiles_r;
+  const int tiles = g.tiles_m * g.tiles_r * g.shares;
   return start(kern, kPairThreads, dim3(unsigned(C::CG * std::min(tiles, sms / C::CG))), dim3(C::CG), C::kSmem, after_pass, g, st);
 }
 
@@ -917,10 +933,27 @@ shampoo4_status launch_act8_bf16(const Act8Operand& a, const Act8Operand& b, int
               : launch<Bf16Cfg<false>>(a, b, M, R, K, out, true, flags, st);
 }
 
+// The estimated time (us): 0.5 per k-block and 2 per wave of tiles; the join
+// 3 and reading the sums.  Every share gets a k-block.
+int act8_halves_shares(int64_t M, int64_t R, int64_t K) {
+  const int64_t kb = (K + HalvesCfg<2, 4>::kK - 1) / HalvesCfg<2, 4>::kK;
+  const double tiles = double((M + 255) / 256) * double((R + HalvesCfg<2, 4>::R - 1) / HalvesCfg<2, 4>::R);
+  int best = 1;
+  double least = 0.0;
+  for (int64_t s = 1; s <= 32 && s <= kb; ++s) {
+    const int64_t per = (kb + s - 1) / s;
+    if ((kb + per - 1) / per != s) continue;
+    const double cost = std::ceil(tiles * double(s) / 74) * (0.5 * double(per) + 2.0) +
+                        (s > 1 ? 3.0 + double(s) * double(M) * double(R) * 1e-6 : 0.0);
+    if (s == 1 || cost < least) least = cost, best = int(s);
+  }
+  return best;
+}
+
 shampoo4_status launch_act8_halves(const Act8Operand& a, const Act8Operand& b, int b_parts, int64_t M, int64_t R,
-                                   int64_t K, const Act8Out& out, uint32_t* flags, cudaStream_t st) {
-  return b_parts == 1 ? launch<HalvesCfg<1, 5>>(a, b, M, R, K, out, true, flags, st)
-                      : launch<HalvesCfg<2, 4>>(a, b, M, R, K, out, true, flags, st);
+                                   int64_t K, int shares, const Act8Out& out, uint32_t* flags, cudaStream_t st) {
+  return b_parts == 1 ? launch<HalvesCfg<1, 5>>(a, b, M, R, K, out, true, flags, st, shares)
+                      : launch<HalvesCfg<2, 4>>(a, b, M, R, K, out, true, flags, st, shares);
 }
 
 }  // namespace s4

@@ -63,28 +63,31 @@ __device__ __forceinline__ uint32_t bytes4(uint32_t x0, uint32_t x1, uint32_t x2
   return __byte_perm(__byte_perm(x0, x1, sel), __byte_perm(x2, x3, sel), 0x5410);
 }
 
-// Rows of dY as they are (act8_input_grad): a CTA per row, read twice (the
-// second time from cache).
-template <class T>
+// Rows of dY as they are (act8_input_grad): a CTA per row, or a warp per row
+// of up to 1024 columns, read twice (the second time from cache).
+template <class T, bool WARP, bool A>
 __global__ void __launch_bounds__(kThreads)
 k_act8_digit_rows(Mat dy, const float* __restrict__ scale, int8_t* digits, int64_t ld, float* row_scale, int64_t rows,
                   int cols) {
   let_next_start();
   __shared__ uint32_t slots[kThreads / 32];
-  const int64_t row = blockIdx.x;
+  const int64_t row = WARP ? int64_t(blockIdx.x) * blockDim.y + threadIdx.y : int64_t(blockIdx.x);
+  if (row >= rows) return;                               // a whole warp, or nobody
   const T* x = static_cast<const T*>(dy.p) + row * dy.ld;
+  const int step = int(blockDim.x) * 8;
   Raw8<T> r;
   uint32_t m = 0;
-  for (int c = int(threadIdx.x) * 8; c < cols; c += kThreads * 8) {
-    load8(x, c, cols, dy.vec, r);
+  for (int c = int(threadIdx.x) * 8; c < cols; c += step) {
+    load8<A>(x, c, cols, dy.vec, r);
 #pragma unroll
     for (int i = 0; i < 8; ++i)
       if (c + i < cols) m = max(m, abs_bits(elt(r, i) * __ldg(scale + c + i)));
   }
-  const Fixed f(cta_max(m, slots));
+  if (WARP) __syncwarp();
+  const Fixed f(WARP ? __reduce_max_sync(0xffffffffu, m) : cta_max(m, slots));
   if (threadIdx.x == 0) row_scale[row] = f.scale;
-  for (int c = int(threadIdx.x) * 8; c < ld; c += kThreads * 8) {      // ld: the padding gets zeros
-    load8(x, c, cols, dy.vec, r);
+  for (int c = int(threadIdx.x) * 8; c < ld; c += step) {               // ld: the padding gets zeros
+    load8<A>(x, c, cols, dy.vec, r);
     uint32_t q[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) q[i] = c + i < cols ? digits_of(elt(r, i) * __ldg(scale + c + i), f.inv) : 0u;
@@ -104,7 +107,7 @@ k_act8_digit_rows(Mat dy, const float* __restrict__ scale, int8_t* digits, int64
 // digit row is written in pieces of 128 bytes.  A thread holds 4 tokens by 8
 // columns of a tile.
 constexpr int kColTile = 64, kTokTile = 128, kColCluster = 8;
-template <class T>
+template <class T, bool A>
 __global__ void __launch_bounds__(kThreads, 4)
 k_act8_digit_columns(Mat dy, const float* __restrict__ scale, int8_t* digits, int64_t ld, float* row_scale,
                      int64_t tokens, int64_t cols) {
@@ -122,7 +125,7 @@ k_act8_digit_columns(Mat dy, const float* __restrict__ scale, int8_t* digits, in
   __syncthreads();
 
   // This thread's 4 tokens by 8 columns of tile tt, and the tokens' scales.
-  const bool inside = dy.vec && c + 8 <= cols;
+  const bool inside = A && c + 8 <= cols;
   auto fetch = [&](int64_t tt, Raw8<T> (&r)[4], float (&s)[4]) {
     const int64_t t0 = tt * kTokTile + tgrp * 4;
     const T* p = x + t0 * dy.ld;
@@ -137,7 +140,7 @@ k_act8_digit_columns(Mat dy, const float* __restrict__ scale, int8_t* digits, in
     } else {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        load8(p + j * dy.ld, c, t0 + j < tokens ? int(cols) : 0, dy.vec, r[j]);
+        load8<A>(p + j * dy.ld, c, t0 + j < tokens ? int(cols) : 0, dy.vec, r[j]);
         s[j] = t0 + j < tokens ? __ldg(scale + t0 + j) : 0.0f;
       }
     }
@@ -228,7 +231,7 @@ __global__ void __launch_bounds__(kThreads) k_act8_align(Mat x, __nv_bfloat16* o
   const Piece<1> p;
   if (p.row >= rows || p.c >= cols) return;
   Raw8<__nv_bfloat16> r;
-  load8(static_cast<const __nv_bfloat16*>(x.p) + p.row * x.ld, p.c, cols, x.vec, r);
+  load8<false>(static_cast<const __nv_bfloat16*>(x.p) + p.row * x.ld, p.c, cols, 0, r);
   float v[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) v[i] = elt(r, i);
@@ -245,7 +248,7 @@ __device__ __forceinline__ uint32_t finite_bits(float x) {
   const uint32_t b = abs_bits(x);
   return b < 0x7f800000u ? b : 0u;
 }
-template <class T>
+template <class T, bool A>
 __global__ void __launch_bounds__(kThreads) k_act8_largest(Mat dy, const float* __restrict__ scales, int64_t nscales,
                                                            Largest* out, int64_t rows, int cols) {
   __shared__ uint32_t slots[kThreads / 32];
@@ -254,7 +257,7 @@ __global__ void __launch_bounds__(kThreads) k_act8_largest(Mat dy, const float* 
     const T* x = static_cast<const T*>(dy.p) + row * dy.ld;
     for (int c = int(threadIdx.x) * 8; c < cols; c += kThreads * 8) {
       Raw8<T> r;
-      load8(x, c, cols, dy.vec, r);
+      load8<A>(x, c, cols, dy.vec, r);
 #pragma unroll
       for (int i = 0; i < 8; ++i) m = max(m, finite_bits(elt(r, i)));
     }
@@ -293,7 +296,7 @@ __device__ __forceinline__ void store_halves(const float (&v)[8], float power, _
 
 // Both operands in one launch: blockIdx.z 0 the codes' values, 1 dY (the
 // column pieces of the wider one; the other's surplus warps leave).
-template <class T, int PARTS>
+template <class T, int PARTS, bool A>
 __global__ void __launch_bounds__(kThreads)
 k_act8_halves(Ckpt k, __half* co, int64_t ldco, int cols_c, Mat dy, __half* dyo, int64_t lddyo, int cols_dy,
               const Largest* largest, float* factor, int64_t rows) {
@@ -313,10 +316,24 @@ k_act8_halves(Ckpt k, __half* co, int64_t ldco, int cols_c, Mat dy, __half* dyo,
   } else {
     if (p.c >= cols_dy) return;
     Raw8<T> r;
-    load8(static_cast<const T*>(dy.p) + p.row * dy.ld, p.c, cols_dy, dy.vec, r);
+    load8<A>(static_cast<const T*>(dy.p) + p.row * dy.ld, p.c, cols_dy, dy.vec, r);
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = elt(r, i);
     store_halves<PARTS>(v, pd, dyo + p.row * lddyo, rows * lddyo, p.c, cols_dy);
+  }
+}
+
+// The shares' sums, added in order, into the result.
+template <class T>
+__global__ void __launch_bounds__(kThreads) k_act8_join(const float* __restrict__ sums, int shares, T* y, int64_t ldy,
+                                                        int accumulate, int64_t rows, int cols) {
+  const int64_t n = rows * cols;
+  for (int64_t i = int64_t(blockIdx.x) * kThreads + threadIdx.x; i < n; i += int64_t(gridDim.x) * kThreads) {
+    float v = __ldg(sums + i);
+    for (int k = 1; k < shares; ++k) v += __ldg(sums + k * n + i);
+    T* p = y + i / cols * ldy + i % cols;
+    if (accumulate) v += float(*p);
+    *p = T(v);
   }
 }
 
@@ -346,7 +363,9 @@ struct GradPlan {
   int dy_parts, code_parts;
   int64_t ld_dy, ld_code;        // elements
   size_t scale_bytes, dy_bytes, code_bytes;
-  size_t total() const { return scale_bytes + dy_bytes + code_bytes; }
+  int shares;                    // halves: parts of the contraction, and room for their sums
+  size_t sum_bytes;
+  size_t total() const { return scale_bytes + dy_bytes + code_bytes + sum_bytes; }
 };
 GradPlan grad_plan(bool weight, int32_t dtype, int32_t result, int32_t group, int64_t tokens, int64_t out,
                    int64_t inner) {
@@ -367,6 +386,10 @@ GradPlan grad_plan(bool weight, int32_t dtype, int32_t result, int32_t group, in
   // room for a copy of a bfloat16 dY whatever its alignment turns out to be
   p.dy_bytes = round_up(size_t(tokens) * p.ld_dy * 2 * p.dy_parts, 256);
   p.code_bytes = round_up(size_t(weight ? tokens : out) * p.ld_code * 2 * p.code_parts, 256);
+  if (p.path == kHalves) {
+    p.shares = act8_halves_shares(inner, out, tokens);
+    p.sum_bytes = p.shares > 1 ? round_up(size_t(p.shares) * out * inner * 4, 256) : 0;
+  }
   return p;
 }
 
@@ -375,8 +398,9 @@ shampoo4_status digit_pass(bool weight, const void* dy, int32_t dtype, int64_t l
                            cudaStream_t st) {
   const Mat m = mat(dy, lddy, dtype);
   const int64_t strips = (out + kColTile - 1) / kColTile;
-  return by_dtype(dtype, [&](auto* tag) -> shampoo4_status {
+  return by_dtype(dtype, [&](auto* tag) { return by_flag(m.vec != 0, [&](auto flag) -> shampoo4_status {
     using T = std::remove_pointer_t<decltype(tag)>;
+    constexpr bool A = decltype(flag)::value;
     if (weight) {
       unsigned ctas = 1;                                // per strip: no more than it has tiles
       while (ctas < kColCluster && int64_t(ctas) * kTokTile < tokens) ctas *= 2;
@@ -391,13 +415,18 @@ shampoo4_status digit_pass(bool weight, const void* dy, int32_t dtype, int64_t l
       attr[0].val.clusterDim.z = 1;
       cfg.attrs = attr;
       cfg.numAttrs = 1;
-      S4_CUDA(cudaLaunchKernelEx(&cfg, k_act8_digit_columns<T>, m, scale, digits, ld, row_scale, tokens, out));
+      S4_CUDA(cudaLaunchKernelEx(&cfg, (k_act8_digit_columns<T, A>), m, scale, digits, ld, row_scale, tokens, out));
     } else {
-      k_act8_digit_rows<T><<<unsigned(tokens), kThreads, 0, st>>>(m, scale, digits, ld, row_scale, tokens, int(out));
+      if (out <= 1024)
+        k_act8_digit_rows<T, true, A><<<unsigned((tokens + 7) / 8), dim3(32, 8), 0, st>>>(m, scale, digits, ld, row_scale,
+                                                                                      tokens, int(out));
+      else
+        k_act8_digit_rows<T, false, A><<<unsigned(tokens), kThreads, 0, st>>>(m, scale, digits, ld, row_scale, tokens,
+                                                                          int(out));
       S4_CUDA(cudaGetLastError());
     }
     return SHAMPOO4_OK;
-  });
+  }); });
 }
 
 shampoo4_status expand(const Ckpt& k, int64_t rows, int64_t cols, void* o, int64_t ld, cudaStream_t st) {
@@ -431,17 +460,18 @@ shampoo4_status halves_pass(const void* dy, int32_t dtype, int64_t lddy, const C
   if (!piece_grid(tokens, widest, b, 1, &g)) return SHAMPOO4_ERR_INVALID_ARG;
   g.z = 2;
   S4_CUDA(cudaMemsetAsync(largest, 0, sizeof(Largest), st));
-  return by_dtype(dtype, [&](auto* tag) -> shampoo4_status {
+  return by_dtype(dtype, [&](auto* tag) { return by_flag(m.vec != 0, [&](auto flag) -> shampoo4_status {
     using T = std::remove_pointer_t<decltype(tag)>;
-    k_act8_largest<T><<<unsigned(std::min<int64_t>(tokens, 148 * 4)), kThreads, 0, st>>>(
+    constexpr bool A = decltype(flag)::value;
+    k_act8_largest<T, A><<<unsigned(std::min<int64_t>(tokens, 148 * 4)), kThreads, 0, st>>>(
         m, k.scales, tokens * k.groups, largest, tokens, int(out));
     S4_CUDA(cudaGetLastError());
-    k_act8_halves<T, sizeof(T) == 4 ? 2 : 1><<<g, b, 0, st>>>(k, static_cast<__half*>(cp), ld_code, int(inner), m,
+    k_act8_halves<T, sizeof(T) == 4 ? 2 : 1, A><<<g, b, 0, st>>>(k, static_cast<__half*>(cp), ld_code, int(inner), m,
                                                              static_cast<__half*>(dyp), ld_dy, int(out), largest,
                                                              factor, tokens);
     S4_CUDA(cudaGetLastError());
     return SHAMPOO4_OK;
-  });
+  }); });
 }
 
 // Both gradients: weight: Y[out, inner] = dY^T X; else Y[tokens, inner] = dY W.
@@ -468,9 +498,22 @@ shampoo4_status grad(bool weight, const void* dy, int32_t dtype, int64_t lddy, c
     Largest* largest = reinterpret_cast<Largest*>(w);
     float* factor = reinterpret_cast<float*>(largest + 1);
     S4_TRY(halves_pass(dy, dtype, lddy, k, tokens, out, inner, largest, factor, dyp, p.ld_dy, cp, p.ld_code, st));
-    o.factor = factor;
-    return launch_act8_halves(Act8Operand{cp, p.ld_code, K}, Act8Operand{dyp, p.ld_dy, tokens}, p.dy_parts, inner, R,
-                              K, o, flags, st);
+    const Act8Operand a{cp, p.ld_code, K}, b{dyp, p.ld_dy, tokens};
+    if (p.shares == 1) {
+      o.factor = factor;
+      return launch_act8_halves(a, b, p.dy_parts, inner, R, K, 1, o, flags, st);
+    }
+    float* sums = reinterpret_cast<float*>(cp + p.code_bytes);
+    S4_TRY(launch_act8_halves(a, b, p.dy_parts, inner, R, K, p.shares,
+                              Act8Out{sums, inner, ACT8_FP32, 0, nullptr, nullptr, nullptr, factor}, flags, st));
+    const unsigned ctas = unsigned(std::min<int64_t>((R * inner + kThreads - 1) / kThreads, 148 * 8));
+    return by_dtype(o.dtype, [&](auto* tag) -> shampoo4_status {
+      using T = std::remove_pointer_t<decltype(tag)>;
+      k_act8_join<T><<<ctas, kThreads, 0, st>>>(sums, p.shares, static_cast<T*>(o.y), o.ld, o.accumulate, R,
+                                                int(inner));
+      S4_CUDA(cudaGetLastError());
+      return SHAMPOO4_OK;
+    });
   }
   Act8Operand b{dy, lddy, 0};
   if (!row_aligned(dy, lddy, dtype)) {

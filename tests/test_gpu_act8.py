@@ -275,7 +275,7 @@ def grad_tolerance(dy, codes, scales, group, dtype, result, weight):
 
 SHAPES = [(1, 1, 1), (1, 64, 300), (2, 7, 17), (63, 130, 65), (64, 128, 256), (65, 256, 257), (200, 129, 520),
           (513, 300, 96), (1100, 64, 128), (30, 1500, 700), (3000, 140, 260), (16, 500, 2900), (17, 2500, 130), (70, 1800, 1700),
-          (1800, 90, 1700)]
+          (1800, 90, 1700), (4100, 70, 33), (2000, 300, 90)]
 TYPES = [("bf16", "bf16"), ("bf16", "fp32"), ("fp16", "fp16"), ("fp32", "fp32"), ("bf16", "fp16"), ("fp32", "bf16")]
 
 
