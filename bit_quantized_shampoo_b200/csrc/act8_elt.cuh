@@ -292,9 +292,9 @@ template <int ROWS>
 struct Piece {
   int64_t row;       // the first row
   int c;             // this lane's first column
-  __device__ __forceinline__ Piece() {
+  __device__ __forceinline__ explicit Piece(unsigned block_y = blockIdx.y) {
     row = int64_t(blockIdx.x) * (blockDim.y * ROWS) + threadIdx.y;
-    c = int((blockIdx.y * (blockDim.x >> 5) + (threadIdx.x >> 5)) * kChunk + (threadIdx.x & 31) * 8);
+    c = int((block_y * (blockDim.x >> 5) + (threadIdx.x >> 5)) * kChunk + (threadIdx.x & 31) * 8);
   }
   __device__ __forceinline__ int64_t at(int u) const { return row + int64_t(u) * blockDim.y; }
 };

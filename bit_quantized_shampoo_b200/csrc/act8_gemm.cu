@@ -69,7 +69,7 @@ struct Cfg {
   static constexpr int kAccCols = kN <= 128 && !kSmallApart ? 128 : 256;   // columns from one accumulator to the other
   static_assert(!kSmallApart || 2 * kN <= kAccCols, "both sums fit");
   static constexpr int kTmemCols = 2 * kAccCols;
-  static_assert(kSmem <= 227 * 1024, "stages fit in shared memory");
+  static_assert(kSmem + 16 * R + 512 <= 227 * 1024, "stages, row scales and barriers fit in shared memory");
   static_assert(R % 64 == 0 && kN <= 256 && kN % 32 == 0 && kBRows % 8 == 0 && kBTile % 1024 == 0, "tile shape");
   static_assert(KIND != kI8 || (PA == 1 && PB == 1 && !B_MN), "integer operands");
   static_assert(KIND == kI8 || (ND == 1 && A_MN), "16-bit operands");
@@ -239,18 +239,55 @@ __device__ __forceinline__ void load_chunk(uint32_t tacc, int i, float (&v)[32])
   }
 }
 
+// Two 16-bit results in one word.
+__device__ __forceinline__ uint32_t pack_pair(__nv_bfloat16*, float lo, float hi) {
+  const __nv_bfloat162 x = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&x);
+}
+__device__ __forceinline__ uint32_t pack_pair(__half*, float lo, float hi) {
+  const __half2 x = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&x);
+}
+__device__ __forceinline__ uint32_t pack_pair(float*, float, float) { return 0u; }   // not used
+
 // 32 rows r0.. of column m to Y: a store instruction writes 32 consecutive
-// columns of a row.  A chunk inside the matrix goes out without a test per
-// row: with one, the warp waits for each row's shuffle in turn and the
-// epilogue, not the products, set the pace (391 against 265 us at 8192 x
-// 11008 x 4096).
+// columns of a row, or, of 16-bit results whose rows are 4-byte aligned, a
+// pair of columns per lane for two rows (neighbouring lanes swap two rows'
+// halves).  rs: the rows' scales in shared memory (null: none), read four at a
+// time.  A chunk inside the matrix goes out without a test per row.  The
+// epilogue is bound by shuffles, shared memory and store instructions: one
+// shuffle and one store per row took 5.5 us for a pair's tile of 256 rows, as
+// long as 2300 of contraction; this takes 4.3.
 template <class T>
 __device__ __forceinline__ void store_chunk(const Act8Out& o, int R, int M, int r0, int m, float cs, float bias,
-                                            float rs_lane, float (&v)[32]) {
+                                            const float* rs, float (&v)[32]) {
   T* y = static_cast<T*>(o.y) + int64_t(r0) * o.ld + m;
+  if (rs) {
 #pragma unroll
-  for (int j = 0; j < 32; ++j) v[j] = fmaf(v[j] * __shfl_sync(0xffffffffu, rs_lane, j), cs, bias);
-  if (!o.accumulate && r0 + 32 <= R && __all_sync(0xffffffffu, m < M)) {
+    for (int j = 0; j < 32; j += 4) {
+      const float4 s = *reinterpret_cast<const float4*>(rs + j);
+      v[j] *= s.x;
+      v[j + 1] *= s.y;
+      v[j + 2] *= s.z;
+      v[j + 3] *= s.w;
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < 32; ++j) v[j] = fmaf(v[j], cs, bias);
+  const bool whole = !o.accumulate && r0 + 32 <= R && __all_sync(0xffffffffu, m < M);
+  if (sizeof(T) == 2 && whole && ((reinterpret_cast<uintptr_t>(o.y) | uintptr_t(o.ld * 2)) & 3) == 0) {
+    const bool odd = m & 1;
+    uint32_t* p = reinterpret_cast<uint32_t*>(y - (odd ? 1 : 0) + (odd ? 2 : 0) * o.ld);   // even lanes rows 4k, odd 4k + 2
+    const int64_t step = o.ld / 2;                          // words
+#pragma unroll
+    for (int j = 0; j < 32; j += 4) {
+      const uint32_t a = pack_pair(y, v[j], v[j + 1]), b = pack_pair(y, v[j + 2], v[j + 3]);
+      const uint32_t mine = odd ? b : a, other = __shfl_xor_sync(0xffffffffu, odd ? a : b, 1);
+      const uint32_t left = odd ? other : mine, right = odd ? mine : other;   // columns m & ~1 and m | 1
+      p[j * step] = __byte_perm(left, right, 0x5410);
+      p[(j + 1) * step] = __byte_perm(left, right, 0x7632);
+    }
+  } else if (whole) {
 #pragma unroll
     for (int j = 0; j < 32; ++j) put(y + int64_t(j) * o.ld, v[j]);
   } else if (m < M) {
@@ -263,10 +300,10 @@ __device__ __forceinline__ void store_chunk(const Act8Out& o, int R, int M, int 
   }
 }
 __device__ __forceinline__ void store_any(const Act8Out& o, int R, int M, int r0, int m, float cs, float bias,
-                                          float rs_lane, float (&v)[32]) {
-  if (o.dtype == ACT8_FP32) store_chunk<float>(o, R, M, r0, m, cs, bias, rs_lane, v);
-  else if (o.dtype == ACT8_BF16) store_chunk<__nv_bfloat16>(o, R, M, r0, m, cs, bias, rs_lane, v);
-  else store_chunk<__half>(o, R, M, r0, m, cs, bias, rs_lane, v);
+                                          const float* rs, float (&v)[32]) {
+  if (o.dtype == ACT8_FP32) store_chunk<float>(o, R, M, r0, m, cs, bias, rs, v);
+  else if (o.dtype == ACT8_BF16) store_chunk<__nv_bfloat16>(o, R, M, r0, m, cs, bias, rs, v);
+  else store_chunk<__half>(o, R, M, r0, m, cs, bias, rs, v);
 }
 __device__ __forceinline__ float row_scale(const Act8Out& o, int R, int r) {
   return o.row_scale && r < R ? __ldg(o.row_scale + r) : 1.0f;
@@ -278,6 +315,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_act8_gemm(const __grid_cons
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ uint64_t full_bar[C::STAGES], empty_bar[C::STAGES], acc_full[2], acc_empty[2], done_bar;
   __shared__ uint32_t tmem_slot;
+  __shared__ __align__(16) float row_scales[8][C::R / 2];
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = C::CG == 2 ? cta_rank() : 0u;
@@ -448,9 +486,13 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_act8_gemm(const __grid_cons
       const int m = (tm * C::CG + int(rank)) * kLanes + 32 * q + lane, r0 = tr * C::R + 32 * c0;
       const float cs = g.out.col_scale && m < g.M ? __ldg(g.out.col_scale + m) : factor;
       const float bias = g.out.bias && m < g.M ? __ldg(g.out.bias + m) : 0.0f;
-      float rs[kChunks];                                    // fetched under the products
+      float* rs = g.out.row_scale ? row_scales[warp - 2] : nullptr;   // fetched under the products
+      if (rs) {
+        __syncwarp();
 #pragma unroll
-      for (int c = 0; c < kChunks; ++c) rs[c] = row_scale(g.out, g.R, r0 + 32 * c + lane);
+        for (int c = 0; c < kChunks; ++c) rs[32 * c + lane] = row_scale(g.out, g.R, r0 + 32 * c + lane);
+        __syncwarp();
+      }
       const int share = t % shares, blocks = min(kblocks - share * g.share_blocks, g.share_blocks);
       const int passes = max(1, (blocks + chunk - 1) / chunk);
       Act8Out out = g.out;
@@ -487,7 +529,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_act8_gemm(const __grid_cons
 #pragma unroll
               for (int j = 0; j < 32; ++j) v[j] = 0.0f;
             }
-            store_any(g.out, g.R, g.M, r0 + 32 * c, m, cs, bias, rs[c], v);
+            store_any(g.out, g.R, g.M, r0 + 32 * c, m, cs, bias, rs ? rs + 32 * c : nullptr, v);
           }
         }
         fence_before_sync();
@@ -506,7 +548,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_act8_gemm(const __grid_cons
 #pragma unroll
         for (int c = 0; c < kChunks; ++c)
           if (r0 + 32 * c < g.R)
-            store_any(out, g.R, g.M, r0 + 32 * c, m, cs, bias, rs[c], sum[c]);
+            store_any(out, g.R, g.M, r0 + 32 * c, m, cs, bias, rs ? rs + 32 * c : nullptr, sum[c]);
       }
     }
   }
@@ -560,7 +602,7 @@ struct SmallCfg {
   static constexpr int kSmem = STAGES * kStage + 1024;
   static_assert(kN % 16 == 0 && kN <= 256 && kBTile % 1024 == 0, "tile shape");
   static_assert(kCols * kLanes * 4 <= STAGES * kStage, "the partial sums reuse the stages");
-  static_assert(2 * (kSmem + 1024 + 256) <= 228 * 1024, "two CTAs per SM");
+  static_assert(2 * (kSmem + 1024 + 1024) <= 228 * 1024, "two CTAs per SM");
 };
 
 template <class C>
@@ -569,6 +611,7 @@ __global__ void __launch_bounds__(kSmallThreads, 2) k_act8_small(const __grid_co
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ uint64_t full_bar[C::STAGES], empty_bar[C::STAGES], done_bar;
   __shared__ uint32_t tmem_slot;
+  __shared__ __align__(16) float scales[4][32];
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int shares = gridDim.y, share = blockIdx.y;           // the cluster lies along y
@@ -672,7 +715,10 @@ __global__ void __launch_bounds__(kSmallThreads, 2) k_act8_small(const __grid_co
             for (int j = 0; j < 32; ++j) v[j] = fmaf(v[j], 256.0f, __int2float_rn(int(r[j])));
           }
         }
-        store_any(g.out, min(g.R, r0 + C::R), g.M, r0 + c, m, cs, bias, row_scale(g.out, g.R, r0 + c + lane), v);
+        __syncwarp();
+        scales[warp - 2][lane] = c + lane < C::R ? row_scale(g.out, g.R, r0 + c + lane) : 1.0f;
+        __syncwarp();
+        store_any(g.out, min(g.R, r0 + C::R), g.M, r0 + c, m, cs, bias, scales[warp - 2], v);
       }
       fence_before_sync();
     }
@@ -898,9 +944,9 @@ Form choose_form(int64_t M, int64_t R, int64_t K, int pair_rows, int digits, con
 }  // namespace
 
 //                               kind   A_MN   B_MN   R   PA PB ND CG stages chunk
-using CodesCfg = Cfg<            kI8,   false, false, 256, 1, 1, 1, 2, 7, 0>;
+using CodesCfg = Cfg<            kI8,   false, false, 256, 1, 1, 1, 2, 6, 0>;
 using DigitsCfg = Cfg<           kI8,   true,  false, 64,  1, 1, kAct8Digits, 2, 8, 1024>;
-template <bool B_MN> using Bf16Cfg = Cfg<kBf16, true, B_MN, 256, 1, 1, 1, 2, 7, 0>;
+template <bool B_MN> using Bf16Cfg = Cfg<kBf16, true, B_MN, 256, 1, 1, 1, 2, 6, 0>;
 template <int PB, int STAGES>
 using HalvesCfg = Cfg<           kHalf, true,  true,  128, 2, PB, 1, 2, STAGES, 4>;
 

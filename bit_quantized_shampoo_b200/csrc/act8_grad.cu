@@ -65,6 +65,16 @@ __device__ __forceinline__ uint32_t bytes4(uint32_t x0, uint32_t x1, uint32_t x2
 
 // Rows of dY as they are (act8_input_grad): a CTA per row, or a warp per row
 // of up to 1024 columns, read twice (the second time from cache).
+__device__ __forceinline__ void scales8(const float* s, int c, int n, bool vec, float (&v)[8]) {
+  if (vec && c + 8 <= n) {
+    const float4 a = __ldg(reinterpret_cast<const float4*>(s + c)), b = __ldg(reinterpret_cast<const float4*>(s + c + 4));
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = c + i < n ? __ldg(s + c + i) : 0.0f;
+  }
+}
 template <class T, bool WARP, bool A>
 __global__ void __launch_bounds__(kThreads)
 k_act8_digit_rows(Mat dy, const float* __restrict__ scale, int8_t* digits, int64_t ld, float* row_scale, int64_t rows,
@@ -75,22 +85,29 @@ k_act8_digit_rows(Mat dy, const float* __restrict__ scale, int8_t* digits, int64
   if (row >= rows) return;                               // a whole warp, or nobody
   const T* x = static_cast<const T*>(dy.p) + row * dy.ld;
   const int step = int(blockDim.x) * 8;
+  const bool vec = (reinterpret_cast<uintptr_t>(scale) & 15) == 0;
   Raw8<T> r;
+  float s[8];
   uint32_t m = 0;
-  for (int c = int(threadIdx.x) * 8; c < cols; c += step) {
+#pragma unroll 2
+  for (int c = int(threadIdx.x) * 8; c < cols; c += step) {   // past the last column: 0 * 0
     load8<A>(x, c, cols, dy.vec, r);
+    scales8(scale, c, cols, vec, s);
+    float y[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (c + i < cols) m = max(m, abs_bits(elt(r, i) * __ldg(scale + c + i)));
+    for (int i = 0; i < 8; ++i) y[i] = elt(r, i) * s[i];
+    const float a = absmax3_nan(y[0], y[1], y[2]), b = absmax3_nan(y[3], y[4], y[5]);
+    m = max(m, abs_bits(max2_nan(absmax3_nan(a, y[6], y[7]), b)));
   }
   if (WARP) __syncwarp();
   const Fixed f(WARP ? __reduce_max_sync(0xffffffffu, m) : cta_max(m, slots));
   if (threadIdx.x == 0) row_scale[row] = f.scale;
   for (int c = int(threadIdx.x) * 8; c < ld; c += step) {               // ld: the padding gets zeros
     load8<A>(x, c, cols, dy.vec, r);
+    scales8(scale, c, cols, vec, s);
     uint32_t q[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) q[i] = c + i < cols ? digits_of(elt(r, i) * __ldg(scale + c + i), f.inv) : 0u;
+    for (int i = 0; i < 8; ++i) q[i] = digits_of(elt(r, i) * s[i], f.inv);
 #pragma unroll
     for (int d = 0; d < kAct8Digits; ++d) {
       const int b = kAct8Digits - 1 - d;
@@ -294,20 +311,21 @@ __device__ __forceinline__ void store_halves(const float (&v)[8], float power, _
   if (PARTS == 2) store8(o + plane, c, cols, 1, lo);
 }
 
-// Both operands in one launch: blockIdx.z 0 the codes' values, 1 dY (the
-// column pieces of the wider one; the other's surplus warps leave).
+// Both operands in one launch: the first code_blocks of blockIdx.y the codes'
+// values, the others dY.
 template <class T, int PARTS, bool A>
 __global__ void __launch_bounds__(kThreads)
 k_act8_halves(Ckpt k, __half* co, int64_t ldco, int cols_c, Mat dy, __half* dyo, int64_t lddyo, int cols_dy,
-              const Largest* largest, float* factor, int64_t rows) {
+              const Largest* largest, float* factor, int64_t rows, unsigned code_blocks) {
   let_next_start();
-  const Piece<1> p;
+  const bool codes = blockIdx.y < code_blocks;
+  const Piece<1> p(codes ? blockIdx.y : blockIdx.y - code_blocks);
   const float pc = value_power(largest), pd = power_to(largest->dy);
-  if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0 && threadIdx.x == 0 && threadIdx.y == 0)
+  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0 && threadIdx.y == 0)
     *factor = (1.0f / pc) * (1.0f / pd);
   if (p.row >= rows) return;
   float v[8];
-  if (blockIdx.z == 0) {
+  if (codes) {
     if (p.c >= cols_c) return;
     uint2 w;
     load_codes8(k.codes + p.row * k.ldc, p.c, cols_c, w);
@@ -454,11 +472,11 @@ shampoo4_status halves_pass(const void* dy, int32_t dtype, int64_t lddy, const C
                             int64_t inner, Largest* largest, float* factor, void* dyp, int64_t ld_dy, void* cp,
                             int64_t ld_code, cudaStream_t st) {
   const Mat m = mat(dy, lddy, dtype);
-  const int64_t widest = std::max(out, inner);
-  const dim3 b = piece_block(widest);
-  dim3 g;
-  if (!piece_grid(tokens, widest, b, 1, &g)) return SHAMPOO4_ERR_INVALID_ARG;
-  g.z = 2;
+  const dim3 b = piece_block(std::max(out, inner));
+  dim3 g, gc;
+  if (!piece_grid(tokens, out, b, 1, &g) || !piece_grid(tokens, inner, b, 1, &gc) || g.y + gc.y > 65535)
+    return SHAMPOO4_ERR_INVALID_ARG;
+  g.y += gc.y;
   S4_CUDA(cudaMemsetAsync(largest, 0, sizeof(Largest), st));
   return by_dtype(dtype, [&](auto* tag) { return by_flag(m.vec != 0, [&](auto flag) -> shampoo4_status {
     using T = std::remove_pointer_t<decltype(tag)>;
@@ -468,7 +486,7 @@ shampoo4_status halves_pass(const void* dy, int32_t dtype, int64_t lddy, const C
     S4_CUDA(cudaGetLastError());
     k_act8_halves<T, sizeof(T) == 4 ? 2 : 1, A><<<g, b, 0, st>>>(k, static_cast<__half*>(cp), ld_code, int(inner), m,
                                                              static_cast<__half*>(dyp), ld_dy, int(out), largest,
-                                                             factor, tokens);
+                                                             factor, tokens, gc.y);
     S4_CUDA(cudaGetLastError());
     return SHAMPOO4_OK;
   }); });
