@@ -346,7 +346,9 @@ def quant4_tables(codebook="linear_square"):
 # 16-byte aligned), scales fp32 (rows x groups); group 0 means one scale per
 # row, else 32, 64, 128 or 256 columns share one.  Matrices are 2-D CUDA
 # tensors with unit column stride.  Results may be given (``out``) or are
-# allocated; ``stream`` defaults to the current stream of the tensors' device.
+# allocated, and must not overlap inputs; ``stream`` defaults to the current
+# stream of the tensors' device (another one has to wait for the current one
+# before the call, and the current one for it before the results are used).
 # Arguments that do not fit raise TypeError or ValueError before anything is
 # enqueued.  The checks and calls are in csrc/act8_binding.cpp: the smallest
 # of these calls take a few microseconds, less than the same checks in Python.

@@ -356,7 +356,7 @@ k_act8_swiglu_backward(Mat dh, Ckpt kg, Ckpt ku, T* dg, int64_t lddg, int vecg, 
     for (int i = 0; i < 8; ++i) {
       const float x = elt(d[k], i), sig = sigmoid<T>(g[i]);
       ou[i] = x * (g[i] * sig);
-      og[i] = x * u[i] * (sig * fmaf(g[i], 1.0f - sig, 1.0f));
+      og[i] = x * (u[i] * (sig * fmaf(g[i], 1.0f - sig, 1.0f)));   // the slope first: dh up may pass fp32's range
     }
     store8_any<A>(dg + row * lddg, p.c, n, vecg, og);
     store8_any<A>(du + row * lddu, p.c, n, vecu, ou);

@@ -6,7 +6,8 @@
 //
 // Every function takes positional arguments only (api.py gives them names and
 // defaults) and follows the same order: check, allocate (results on the
-// current stream, scratch on the call's stream), call on the tensors' device.
+// current stream, and kept for the call's stream; scratch on the call's
+// stream), call on the tensors' device.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 #include <ATen/ATen.h>
@@ -234,6 +235,10 @@ struct Where {
     Py_DECREF(raw);
     if (!st && PyErr_Occurred()) throw Refused();
   }
+  // A fresh result dropped while this stream still writes it stays allocated.
+  void keep(const at::Tensor& t) const {
+    if (given && t.defined()) t.record_stream(c10::cuda::getStreamFromExternal(st, device.index()).unwrap());
+  }
   shampoo4_stream_t stream() const { return reinterpret_cast<shampoo4_stream_t>(st); }
   // Scratch that the caching allocator keeps for the work on this stream.
   at::Tensor scratch(int64_t bytes) const {
@@ -302,6 +307,8 @@ PyObject* pack(PyObject*, PyObject* const* a, Py_ssize_t n) {
     }
     const Where w(x.device, a[4]);
     check("act8_pack", act8_pack(x.p, x.dtype, x.rows, x.cols, x.ld, int32_t(group), k.p, k.ld, k.scales, w.stream()));
+    w.keep(s.codes);
+    w.keep(s.scales);
     if (a[2] != Py_None) return PyTuple_Pack(2, a[2], a[3]);
     return pair(THPVariable_Wrap(s.codes), THPVariable_Wrap(s.scales));
   });
@@ -317,6 +324,7 @@ PyObject* unpack(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Where w(k.device, a[5]);
     check("act8_unpack", act8_unpack(k.p, k.ld, k.scales, k.rows, k.cols, int32_t(group), o.m.p, o.m.dtype, o.m.ld,
                                      w.stream()));
+    w.keep(o.made);
     return o.object();
   });
 }
@@ -333,6 +341,7 @@ PyObject* matmul(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Where w(x.device, a[8]);
     check("act8_matmul", act8_matmul(x.p, x.ld, x.scales, k.p, k.ld, k.scales, bias, x.rows, outs, x.cols, o.m.p,
                                      o.m.dtype, o.m.ld, flags, w.stream()));
+    w.keep(o.made);
     return o.object();
   });
 }
@@ -365,6 +374,9 @@ PyObject* linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
     }
     check("act8_linear", act8_linear(x.p, x.dtype, x.ld, k.p, k.ld, k.scales, bias, x.rows, outs, x.cols, c.p, c.ld,
                                      c.scales, o.m.p, o.m.dtype, o.m.ld, flags, w.stream()));
+    w.keep(o.made);
+    w.keep(s.codes);
+    w.keep(s.scales);
     if (!keep) return o.object();
     PyObject* r = PyTuple_New(3);
     if (!r) throw Refused();
@@ -405,6 +417,7 @@ PyObject* grad(PyObject*, PyObject* const* a, Py_ssize_t n) {
       check("act8_input_grad", act8_input_grad(dy.p, dy.dtype, dy.ld, k.p, k.ld, k.scales, dy.rows, dy.cols, k.cols,
                                                o.m.p, o.m.dtype, o.m.ld, add, work.data_ptr(), bytes, flags,
                                                w.stream()));
+    w.keep(o.made);
     return o.object();
   });
 }
@@ -424,6 +437,11 @@ PyObject* swiglu(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Where w(g.device, a[4]);
     check("act8_swiglu", act8_swiglu(g.p, g.ld, u.p, u.ld, g.dtype, g.rows, g.cols, int32_t(group), o.m.p, o.m.ld,
                                      sg.k.p, sg.k.ld, sg.k.scales, su.k.p, su.k.ld, su.k.scales, w.stream()));
+    w.keep(o.made);
+    for (const Store* s : {&sg, &su}) {
+      w.keep(s->codes);
+      w.keep(s->scales);
+    }
     PyObject* kept = PyTuple_New(4);
     if (!kept) throw Refused();
     PyTuple_SET_ITEM(kept, 0, THPVariable_Wrap(sg.codes));
@@ -454,6 +472,8 @@ PyObject* swiglu_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     check("act8_swiglu_backward",
           act8_swiglu_backward(d.p, d.ld, d.dtype, g.p, g.ld, g.scales, u.p, u.ld, u.scales, d.rows, d.cols,
                                int32_t(group), og.m.p, og.m.ld, ou.m.p, ou.m.ld, w.stream()));
+    w.keep(og.made);
+    w.keep(ou.made);
     return pair(og.object(), ou.object());
   });
 }

@@ -479,7 +479,9 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_act8_gemm(const __grid_cons
     int i = 0;
     bool ok = true;
     wait_previous();
-    const float factor = g.out.factor ? __ldg(g.out.factor) : 1.0f;
+    // one after the other: their product may lie outside fp32 where the result does not
+    const bool scaled = C::KIND == kHalf && g.out.factor;
+    const float factor = scaled ? __ldg(g.out.factor) : 1.0f, factor2 = scaled ? __ldg(g.out.factor + 1) : 1.0f;
     for (int t = first; ok && t < items; t += step) {
       int tm, tr;
       tile_of(g, t / shares, tm, tr);
@@ -546,9 +548,14 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_act8_gemm(const __grid_cons
       }
       if (C::CHUNK && ok) {
 #pragma unroll
-        for (int c = 0; c < kChunks; ++c)
-          if (r0 + 32 * c < g.R)
-            store_any(out, g.R, g.M, r0 + 32 * c, m, cs, bias, rs ? rs + 32 * c : nullptr, sum[c]);
+        for (int c = 0; c < kChunks; ++c) {
+          if (r0 + 32 * c >= g.R) break;
+          if (C::KIND == kHalf) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) sum[c][j] *= factor2;
+          }
+          store_any(out, g.R, g.M, r0 + 32 * c, m, cs, bias, rs ? rs + 32 * c : nullptr, sum[c]);
+        }
       }
     }
   }

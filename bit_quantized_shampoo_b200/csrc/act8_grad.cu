@@ -288,14 +288,16 @@ __global__ void __launch_bounds__(kThreads) k_act8_largest(Mat dy, const float* 
   if (threadIdx.x == 0) atomicMax(&out->scale, s);
 }
 
-// 2^e with 2^13 < 2^e x < 2^15 for the x of these bits (1 for zero), within
-// the exponents whose powers and inverses are normal.
-__device__ __forceinline__ float power_to(uint32_t bits) {
-  const int e = bits == 0u ? 0 : min(max(14 + 127 - int(bits >> 23), -126), 126);
-  return __uint_as_float(uint32_t(127 + e) << 23);
+// The e with 2^13 < 2^e x < 2^15 for the x of these bits (0 for zero), within
+// the exponents whose powers are normal.
+__device__ __forceinline__ int power_to(uint32_t bits) {
+  return bits == 0u ? 0 : min(max(14 + 127 - int(bits >> 23), -126), 126);
 }
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float(uint32_t(127 + e) << 23); }
 // A value's largest is its scale's 127-fold, 2^7 of it.
-__device__ __forceinline__ float value_power(const Largest* l) { return power_to(l->scale == 0u ? 0u : min(l->scale + (7u << 23), 0x7f000000u)); }
+__device__ __forceinline__ int value_power(const Largest* l) {
+  return power_to(l->scale == 0u ? 0u : min(l->scale + (7u << 23), 0x7f000000u));
+}
 
 template <int PARTS>
 __device__ __forceinline__ void store_halves(const float (&v)[8], float power, __half* o, int64_t plane, int c,
@@ -320,9 +322,13 @@ k_act8_halves(Ckpt k, __half* co, int64_t ldco, int cols_c, Mat dy, __half* dyo,
   let_next_start();
   const bool codes = blockIdx.y < code_blocks;
   const Piece<1> p(codes ? blockIdx.y : blockIdx.y - code_blocks);
-  const float pc = value_power(largest), pd = power_to(largest->dy);
-  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0 && threadIdx.y == 0)
-    *factor = (1.0f / pc) * (1.0f / pd);
+  const int ec = value_power(largest), ed = power_to(largest->dy);
+  const float pc = pow2(ec), pd = pow2(ed);
+  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0 && threadIdx.y == 0) {
+    const int e = -(ec + ed);                            // up to 252: two factors of half the exponent
+    factor[0] = pow2(e >> 1);
+    factor[1] = pow2(e - (e >> 1));
+  }
   if (p.row >= rows) return;
   float v[8];
   if (codes) {
@@ -374,7 +380,7 @@ GradPath grad_path(int32_t dtype, int32_t result, int32_t group, int64_t rows, i
 size_t round_up(size_t n, size_t a) { return (n + a - 1) / a * a; }
 
 // Workspace of a gradient: scales (digits) or the largest magnitudes and the
-// result's factor (halves), dY (tokens x out) in the form its product takes,
+// result's factors (halves), dY (tokens x out) in the form its product takes,
 // then, but for digits, the codes' values (code_rows x inner) in 16 bits.
 struct GradPlan {
   GradPath path;
@@ -466,7 +472,7 @@ shampoo4_status align_dy(const void* x, int64_t ldx, int64_t rows, int64_t cols,
   return SHAMPOO4_OK;
 }
 
-// Both operands as halves at dyp and cp; the result's factor next to the
+// Both operands as halves at dyp and cp; the result's factors next to the
 // largest magnitudes at `largest`.
 shampoo4_status halves_pass(const void* dy, int32_t dtype, int64_t lddy, const Ckpt& k, int64_t tokens, int64_t out,
                             int64_t inner, Largest* largest, float* factor, void* dyp, int64_t ld_dy, void* cp,

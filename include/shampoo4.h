@@ -601,7 +601,7 @@ shampoo4_status act8_input_grad(const void* d_dy, int32_t dtype, int64_t lddy, c
  * `dtype`, fp32 arithmetic rounded once), which keeps gate and up as 8-bit
  * codes in the same pass; and its gradients from those codes:
  *   dup = dh gate sig,   dgate = dh up sig (1 + gate (1 - sig)),
- *   sig = sigmoid(gate). */
+ *   sig = sigmoid(gate) (below 2^-126 it counts as 0). */
 shampoo4_status act8_swiglu(const void* d_gate, int64_t ldg, const void* d_up, int64_t ldu, int32_t dtype,
                             int64_t rows, int64_t cols, int32_t group, void* d_h, int64_t ldh, int8_t* d_gate_codes,
                             int64_t ldgc, float* d_gate_scales, int8_t* d_up_codes, int64_t lduc, float* d_up_scales,

@@ -427,6 +427,26 @@ def test_fp32_gradient_of_huge_values_stays_finite():
     within(f64(dw), np.full((4, 8), float(np.float32(3.4e38)) * 127 * float(scales[0, 0])), 3.4e38 * 2.0 ** -13)
 
 
+@pytest.mark.parametrize("tokens", [60, 1000])                # the contraction whole, and split
+def test_grouped_gradient_of_tiny_and_huge_values(tokens):
+    """The powers that scale the two operands multiply to more than fp32
+    holds, where the result does not."""
+    api = _api()
+    x, codes, scales = stored(tokens, 96, 70, 32, 1e-20)
+    dy = data(tokens, 40, "fp32", 71, scale=1e-18).abs()
+    dw = api.act8_weight_grad(dy, *x, group=32)
+    want = f64(dy).T @ A.values64(codes, scales, 32)
+    within(f64(dw), want, grad_tolerance(f64(dy), codes, scales, 32, "fp32", "fp32", True)
+           + half_step("fp32") * np.abs(want))
+    assert dw.abs().max() > 1e-37
+    x, codes, scales = stored(tokens, 96, 70, 32, 1e30)
+    dy = data(tokens, 40, "fp32", 71, scale=1e30)
+    dy[:, 3] = 0
+    dw = api.act8_weight_grad(dy, *x, group=32)
+    # the products overflow (1e60): infinite, or NaN where a split contraction's sums are infinite with both signs
+    assert torch.all(dw[3] == 0) and not torch.isfinite(dw[:3]).any() and not torch.isfinite(dw[4:]).any()
+
+
 # --------------------------------------------------------- gated activation
 
 def swiglu_tol(dtype, want, extra=0.0):
@@ -492,6 +512,20 @@ def test_swiglu_saturates():
     within(f64(h), A.swiglu(f64(gate), f64(up)), np.abs(A.swiglu(f64(gate), f64(up))) * 2.0 ** -21 + 1e-36)
     dg, du = api.act8_swiglu_backward(torch.ones_like(gate), kept)
     assert torch.isfinite(dg).all() and torch.isfinite(du).all()
+
+
+def test_swiglu_gradient_where_dh_up_passes_the_range():
+    """dh up overflows fp32, dgate does not (gate -60).  The exponential moves
+    by 60 times its argument's 2^-24; 16 more roundings of 2^-24 follow."""
+    api = _api()
+    gate = torch.full((4, 40), -60.0, device="cuda")
+    up, dh = torch.full_like(gate, 1e25), torch.full_like(gate, 1e25)
+    _, kept = api.act8_swiglu(gate, up, group=32)
+    g, u = (A.values64(c.cpu().numpy(), s.cpu().numpy(), 32) for c, s in (kept[:2], kept[2:]))
+    dg, du = api.act8_swiglu_backward(dh, kept, group=32)
+    want_g, want_u = A.swiglu_grad(f64(dh), g, u)
+    within(f64(dg), want_g, np.abs(want_g) * 76 * 2.0 ** -24)
+    within(f64(du), want_u, np.abs(want_u) * 76 * 2.0 ** -24)
 
 
 # ------------------------------------------------------------- used together
@@ -614,6 +648,25 @@ def test_explicit_stream_argument():
     side.synchronize()
     assert torch.equal(y, api.act8_linear(x, *ws[0][0]))
     assert torch.equal(dw, api.act8_weight_grad(dy, c, s))
+
+
+def test_results_dropped_early_stay_with_the_given_stream():
+    """Results made for another stream and dropped at once: what is allocated
+    next must not share their memory while that stream still writes."""
+    api = _api()
+    side = torch.cuda.Stream()
+    x = data(4096, 4096, "fp32", 95)
+    codes, scales = api.act8_pack(x)
+    torch.cuda.synchronize()
+    bad = 0
+    for _ in range(5):
+        for _ in range(4):
+            api.act8_unpack(codes, scales, stream=side)
+        mark = torch.full((4096, 4096), 3.0, device="cuda")
+        side.synchronize()
+        bad += int((mark != 3.0).any())
+        del mark
+    assert bad == 0
 
 
 def test_two_streams_at_once_do_not_mix():
