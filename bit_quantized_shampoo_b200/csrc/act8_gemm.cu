@@ -19,7 +19,11 @@
 // results of a row without a transposing pass.  Digits are stacked along the
 // MMA's N, so A is read once for all three.  The accumulator is
 // double-buffered in tensor memory: one tile's epilogue runs under the next
-// one's products.  The pairs are persistent, one CTA per SM.
+// one's products.  The pairs are persistent, one CTA per SM.  Bound by the
+// tensor cores, and in a loop by the power cap: 8192 x 11008 x 4096 codes 215
+// us alone (3.4 POPS), 227 to 239 in a loop; its weight gradient in digits 648
+// us alone (3.4 POPS of three products), bfloat16 453 us (1.63 PFLOP/s); the
+// tensor pipe is 88 to 92% busy where tiles fill the waves.
 //
 // Warp roles (320 threads): warp 0 issues the TMA loads, warp 1 of the leader
 // the MMAs, warps 2..9 drain the accumulator, two per lane quarter with half of
@@ -596,6 +600,8 @@ __device__ __forceinline__ void store_row4(const Act8Out& o, int r, int m, int M
 // shares fill the SMs, two CTAs each; their integer partial sums meet in
 // shared memory, each CTA of the cluster finishing R / cluster rows (exact,
 // so the split changes no result).  Same roles as above, warps 2..5 finish.
+// One row, 4096 x 4096: 10 us with cold caches, 7.4 with the row's
+// quantization where W is in L2; 13 rows, 11008 x 4096: 14 us cold, 3.2 TB/s.
 template <bool A_MN_, int R_, int ND_, int STAGES_>
 struct SmallCfg {
   static constexpr int KIND = kI8, R = R_, ND = ND_, CG = 1, STAGES = STAGES_;
