@@ -272,6 +272,8 @@ __device__ __forceinline__ uint32_t cta_max(uint32_t m, uint32_t* slots) {
 // The product enqueued next may be launched now (it waits for this kernel's
 // results itself).
 __device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+// The results of the pass enqueued before are there.
+__device__ __forceinline__ void wait_for_pass() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 struct Mat {
   const void* p;

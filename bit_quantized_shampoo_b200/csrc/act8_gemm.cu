@@ -553,12 +553,13 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_act8_gemm(const __grid_cons
       if (C::CHUNK && ok) {
 #pragma unroll
         for (int c = 0; c < kChunks; ++c) {
-          if (r0 + 32 * c >= g.R) break;
-          if (C::KIND == kHalf) {
+          if (r0 + 32 * c < g.R) {
+            if (C::KIND == kHalf) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j) sum[c][j] *= factor2;
+              for (int j = 0; j < 32; ++j) sum[c][j] *= factor2;
+            }
+            store_any(out, g.R, g.M, r0 + 32 * c, m, cs, bias, rs ? rs + 32 * c : nullptr, sum[c]);
           }
-          store_any(out, g.R, g.M, r0 + 32 * c, m, cs, bias, rs ? rs + 32 * c : nullptr, sum[c]);
         }
       }
     }

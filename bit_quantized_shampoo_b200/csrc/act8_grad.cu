@@ -243,6 +243,7 @@ __global__ void __launch_bounds__(kThreads) k_act8_expand(Ckpt k, __nv_bfloat16*
   float v[8];
   values8(w, __ldg(k.scales + p.row * k.groups + (p.c >> k.shift)), v);
   store8(o + p.row * ld, p.c, cols, 1, v);
+  wait_for_pass();                       // nothing of it is read here, but the product relies on both
 }
 // A bfloat16 dY with rows that are not 16-byte aligned, copied to rows that are
 // (8192 x 4096: 22 us, 6.2 TB/s).
@@ -260,9 +261,11 @@ __global__ void __launch_bounds__(kThreads) k_act8_align(Mat x, __nv_bfloat16* o
 
 // ---- halves
 
-// Bits of the largest finite magnitudes, for both operands, zeroed by the
-// caller: [0] of the scales, [1] of dY (elements that are not finite do not
-// count: they stay so whatever the factor).
+// Bits of the largest finite magnitudes, for both operands (elements that are
+// not finite do not count: they stay so whatever the factor).  `lanes` threads
+// share a row of dY, four rows in flight.  Up to 8 CTAs are a cluster and join
+// their maxima in shared memory; more raise the words at `out` (an integer
+// maximum: the order is free), which the caller has zeroed.
 // 4096 x 4096 fp32: 17 us, 3.9 TB/s.
 struct Largest { uint32_t scale, dy; };
 __device__ __forceinline__ uint32_t finite_bits(float x) {
@@ -271,25 +274,50 @@ __device__ __forceinline__ uint32_t finite_bits(float x) {
 }
 template <class T, bool A>
 __global__ void __launch_bounds__(kThreads) k_act8_largest(Mat dy, const float* __restrict__ scales, int64_t nscales,
-                                                           Largest* out, int64_t rows, int cols) {
+                                                           Largest* out, int64_t rows, int cols, int lanes) {
+  let_next_start();
   __shared__ uint32_t slots[kThreads / 32];
-  uint32_t m = 0;
-  for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
-    const T* x = static_cast<const T*>(dy.p) + row * dy.ld;
-    for (int c = int(threadIdx.x) * 8; c < cols; c += kThreads * 8) {
-      Raw8<T> r;
-      load8<A>(x, c, cols, dy.vec, r);
+  __shared__ Largest mine;
+  const unsigned ctas = gridDim.x * gridDim.y;
+  const int64_t stride = int64_t(gridDim.x) * (kThreads / lanes);
+  const T* x = static_cast<const T*>(dy.p);
+  uint32_t m = 0, s = 0;
+  for (int64_t row = int64_t(blockIdx.x) * (kThreads / lanes) + threadIdx.x / lanes; row < rows; row += 4 * stride)
+    for (int64_t c = (int64_t(blockIdx.y) * lanes + threadIdx.x % lanes) * 8; c < cols; c += int64_t(gridDim.y) * lanes * 8) {
+      Raw8<T> r[4];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) m = max(m, finite_bits(elt(r, i)));
+      for (int u = 0; u < 4; ++u)
+        load8<A>(x + (row + u * stride) * dy.ld, int(c), row + u * stride < rows ? cols : 0, dy.vec, r[u]);
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m = max(m, finite_bits(elt(r[u], i)));
     }
-  }
-  m = cta_max(m, slots);
-  if (threadIdx.x == 0) atomicMax(&out->dy, m);
-  uint32_t s = 0;
-  for (int64_t i = int64_t(blockIdx.x) * kThreads + threadIdx.x; i < nscales; i += int64_t(gridDim.x) * kThreads)
+#pragma unroll 4
+  for (int64_t i = int64_t(blockIdx.y * gridDim.x + blockIdx.x) * kThreads + threadIdx.x; i < nscales;
+       i += int64_t(ctas) * kThreads)
     s = max(s, finite_bits(__ldg(scales + i)));
+  m = cta_max(m, slots);
   s = cta_max(s, slots);
-  if (threadIdx.x == 0) atomicMax(&out->scale, s);
+  if (ctas > kColCluster) {
+    if (threadIdx.x == 0) {
+      atomicMax(&out->dy, m);
+      atomicMax(&out->scale, s);
+    }
+    return;
+  }
+  cg::cluster_group cluster = cg::this_cluster();
+  if (threadIdx.x == 0) mine = Largest{s, m};
+  cluster.sync();
+  if (cluster.block_rank() == 0 && threadIdx.x == 0) {
+    for (unsigned k = 1; k < ctas; ++k) {
+      const Largest* l = cluster.map_shared_rank(&mine, k);
+      s = max(s, l->scale);
+      m = max(m, l->dy);
+    }
+    *out = Largest{s, m};
+  }
+  cluster.sync();                                        // nobody leaves while its word is read
 }
 
 // The e with 2^13 < 2^e x < 2^15 for the x of these bits (0 for zero), within
@@ -326,29 +354,28 @@ k_act8_halves(Ckpt k, __half* co, int64_t ldco, int cols_c, Mat dy, __half* dyo,
   let_next_start();
   const bool codes = blockIdx.y < code_blocks;
   const Piece<1> p(codes ? blockIdx.y : blockIdx.y - code_blocks);
-  const int ec = value_power(largest), ed = power_to(largest->dy);
-  const float pc = pow2(ec), pd = pow2(ed);
+  if (p.row >= rows || p.c >= (codes ? cols_c : cols_dy)) return;
+  wait_for_pass();
+  const Largest l = *largest;                            // cached: every CTA reads these words
+  float v[8];
+  if (codes) {
+    uint2 w;
+    load_codes8(k.codes + p.row * k.ldc, p.c, cols_c, w);
+    values8(w, __ldg(k.scales + p.row * k.groups + (p.c >> k.shift)), v);
+  } else {
+    Raw8<T> r;
+    load8<A>(static_cast<const T*>(dy.p) + p.row * dy.ld, p.c, cols_dy, dy.vec, r);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = elt(r, i);
+  }
+  const int ec = value_power(&l), ed = power_to(l.dy);
   if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0 && threadIdx.y == 0) {
     const int e = -(ec + ed);                            // up to 252: two factors of half the exponent
     factor[0] = pow2(e >> 1);
     factor[1] = pow2(e - (e >> 1));
   }
-  if (p.row >= rows) return;
-  float v[8];
-  if (codes) {
-    if (p.c >= cols_c) return;
-    uint2 w;
-    load_codes8(k.codes + p.row * k.ldc, p.c, cols_c, w);
-    values8(w, __ldg(k.scales + p.row * k.groups + (p.c >> k.shift)), v);
-    store_halves<2>(v, pc, co + p.row * ldco, rows * ldco, p.c, cols_c);
-  } else {
-    if (p.c >= cols_dy) return;
-    Raw8<T> r;
-    load8<A>(static_cast<const T*>(dy.p) + p.row * dy.ld, p.c, cols_dy, dy.vec, r);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = elt(r, i);
-    store_halves<PARTS>(v, pd, dyo + p.row * lddyo, rows * lddyo, p.c, cols_dy);
-  }
+  if (codes) store_halves<2>(v, pow2(ec), co + p.row * ldco, rows * ldco, p.c, cols_c);
+  else store_halves<PARTS>(v, pow2(ed), dyo + p.row * lddyo, rows * lddyo, p.c, cols_dy);
 }
 
 // The shares' sums, added in order, into the result (512 x 512: 4.6 us).
@@ -421,6 +448,33 @@ GradPlan grad_plan(bool weight, int32_t dtype, int32_t result, int32_t group, in
   return p;
 }
 
+// after_pass: the kernel enqueued just before is this call's own pass; this
+// one may start under it and waits for it itself.
+template <class... P, class... A>
+shampoo4_status start(void (*kern)(P...), dim3 grid, dim3 block, dim3 cluster, bool after_pass, cudaStream_t st,
+                      A... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  unsigned n = 0;
+  if (cluster.x * cluster.y > 1) {
+    attr[n].id = cudaLaunchAttributeClusterDimension;
+    attr[n].val.clusterDim.x = cluster.x;
+    attr[n].val.clusterDim.y = cluster.y;
+    attr[n++].val.clusterDim.z = 1;
+  }
+  if (after_pass) {
+    attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[n++].val.programmaticStreamSerializationAllowed = 1;
+  }
+  cfg.attrs = attr;
+  cfg.numAttrs = n;
+  S4_CUDA(cudaLaunchKernelEx(&cfg, kern, P(args)...));
+  return SHAMPOO4_OK;
+}
+
 shampoo4_status digit_pass(bool weight, const void* dy, int32_t dtype, int64_t lddy, const float* scale,
                            int64_t tokens, int64_t out, int8_t* digits, int64_t ld, float* row_scale,
                            cudaStream_t st) {
@@ -432,18 +486,8 @@ shampoo4_status digit_pass(bool weight, const void* dy, int32_t dtype, int64_t l
     if (weight) {
       unsigned ctas = 1;                                // per strip: no more than it has tiles
       while (ctas < kColCluster && int64_t(ctas) * kTokTile < tokens) ctas *= 2;
-      cudaLaunchConfig_t cfg{};
-      cfg.gridDim = dim3(unsigned(strips), ctas);
-      cfg.blockDim = dim3(kThreads);
-      cfg.stream = st;
-      cudaLaunchAttribute attr[1];
-      attr[0].id = cudaLaunchAttributeClusterDimension;
-      attr[0].val.clusterDim.x = 1;
-      attr[0].val.clusterDim.y = ctas;
-      attr[0].val.clusterDim.z = 1;
-      cfg.attrs = attr;
-      cfg.numAttrs = 1;
-      S4_CUDA(cudaLaunchKernelEx(&cfg, (k_act8_digit_columns<T, A>), m, scale, digits, ld, row_scale, tokens, out));
+      return start(k_act8_digit_columns<T, A>, dim3(unsigned(strips), ctas), dim3(kThreads), dim3(1, ctas), false, st,
+                   m, scale, digits, ld, row_scale, tokens, out);
     } else {
       if (out <= 1024)
         k_act8_digit_rows<T, true, A><<<unsigned((tokens + 7) / 8), dim3(32, 8), 0, st>>>(m, scale, digits, ld, row_scale,
@@ -457,13 +501,12 @@ shampoo4_status digit_pass(bool weight, const void* dy, int32_t dtype, int64_t l
   }); });
 }
 
-shampoo4_status expand(const Ckpt& k, int64_t rows, int64_t cols, void* o, int64_t ld, cudaStream_t st) {
+shampoo4_status expand(const Ckpt& k, int64_t rows, int64_t cols, void* o, int64_t ld, bool after_pass,
+                       cudaStream_t st) {
   const dim3 b = piece_block(cols);
   dim3 g;
   if (!piece_grid(rows, cols, b, 1, &g)) return SHAMPOO4_ERR_INVALID_ARG;
-  k_act8_expand<<<g, b, 0, st>>>(k, static_cast<__nv_bfloat16*>(o), ld, rows, int(cols));
-  S4_CUDA(cudaGetLastError());
-  return SHAMPOO4_OK;
+  return start(k_act8_expand, g, b, dim3(1), after_pass, st, k, static_cast<__nv_bfloat16*>(o), ld, rows, int(cols));
 }
 
 shampoo4_status align_dy(const void* x, int64_t ldx, int64_t rows, int64_t cols, void* o, int64_t ld,
@@ -487,18 +530,31 @@ shampoo4_status halves_pass(const void* dy, int32_t dtype, int64_t lddy, const C
   if (!piece_grid(tokens, out, b, 1, &g) || !piece_grid(tokens, inner, b, 1, &gc) || g.y + gc.y > 65535)
     return SHAMPOO4_ERR_INVALID_ARG;
   g.y += gc.y;
-  S4_CUDA(cudaMemsetAsync(largest, 0, sizeof(Largest), st));
+  // The search: up to 8 pieces per thread fit one cluster, which needs no
+  // zeroed words, and the next kernel starts under it (4 x 125 x 129: 14.6 ->
+  // 10.6 us in all); more take all SMs.
+  int lanes = 1;
+  while (lanes < kThreads && int64_t(lanes) * 8 < out) lanes *= 2;
+  const int64_t pieces = tokens * ((out + 7) / 8) + tokens * k.groups / 4, room = 148 * 4;
+  const int64_t x = std::min((tokens + kThreads / lanes - 1) / (kThreads / lanes), room);
+  const int64_t y = std::min((out + lanes * 8 - 1) / (lanes * 8), room / x);
+  dim3 ctas{unsigned(x), unsigned(y)}, cluster{1};
+  const bool small = pieces <= int64_t(kColCluster) * kThreads * 8;
+  if (small) {
+    while (cluster.x < kColCluster && cluster.x < x) cluster.x *= 2;
+    while (cluster.x * cluster.y < kColCluster && cluster.y < y) cluster.y *= 2;
+    ctas = cluster;
+  } else {
+    if (x * y <= kColCluster) ctas.x = unsigned(room / y);   // few elements, many scales
+    S4_CUDA(cudaMemsetAsync(largest, 0, sizeof(Largest), st));
+  }
   return by_dtype(dtype, [&](auto* tag) { return by_flag(m.vec != 0, [&](auto flag) -> shampoo4_status {
     using T = std::remove_pointer_t<decltype(tag)>;
     constexpr bool A = decltype(flag)::value;
-    k_act8_largest<T, A><<<unsigned(std::min<int64_t>(tokens, 148 * 4)), kThreads, 0, st>>>(
-        m, k.scales, tokens * k.groups, largest, tokens, int(out));
-    S4_CUDA(cudaGetLastError());
-    k_act8_halves<T, sizeof(T) == 4 ? 2 : 1, A><<<g, b, 0, st>>>(k, static_cast<__half*>(cp), ld_code, int(inner), m,
-                                                             static_cast<__half*>(dyp), ld_dy, int(out), largest,
-                                                             factor, tokens, gc.y);
-    S4_CUDA(cudaGetLastError());
-    return SHAMPOO4_OK;
+    S4_TRY(start(k_act8_largest<T, A>, ctas, dim3(kThreads), cluster, false, st, m, k.scales,
+                 tokens * k.groups, largest, tokens, int(out), lanes));
+    return start(k_act8_halves<T, sizeof(T) == 4 ? 2 : 1, A>, g, b, dim3(1), small, st, k, static_cast<__half*>(cp),
+                 ld_code, int(inner), m, static_cast<__half*>(dyp), ld_dy, int(out), largest, factor, tokens, gc.y);
   }); });
 }
 
@@ -548,7 +604,7 @@ shampoo4_status grad(bool weight, const void* dy, int32_t dtype, int64_t lddy, c
     b = Act8Operand{dyp, p.ld_dy, 0};
     S4_TRY(align_dy(dy, lddy, tokens, out, dyp, p.ld_dy, st));
   }
-  S4_TRY(expand(k, K, inner, cp, p.ld_code, st));
+  S4_TRY(expand(k, K, inner, cp, p.ld_code, b.p == dyp, st));
   return launch_act8_bf16(Act8Operand{cp, p.ld_code, 0}, b, weight ? 1 : 0, inner, R, K, o, flags, st);
 }
 

@@ -427,6 +427,25 @@ def test_fp32_gradient_of_huge_values_stays_finite():
     within(f64(dw), np.full((4, 8), float(np.float32(3.4e38)) * 127 * float(scales[0, 0])), 3.4e38 * 2.0 ** -13)
 
 
+@pytest.mark.parametrize("tokens,out,inner", [(1, 40, 33), (3, 5000, 40), (9, 70, 500), (700, 130, 300), (2000, 7, 64),
+                                              (5, 70000, 33), (2, 9, 70000), (300, 2100, 40)])
+def test_grouped_gradient_scales_by_the_largest_wherever_it_is(tokens, out, inner):
+    """One loud element in dy or in x, in a corner of it: a search that missed
+    it would scale it past a half's range."""
+    api = _api()
+    for t, o, i in ((0, 0, 0), (tokens - 1, out - 1, inner - 1), (tokens // 2, out // 3, inner // 2)):
+        dy = data(tokens, out, "fp32", 72)
+        dy[t, o] = 1e6
+        rng = np.random.default_rng(73)
+        x = rng.standard_normal((tokens, inner)).astype(np.float32)
+        x[t, i] = -1e6
+        codes, scales = A.pack(x, 32)
+        dw = api.act8_weight_grad(dy, *to_gpu(codes, scales), group=32)
+        want = f64(dy).T @ A.values64(codes, scales, 32)
+        within(f64(dw), want, grad_tolerance(f64(dy), codes, scales, 32, "fp32", "fp32", True)
+               + half_step("fp32") * np.abs(want) + TINY["fp32"])
+
+
 @pytest.mark.parametrize("tokens", [60, 1000])                # the contraction whole, and split
 def test_grouped_gradient_of_tiny_and_huge_values(tokens):
     """The powers that scale the two operands multiply to more than fp32
