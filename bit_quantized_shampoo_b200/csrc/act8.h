@@ -35,7 +35,7 @@ struct Act8Out {
 
 // int8 codes both: a is M x K, b is R x K (K contiguous).  after_pass: b was
 // written by the kernel enqueued just before on this stream, and a was not;
-// the launch may then overlap that kernel's end.  (The other two always
+// the launch may then overlap that kernel's end.  (The others always
 // follow their own operand pass.)
 shampoo4_status launch_act8_codes(const Act8Operand& a, const Act8Operand& b, int64_t M, int64_t R, int64_t K,
                                   const Act8Out& out, bool after_pass, uint32_t* flags, cudaStream_t st);
@@ -43,16 +43,15 @@ shampoo4_status launch_act8_codes(const Act8Operand& a, const Act8Operand& b, in
 // significant first: B = 65536 d0 + 256 d1 + d2.
 shampoo4_status launch_act8_digits(const Act8Operand& a, const Act8Operand& b, int64_t M, int64_t R, int64_t K,
                                    const Act8Out& out, uint32_t* flags, cudaStream_t st);
-// bfloat16 both: a is K x M, b is R x K (b_mn = 0) or K x R (b_mn = 1).
-shampoo4_status launch_act8_bf16(const Act8Operand& a, const Act8Operand& b, int b_mn, int64_t M, int64_t R, int64_t K,
-                                 const Act8Out& out, uint32_t* flags, cudaStream_t st);
-// Halves both, operands the sums of their planes: a is K x M in two, b is
-// K x R in b_parts (1 or 2).  The product of the second planes is left out.
+// Halves both, operands the sums of their planes: a is K x M in a_parts, b is
+// K x R in b_parts: 2 and 1 or 2 (the product of the second planes is left
+// out), or 1 and 1.
 // shares (act8_halves_shares, one of the least estimated time): with more than
 // one, the contraction is cut in that many and out.y receives their sums, fp32,
 // R x M each, for the caller to add up.
 int act8_halves_shares(int64_t M, int64_t R, int64_t K);
-shampoo4_status launch_act8_halves(const Act8Operand& a, const Act8Operand& b, int b_parts, int64_t M, int64_t R,
-                                   int64_t K, int shares, const Act8Out& out, uint32_t* flags, cudaStream_t st);
+shampoo4_status launch_act8_halves(const Act8Operand& a, int a_parts, const Act8Operand& b, int b_parts, int64_t M,
+                                   int64_t R, int64_t K, int shares, const Act8Out& out, uint32_t* flags,
+                                   cudaStream_t st);
 
 }  // namespace s4

@@ -9,8 +9,8 @@
 //                               of fixed point: three int8 products with
 //                               exact int32 sums, joined in the epilogue
 //   the same in 16 bits         A = the codes' values, B = the gradient, each
-//                               as one bfloat16 or as one or two scaled
-//                               halves (kind::f16, fp32 sums)
+//                               as one or two scaled halves (kind::f16, fp32
+//                               sums)
 //
 // A pair of CTAs (cta_group::2) owns a tile of 256 columns m by R rows: each
 // CTA stages its 128 columns of A and half of the rows of B, and the leader's
@@ -22,8 +22,8 @@
 // one's products.  The pairs are persistent, one CTA per SM.  Bound by the
 // tensor cores, and in a loop by the power cap: 8192 x 11008 x 4096 codes 215
 // us alone (3.4 POPS), 227 to 239 in a loop; its weight gradient in digits 648
-// us alone (3.4 POPS of three products), bfloat16 453 us (1.63 PFLOP/s); the
-// tensor pipe is 88 to 92% busy where tiles fill the waves.
+// us alone (3.4 POPS of three products); the tensor
+// pipe is 88 to 92% busy where tiles fill the waves.
 //
 // Warp roles (320 threads): warp 0 issues the TMA loads, warp 1 of the leader
 // the MMAs, warps 2..9 drain the accumulator, two per lane quarter with half of
@@ -44,7 +44,7 @@
 namespace s4 {
 namespace {
 
-enum { kI8 = 0, kBf16 = 1, kHalf = 2 };
+enum { kI8 = 0, kHalf = 1 };
 constexpr int kLanes = 128;               // columns m per CTA: the TMEM lanes
 constexpr int kPairThreads = 320, kSmallThreads = 192;
 constexpr int kRowBytes = 128;            // bytes of a swizzle atom row
@@ -88,12 +88,12 @@ struct GemmArgs {
   Act8Out out;
 };
 
-// Instruction descriptor: fp32 sums (accumulator code 1) of half (type code 0)
-// or bfloat16 (1), or int32 sums (code 2) of signed 8-bit integers (1).
+// Instruction descriptor: fp32 sums (accumulator code 1) of halves (type code
+// 0), or int32 sums (code 2) of signed 8-bit integers (1).
 template <class C>
 __host__ __device__ constexpr uint32_t idesc() {
-  return ((C::KIND == kI8 ? 2u : 1u) << 4) | ((C::KIND == kHalf ? 0u : 1u) * ((1u << 7) | (1u << 10))) | (uint32_t(C::A_MN) << 15) |
-         (uint32_t(C::B_MN) << 16) | (uint32_t(C::kN >> 3) << 17) | (uint32_t((C::CG * kLanes) >> 4) << 24);
+  return ((C::KIND == kI8 ? 2u : 1u) << 4) | ((C::KIND == kHalf ? 0u : 1u) * ((1u << 7) | (1u << 10))) |
+         (uint32_t(C::A_MN) << 15) | (uint32_t(C::B_MN) << 16) | (uint32_t(C::kN >> 3) << 17) | (uint32_t((C::CG * kLanes) >> 4) << 24);
 }
 
 template <int KIND, int CG>
@@ -649,7 +649,7 @@ __global__ void __launch_bounds__(kSmallThreads, 2) k_act8_small(const __grid_co
     mbar_init(&done_bar, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     for (int it = 0; it < lead; ++it) load_a(it, it);       // under the tensor memory allocation
-    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&g.b)) : "memory");
+    if (n > 0) asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&g.b)) : "memory");
   }
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_slot)),
@@ -823,7 +823,7 @@ shampoo4_status encode(CUtensorMap* out, int kind, const Act8Operand& x, int64_t
   cuuint64_t strides[2] = {cuuint64_t(x.ld * esize), cuuint64_t(planes > 1 ? x.plane * x.ld * esize : x.ld * esize)};
   cuuint32_t box[3] = {cuuint32_t(128 / esize), cuuint32_t(box_rows), cuuint32_t(planes)};
   cuuint32_t estr[3] = {1u, 1u, 1u};
-  const CUresult r = fn(out, kind == kI8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+  const CUresult r = fn(out, kind == kI8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
                         const_cast<void*>(x.p), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
@@ -960,9 +960,12 @@ Form choose_form(int64_t M, int64_t R, int64_t K, int pair_rows, int digits, con
 //                               kind   A_MN   B_MN   R   PA PB ND CG stages chunk
 using CodesCfg = Cfg<            kI8,   false, false, 256, 1, 1, 1, 2, 6, 0>;
 using DigitsCfg = Cfg<           kI8,   true,  false, 64,  1, 1, kAct8Digits, 2, 8, 1024>;
-template <bool B_MN> using Bf16Cfg = Cfg<kBf16, true, B_MN, 256, 1, 1, 1, 2, 6, 0>;
 template <int PB, int STAGES>
 using HalvesCfg = Cfg<           kHalf, true,  true,  128, 2, PB, 1, 2, STAGES, 4>;
+// One half each.  The sum leaves the tensor core every 1024 k (64 additions,
+// each cut off at 2^-22 of the sum at most: 2^-16, far below the bfloat16
+// result); draining 256 rows takes a sixth of the time of those products.
+using HalfCfg = Cfg<             kHalf, true,  true,  256, 1, 1,  1, 2, 6, 16>;
 
 shampoo4_status launch_act8_codes(const Act8Operand& a, const Act8Operand& b, int64_t M, int64_t R, int64_t K,
                                   const Act8Out& out, bool after_pass, uint32_t* flags, cudaStream_t st) {
@@ -987,12 +990,6 @@ shampoo4_status launch_act8_digits(const Act8Operand& a, const Act8Operand& b, i
   return launch<DigitsCfg>(a, b, M, R, K, out, true, flags, st);
 }
 
-shampoo4_status launch_act8_bf16(const Act8Operand& a, const Act8Operand& b, int b_mn, int64_t M, int64_t R, int64_t K,
-                                 const Act8Out& out, uint32_t* flags, cudaStream_t st) {
-  return b_mn ? launch<Bf16Cfg<true>>(a, b, M, R, K, out, true, flags, st)
-              : launch<Bf16Cfg<false>>(a, b, M, R, K, out, true, flags, st);
-}
-
 // The estimated time (us): 0.5 per k-block and 2 per wave of tiles; the join
 // 3 and reading the sums.  Every share gets a k-block.
 int act8_halves_shares(int64_t M, int64_t R, int64_t K) {
@@ -1010,8 +1007,10 @@ int act8_halves_shares(int64_t M, int64_t R, int64_t K) {
   return best;
 }
 
-shampoo4_status launch_act8_halves(const Act8Operand& a, const Act8Operand& b, int b_parts, int64_t M, int64_t R,
-                                   int64_t K, int shares, const Act8Out& out, uint32_t* flags, cudaStream_t st) {
+shampoo4_status launch_act8_halves(const Act8Operand& a, int a_parts, const Act8Operand& b, int b_parts, int64_t M,
+                                   int64_t R, int64_t K, int shares, const Act8Out& out, uint32_t* flags,
+                                   cudaStream_t st) {
+  if (a_parts == 1) return launch<HalfCfg>(a, b, M, R, K, out, true, flags, st, shares);
   return b_parts == 1 ? launch<HalvesCfg<1, 5>>(a, b, M, R, K, out, true, flags, st, shares)
                       : launch<HalvesCfg<2, 4>>(a, b, M, R, K, out, true, flags, st, shares);
 }

@@ -4,7 +4,7 @@
 //   act8_input_grad    dX[t, i] = sum_o dY[t, o] sw[o] wc[o, i]
 //
 // The scale belongs to the contraction index, so it has to go into a factor.
-// Three ways, chosen by the types and the scales alone (grad_path):
+// Two ways, chosen by the scales alone (grad_path):
 //
 //  digits  One scale per row of codes.  F = dY * scale in fp32 becomes fixed
 //          point relative to its largest magnitude over the contraction,
@@ -14,15 +14,14 @@
 //          rounding (half of max|F| / 2^23 per element) and a few fp32
 //          roundings at the end.  1.5 times a bfloat16 product's tensor-core
 //          time, against three times for operands split into bfloat16 parts.
-//  bf16    dY and the result bfloat16, and enough rows: the codes' values rounded to one
-//          bfloat16 (2^-8 at most, no more than the result's own rounding),
-//          dY as it is.  One bfloat16 product.
 //  halves  Scales per group of columns (no common factor per row): values and
 //          dY scaled by powers of two (their largest to about 2^14) and taken
 //          as a half and a half of what is left, 22 bits and never coarser
-//          than 2^-39 of the largest; a 16-bit dY is one half.  Three products
-//          (two for a 16-bit dY), summed in fp32 outside the tensor core
-//          every 256 k.  (Three bfloat16 parts each, six products, measured
+//          than 2^-39 of the largest; a 16-bit dY is one half, and so is a
+//          value for a bfloat16 result of a bfloat16 dY (2^-11, an eighth of
+//          the result's own rounding; as one bfloat16 it would add as much
+//          again).  Three products (two, one), summed in fp32 outside the
+//          tensor core every 256 k (one: every 1024).  (Three bfloat16 parts each, six products, measured
 //          47 us where this takes 32 at 1537 x 768 x 2305 fp32.)
 //
 // The operand passes of this file stream; their bound is HBM bandwidth.
@@ -232,33 +231,6 @@ k_act8_digit_columns(Mat dy, const float* __restrict__ scale, int8_t* digits, in
   }
 }
 
-// The codes' values in bfloat16.  11008 x 4096: 26 us, 5.2 TB/s.
-__global__ void __launch_bounds__(kThreads) k_act8_expand(Ckpt k, __nv_bfloat16* o, int64_t ld, int64_t rows,
-                                                          int cols) {
-  let_next_start();
-  const Piece<1> p;
-  if (p.row >= rows || p.c >= cols) return;
-  uint2 w;
-  load_codes8(k.codes + p.row * k.ldc, p.c, cols, w);
-  float v[8];
-  values8(w, __ldg(k.scales + p.row * k.groups + (p.c >> k.shift)), v);
-  store8(o + p.row * ld, p.c, cols, 1, v);
-  wait_for_pass();                       // nothing of it is read here, but the product relies on both
-}
-// A bfloat16 dY with rows that are not 16-byte aligned, copied to rows that are
-// (8192 x 4096: 22 us, 6.2 TB/s).
-__global__ void __launch_bounds__(kThreads) k_act8_align(Mat x, __nv_bfloat16* o, int64_t ld, int64_t rows, int cols) {
-  let_next_start();
-  const Piece<1> p;
-  if (p.row >= rows || p.c >= cols) return;
-  Raw8<__nv_bfloat16> r;
-  load8<false>(static_cast<const __nv_bfloat16*>(x.p) + p.row * x.ld, p.c, cols, 0, r);
-  float v[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = elt(r, i);
-  store8(o + p.row * ld, p.c, cols, 1, v);
-}
-
 // ---- halves
 
 // Bits of the largest finite magnitudes, for both operands (elements that are
@@ -347,7 +319,7 @@ __device__ __forceinline__ void store_halves(const float (&v)[8], float power, _
 
 // Both operands in one launch: the first code_blocks of blockIdx.y the codes'
 // values, the others dY.  4096 x 4096 codes and fp32 dY: 40 us, 5.5 TB/s.
-template <class T, int PARTS, bool A>
+template <class T, int CODE_PARTS, bool A>
 __global__ void __launch_bounds__(kThreads)
 k_act8_halves(Ckpt k, __half* co, int64_t ldco, int cols_c, Mat dy, __half* dyo, int64_t lddyo, int cols_dy,
               const Largest* largest, float* factor, int64_t rows, unsigned code_blocks) {
@@ -374,7 +346,8 @@ k_act8_halves(Ckpt k, __half* co, int64_t ldco, int cols_c, Mat dy, __half* dyo,
     factor[0] = pow2(e >> 1);
     factor[1] = pow2(e - (e >> 1));
   }
-  if (codes) store_halves<2>(v, pow2(ec), co + p.row * ldco, rows * ldco, p.c, cols_c);
+  constexpr int PARTS = sizeof(T) == 4 ? 2 : 1;
+  if (codes) store_halves<CODE_PARTS>(v, pow2(ec), co + p.row * ldco, rows * ldco, p.c, cols_c);
   else store_halves<PARTS>(v, pow2(ed), dyo + p.row * lddyo, rows * lddyo, p.c, cols_dy);
 }
 
@@ -394,19 +367,8 @@ __global__ void __launch_bounds__(kThreads) k_act8_join(const float* __restrict_
 
 // ------------------------------------------------------------------ host
 
-enum GradPath { kDigits, kBf16, kHalves };
-// The result is rows x inner.  The bfloat16 path writes the codes out in
-// bfloat16 once (3 bytes a code, 26 us for 45M codes) where digits take half
-// as long again per row of the result (335 us for 8192 rows of the same
-// codes): even at about 640 rows.  It also has one form only, pairs of CTAs on
-// 256 x 256 tiles, so it wants tiles for most of them (512 x 768 and 2304 of
-// contraction: 20 against 16 us; 1024 x 4096: 37 against 44).
-constexpr int64_t kDigitRows = 640;
-GradPath grad_path(int32_t dtype, int32_t result, int32_t group, int64_t rows, int64_t inner) {
-  const bool many = rows > kDigitRows && ((rows + 255) / 256) * ((inner + 255) / 256) >= 48;
-  if (dtype == ACT8_BF16 && result == ACT8_BF16 && (group != 0 || many)) return kBf16;
-  return group == 0 ? kDigits : kHalves;
-}
+enum GradPath { kDigits, kHalves };
+GradPath grad_path(int32_t group) { return group == 0 ? kDigits : kHalves; }
 
 size_t round_up(size_t n, size_t a) { return (n + a - 1) / a * a; }
 
@@ -415,7 +377,7 @@ size_t round_up(size_t n, size_t a) { return (n + a - 1) / a * a; }
 // then, but for digits, the codes' values (code_rows x inner) in 16 bits.
 struct GradPlan {
   GradPath path;
-  int dy_parts, code_parts;
+  int dy_parts, code_parts;      // halves of an element
   int64_t ld_dy, ld_code;        // elements
   size_t scale_bytes, dy_bytes, code_bytes;
   int shares;                    // halves: parts of the contraction, and room for their sums
@@ -425,7 +387,7 @@ struct GradPlan {
 GradPlan grad_plan(bool weight, int32_t dtype, int32_t result, int32_t group, int64_t tokens, int64_t out,
                    int64_t inner) {
   GradPlan p{};
-  p.path = grad_path(dtype, result, group, weight ? out : tokens, inner);
+  p.path = grad_path(group);
   if (p.path == kDigits) {
     const int64_t rows = weight ? out : tokens, k = weight ? tokens : out;
     p.ld_dy = int64_t(round_up(size_t(k), 16));
@@ -434,17 +396,14 @@ GradPlan grad_plan(bool weight, int32_t dtype, int32_t result, int32_t group, in
     return p;
   }
   p.dy_parts = dtype == ACT8_FP32 ? 2 : 1;
-  p.code_parts = p.path == kBf16 ? 1 : 2;
-  p.scale_bytes = p.path == kBf16 ? 0 : 256;
+  p.code_parts = dtype == ACT8_BF16 && result == ACT8_BF16 ? 1 : 2;
+  p.scale_bytes = 256;
   p.ld_dy = int64_t(round_up(size_t(out), 8));
   p.ld_code = int64_t(round_up(size_t(inner), 8));
-  // room for a copy of a bfloat16 dY whatever its alignment turns out to be
   p.dy_bytes = round_up(size_t(tokens) * p.ld_dy * 2 * p.dy_parts, 256);
-  p.code_bytes = round_up(size_t(weight ? tokens : out) * p.ld_code * 2 * p.code_parts, 256);
-  if (p.path == kHalves) {
-    p.shares = act8_halves_shares(inner, out, tokens);
-    p.sum_bytes = p.shares > 1 ? round_up(size_t(p.shares) * out * inner * 4, 256) : 0;
-  }
+  p.code_bytes = round_up(size_t(tokens) * p.ld_code * 2 * p.code_parts, 256);
+  p.shares = p.code_parts == 2 ? act8_halves_shares(inner, out, tokens) : 1;
+  p.sum_bytes = p.shares > 1 ? round_up(size_t(p.shares) * out * inner * 4, 256) : 0;
   return p;
 }
 
@@ -501,29 +460,11 @@ shampoo4_status digit_pass(bool weight, const void* dy, int32_t dtype, int64_t l
   }); });
 }
 
-shampoo4_status expand(const Ckpt& k, int64_t rows, int64_t cols, void* o, int64_t ld, bool after_pass,
-                       cudaStream_t st) {
-  const dim3 b = piece_block(cols);
-  dim3 g;
-  if (!piece_grid(rows, cols, b, 1, &g)) return SHAMPOO4_ERR_INVALID_ARG;
-  return start(k_act8_expand, g, b, dim3(1), after_pass, st, k, static_cast<__nv_bfloat16*>(o), ld, rows, int(cols));
-}
-
-shampoo4_status align_dy(const void* x, int64_t ldx, int64_t rows, int64_t cols, void* o, int64_t ld,
-                         cudaStream_t st) {
-  const dim3 b = piece_block(cols);
-  dim3 g;
-  if (!piece_grid(rows, cols, b, 1, &g)) return SHAMPOO4_ERR_INVALID_ARG;
-  k_act8_align<<<g, b, 0, st>>>(mat(x, ldx, ACT8_BF16), static_cast<__nv_bfloat16*>(o), ld, rows, int(cols));
-  S4_CUDA(cudaGetLastError());
-  return SHAMPOO4_OK;
-}
-
 // Both operands as halves at dyp and cp; the result's factors next to the
 // largest magnitudes at `largest`.
 shampoo4_status halves_pass(const void* dy, int32_t dtype, int64_t lddy, const Ckpt& k, int64_t tokens, int64_t out,
-                            int64_t inner, Largest* largest, float* factor, void* dyp, int64_t ld_dy, void* cp,
-                            int64_t ld_code, cudaStream_t st) {
+                            int64_t inner, Largest* largest, float* factor, const GradPlan& p, void* dyp, void* cp,
+                            cudaStream_t st) {
   const Mat m = mat(dy, lddy, dtype);
   const dim3 b = piece_block(std::max(out, inner));
   dim3 g, gc;
@@ -553,8 +494,9 @@ shampoo4_status halves_pass(const void* dy, int32_t dtype, int64_t lddy, const C
     constexpr bool A = decltype(flag)::value;
     S4_TRY(start(k_act8_largest<T, A>, ctas, dim3(kThreads), cluster, false, st, m, k.scales,
                  tokens * k.groups, largest, tokens, int(out), lanes));
-    return start(k_act8_halves<T, sizeof(T) == 4 ? 2 : 1, A>, g, b, dim3(1), small, st, k, static_cast<__half*>(cp),
-                 ld_code, int(inner), m, static_cast<__half*>(dyp), ld_dy, int(out), largest, factor, tokens, gc.y);
+    return start(p.code_parts == 1 ? k_act8_halves<T, 1, A> : k_act8_halves<T, 2, A>, g, b, dim3(1), small, st, k,
+                 static_cast<__half*>(cp), p.ld_code, int(inner), m, static_cast<__half*>(dyp), p.ld_dy, int(out),
+                 largest, factor, tokens, gc.y);
   }); });
 }
 
@@ -564,8 +506,8 @@ shampoo4_status grad(bool weight, const void* dy, int32_t dtype, int64_t lddy, c
                      uint32_t* flags, cudaStream_t st) {
   const int64_t K = weight ? tokens : out, R = weight ? out : tokens;
   if (K == 0 && o.accumulate) return SHAMPOO4_OK;
+  if (K == 0) return launch_act8_codes(Act8Operand{}, Act8Operand{}, inner, R, 0, o, false, flags, st);   // zeros
   const GradPlan p = grad_plan(weight, dtype, o.dtype, group, tokens, out, inner);
-  if (K == 0) return launch_act8_bf16(Act8Operand{}, Act8Operand{}, 0, inner, R, 0, o, flags, st);
   if (!ws || !aligned(ws, 256)) return SHAMPOO4_ERR_INVALID_ARG;
   if (ws_bytes < p.total()) return SHAMPOO4_ERR_WORKSPACE;
   char* w = static_cast<char*>(ws);
@@ -578,34 +520,25 @@ shampoo4_status grad(bool weight, const void* dy, int32_t dtype, int64_t lddy, c
                               st);
   }
   char *dyp = w + p.scale_bytes, *cp = dyp + p.dy_bytes;
-  if (p.path == kHalves) {                                  // groups: only the weight gradient has them
-    Largest* largest = reinterpret_cast<Largest*>(w);
-    float* factor = reinterpret_cast<float*>(largest + 1);
-    S4_TRY(halves_pass(dy, dtype, lddy, k, tokens, out, inner, largest, factor, dyp, p.ld_dy, cp, p.ld_code, st));
-    const Act8Operand a{cp, p.ld_code, K}, b{dyp, p.ld_dy, tokens};
-    if (p.shares == 1) {
-      o.factor = factor;
-      return launch_act8_halves(a, b, p.dy_parts, inner, R, K, 1, o, flags, st);
-    }
-    float* sums = reinterpret_cast<float*>(cp + p.code_bytes);
-    S4_TRY(launch_act8_halves(a, b, p.dy_parts, inner, R, K, p.shares,
-                              Act8Out{sums, inner, ACT8_FP32, 0, nullptr, nullptr, nullptr, factor}, flags, st));
-    const unsigned ctas = unsigned(std::min<int64_t>((R * inner + kThreads - 1) / kThreads, 148 * 8));
-    return by_dtype(o.dtype, [&](auto* tag) -> shampoo4_status {
-      using T = std::remove_pointer_t<decltype(tag)>;
-      k_act8_join<T><<<ctas, kThreads, 0, st>>>(sums, p.shares, static_cast<T*>(o.y), o.ld, o.accumulate, R,
-                                                int(inner));
-      S4_CUDA(cudaGetLastError());
-      return SHAMPOO4_OK;
-    });
+  // groups: only the weight gradient has them
+  Largest* largest = reinterpret_cast<Largest*>(w);
+  float* factor = reinterpret_cast<float*>(largest + 1);
+  S4_TRY(halves_pass(dy, dtype, lddy, k, tokens, out, inner, largest, factor, p, dyp, cp, st));
+  const Act8Operand a{cp, p.ld_code, K}, b{dyp, p.ld_dy, tokens};
+  if (p.shares == 1) {
+    o.factor = factor;
+    return launch_act8_halves(a, p.code_parts, b, p.dy_parts, inner, R, K, 1, o, flags, st);
   }
-  Act8Operand b{dy, lddy, 0};
-  if (!row_aligned(dy, lddy, dtype)) {
-    b = Act8Operand{dyp, p.ld_dy, 0};
-    S4_TRY(align_dy(dy, lddy, tokens, out, dyp, p.ld_dy, st));
-  }
-  S4_TRY(expand(k, K, inner, cp, p.ld_code, b.p == dyp, st));
-  return launch_act8_bf16(Act8Operand{cp, p.ld_code, 0}, b, weight ? 1 : 0, inner, R, K, o, flags, st);
+  float* sums = reinterpret_cast<float*>(cp + p.code_bytes);
+  S4_TRY(launch_act8_halves(a, p.code_parts, b, p.dy_parts, inner, R, K, p.shares,
+                            Act8Out{sums, inner, ACT8_FP32, 0, nullptr, nullptr, nullptr, factor}, flags, st));
+  const unsigned ctas = unsigned(std::min<int64_t>((R * inner + kThreads - 1) / kThreads, 148 * 8));
+  return by_dtype(o.dtype, [&](auto* tag) -> shampoo4_status {
+    using T = std::remove_pointer_t<decltype(tag)>;
+    k_act8_join<T><<<ctas, kThreads, 0, st>>>(sums, p.shares, static_cast<T*>(o.y), o.ld, o.accumulate, R, int(inner));
+    S4_CUDA(cudaGetLastError());
+    return SHAMPOO4_OK;
+  });
 }
 
 }  // namespace

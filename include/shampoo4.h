@@ -570,17 +570,15 @@ shampoo4_status act8_linear(const void* d_x, int32_t xdtype, int64_t ldx, const 
  *   act8_input_grad   dX[t, i] = sum_o dY[t, o] w[o, i],  w = value of wc
  *                     (one scale per row)
  * accumulate != 0 adds the product to the result's contents (in fp32,
- * rounded once).  Arithmetic, by the types and scales (xf: a code's value):
+ * rounded once).  Arithmetic, by the scales (xf: a code's value):
  *   one scale per row   dY * scale in fp32, then fixed point: 24 bits below
  *                       its largest magnitude over the contraction (a largest
  *                       below 2^-100 counts as 2^-100); exact integer
  *                       products and sums with the codes.
  *   scales per group    dY and xf to 22 bits, and no finer than 2^-39 of the
- *                       largest in the whole tensor; fp32 sums.
- *   dY and the result bfloat16, with scales per group or more than 640 rows
- *                       and at least 48 tiles of 256 x 256 in the result:
- *                       xf rounded to bfloat16 (off by 2^-8 at most), dY as
- *                       it is; fp32 sums.
+ *                       largest in the whole tensor; fp32 sums.  dY and
+ *                       the result bfloat16: xf to 11 bits (2^-11, an eighth
+ *                       of the result's rounding).
  * A non-finite element of dY, or a non-finite scale, makes every result it
  * enters non-finite.
  * d_workspace: act8_grad_workspace bytes, 256-byte aligned (weight != 0 for

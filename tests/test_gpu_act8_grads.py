@@ -1,0 +1,88 @@
+"""The gradients of the 8-bit product where their arithmetic could lose
+something: results in bfloat16, long contractions, magnitudes far apart.
+
+Tolerances, from the arithmetic (a rounding is off by at most half a step,
+eps / 2 relative to the value: fp32 2^-24, fp16 2^-11, bf16 2^-8) are derived
+at each test; S is the sum of the products' magnitudes.
+"""
+import numpy as np
+import pytest
+import torch
+
+from oracle import act8_oracle as A
+from test_gpu_act8 import DT, TINY, data, f64, half_step, stored, to_gpu, within
+
+pytestmark = pytest.mark.gpu
+
+
+def _api():
+    from bit_quantized_shampoo_b200 import api
+    return api
+
+
+def values64(k, group=0):
+    """Stored codes and scales as fp64 values on the GPU."""
+    codes, scales = k
+    cols = codes.shape[1]
+    index = torch.arange(cols, device="cuda") // group if group else torch.zeros(cols, dtype=torch.long, device="cuda")
+    return codes.double() * scales.double()[:, index]
+
+
+# ---------------------------------------------------- results in bfloat16
+
+@pytest.mark.parametrize("weight,tokens,out,inner,group", [
+    (False, 1100, 1900, 3100, 0), (True, 1900, 1100, 3100, 0), (True, 700, 200, 320, 64), (True, 1300, 900, 3200, 128),
+    (False, 300, 500, 400, 0)])
+def test_bfloat16_gradients_are_the_rounded_result(weight, tokens, out, inner, group):
+    """The error is that of rounding the exact result to bfloat16, whatever
+    the form that the sizes choose.  Values rounded to a half on the way would
+    add 2^-11 / sqrt(3) = 2.8e-4 of a product's magnitude at most (root mean
+    square, signs at random), in quadrature to about 2^-8 / sqrt(3) * 0.72 =
+    1.6e-3: 1.5%; bounded at 3%."""
+    api = _api()
+    dy = data(tokens, out, "bf16", 1, scale=0.01)
+    k = stored(tokens if weight else out, inner, 2, group)[0]
+    v = values64(k, group)
+    if weight:
+        got, want = api.act8_weight_grad(dy, *k, group=group, dtype=torch.bfloat16), dy.double().t() @ v
+    else:
+        got, want = api.act8_input_grad(dy, *k), dy.double() @ v
+    assert got.dtype == torch.bfloat16
+    best = (want.bfloat16().double() - want).norm()
+    assert (got.double() - want).norm() <= 1.03 * best
+
+
+@pytest.mark.parametrize("group", [0, 32])
+def test_bfloat16_gradient_of_values_above_its_range(group):
+    """Stored values beyond bfloat16's largest number, finite in fp32: their
+    products with small gradients are finite, with zeros zero."""
+    api = _api()
+    codes = np.full((40, 64), 127, np.int8)
+    codes[:, 1::2] = -100
+    scales = np.full((40, 1 if group == 0 else 2), np.float32(3.4e38) / np.float32(127), np.float32)
+    dy = torch.full((40, 24), 2.0 ** -60, dtype=torch.bfloat16, device="cuda")
+    dy[:, 5] = 0
+    dw = api.act8_weight_grad(dy, *to_gpu(codes, scales), group=group, dtype=torch.bfloat16)
+    want = f64(dy).T @ A.values64(codes, scales, group)
+    # values as one half at least (2^-11), the digits' step and fp32 sums far below that, and the result's rounding
+    within(f64(dw), want, np.abs(want) * (2.0 ** -11 + 2.0 ** -16 + half_step("bf16")))
+
+
+@pytest.mark.parametrize("group", [0, 64])
+def test_bfloat16_gradient_over_millions_of_tokens(group):
+    """Terms of one sign: sums that are cut off at each step drift by its
+    count.  Beside the result's rounding (2^-8): values as halves (2^-11),
+    and fp32 sums joined once per 1024 tokens, rounded to nearest (at random,
+    so by the root of their count: 8 standard deviations of sqrt(2^13) 2^-24
+    / sqrt(3)), with at most 64 truncated additions of 2^-22 within each."""
+    api = _api()
+    tokens = 1 << 23
+    g = torch.Generator(device="cuda")
+    g.manual_seed(3)
+    codes = torch.randint(90, 128, (tokens, 16), generator=g, dtype=torch.int8, device="cuda")
+    scales = torch.full((tokens, 1), 1.0037 / 64, device="cuda")
+    dy = torch.rand(tokens, 2, generator=g, device="cuda").add_(0.5).bfloat16()
+    got = api.act8_weight_grad(dy, codes, scales, group=group, dtype=torch.bfloat16).double()
+    want = dy.double().t() @ (codes.double() * scales.double())
+    tol = 2.0 ** -11 + 64 * 2.0 ** -22 + 8 * 2.0 ** 6.5 * 2.0 ** -24 / 3 ** 0.5 + half_step("bf16")
+    assert ((got - want).abs() <= tol * want).all()
