@@ -471,7 +471,7 @@ static shampoo4_status matmul(const int8_t* xc, int64_t ldxc, const float* xs, c
                               const float* ws, const float* bias, int64_t tokens, int64_t out, int64_t inner, void* y,
                               int32_t dtype, int64_t ldy, bool after_pack, uint32_t* flags, cudaStream_t st) {
   // no columns: no group, so no scale either
-  const Act8Out o{y, ldy, dtype, 0, inner > 0 ? xs : nullptr, inner > 0 ? ws : nullptr, bias, nullptr};
+  const Act8Out o{y, ldy, dtype, 0, inner > 0 ? xs : nullptr, inner > 0 ? ws : nullptr, bias, 0};
   return launch_act8_codes(Act8Operand{wc, ldwc, 0}, Act8Operand{xc, ldxc, 0}, out, tokens, inner, o, after_pack,
                            flags, st);
 }

@@ -28,7 +28,7 @@ struct Act8Out {
   const float* row_scale;                              // of R, optional
   const float* col_scale;                              // of M, optional
   const float* bias;                                   // of M, optional
-  const float* factor;                                 // halves: two factors of the whole result
+  int32_t col_shift;                                   // halves: column m has col_scale[m >> col_shift]
 };
 
 // All products: Y[r, m] = row_scale[r] col_scale[m] sum_k B[r, k] A[m, k] + bias[m].

@@ -483,14 +483,12 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_act8_gemm(const __grid_cons
     int i = 0;
     bool ok = true;
     wait_previous();
-    // one after the other: their product may lie outside fp32 where the result does not
-    const bool scaled = C::KIND == kHalf && g.out.factor;
-    const float factor = scaled ? __ldg(g.out.factor) : 1.0f, factor2 = scaled ? __ldg(g.out.factor + 1) : 1.0f;
     for (int t = first; ok && t < items; t += step) {
       int tm, tr;
       tile_of(g, t / shares, tm, tr);
       const int m = (tm * C::CG + int(rank)) * kLanes + 32 * q + lane, r0 = tr * C::R + 32 * c0;
-      const float cs = g.out.col_scale && m < g.M ? __ldg(g.out.col_scale + m) : factor;
+      const float cs = g.out.col_scale && m < g.M
+                           ? __ldg(g.out.col_scale + (C::KIND == kHalf ? m >> g.out.col_shift : m)) : 1.0f;
       const float bias = g.out.bias && m < g.M ? __ldg(g.out.bias + m) : 0.0f;
       float* rs = g.out.row_scale ? row_scales[warp - 2] : nullptr;   // fetched under the products
       if (rs) {
@@ -555,10 +553,17 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_act8_gemm(const __grid_cons
         for (int c = 0; c < kChunks; ++c) {
           if (r0 + 32 * c < g.R) {
             if (C::KIND == kHalf) {
+              // powers of two, the smaller first: their product may lie outside fp32 where the result
+              // does not, and the other way round a step might
 #pragma unroll
-              for (int j = 0; j < 32; ++j) sum[c][j] *= factor2;
+              for (int j = 0; j < 32; ++j) {
+                const float f = rs[32 * c + j];
+                sum[c][j] = sum[c][j] * fminf(f, cs) * fmaxf(f, cs);
+              }
+              store_any(out, g.R, g.M, r0 + 32 * c, m, 1.0f, 0.0f, nullptr, sum[c]);
+            } else {
+              store_any(out, g.R, g.M, r0 + 32 * c, m, cs, bias, rs ? rs + 32 * c : nullptr, sum[c]);
             }
-            store_any(out, g.R, g.M, r0 + 32 * c, m, cs, bias, rs ? rs + 32 * c : nullptr, sum[c]);
           }
         }
       }

@@ -14,10 +14,11 @@
 //          rounding (half of max|F| / 2^23 per element) and a few fp32
 //          roundings at the end.  1.5 times a bfloat16 product's tensor-core
 //          time, against three times for operands split into bfloat16 parts.
-//  halves  Scales per group of columns (no common factor per row): values and
-//          dY scaled by powers of two (their largest to about 2^14) and taken
+//  halves  Scales per group of columns (no common factor per row): each column
+//          of dY and each group of the values' columns scaled by a power of
+//          two (its largest over the contraction to about 2^14) and taken
 //          as a half and a half of what is left, 22 bits and never coarser
-//          than 2^-39 of the largest; a 16-bit dY is one half, and so is a
+//          than 2^-39 of that largest; a 16-bit dY is one half, and so is a
 //          value for a bfloat16 result of a bfloat16 dY (2^-11, an eighth of
 //          the result's own rounding; as one bfloat16 it would add as much
 //          again).  Three products (two, one), summed in fp32 outside the
@@ -124,7 +125,7 @@ k_act8_digit_rows(Mat dy, const float* __restrict__ scale, int8_t* digits, int64
 // digit row is written in pieces of 128 bytes.  A thread holds 4 tokens by 8
 // columns of a tile.  Bound by issue slots (60% busy) and shared memory as
 // much as by HBM: 8192 x 4096 bf16 49 us, 3.4 TB/s of dY and digits.
-constexpr int kColTile = 64, kTokTile = 128, kColCluster = 8;
+constexpr int kColTile = 64, kTokTile = 128, kColCluster = 8, kMaxParts = 8;
 template <class T, bool A>
 __global__ void __launch_bounds__(kThreads, 4)
 k_act8_digit_columns(Mat dy, const float* __restrict__ scale, int8_t* digits, int64_t ld, float* row_scale,
@@ -233,83 +234,82 @@ k_act8_digit_columns(Mat dy, const float* __restrict__ scale, int8_t* digits, in
 
 // ---- halves
 
-// Bits of the largest finite magnitudes, for both operands (elements that are
-// not finite do not count: they stay so whatever the factor).  `lanes` threads
-// share a row of dY, four rows in flight.  Up to 8 CTAs are a cluster and join
-// their maxima in shared memory; more raise the words at `out` (an integer
-// maximum: the order is free), which the caller has zeroed.
-// 4096 x 4096 fp32: 15 us, 4.6 TB/s.
-struct Largest { uint32_t scale, dy; };
+// Bits of the largest finite magnitudes (elements that are not finite do not
+// count: they stay so whatever the factor) of each column of dY and of each
+// group's scales: a cluster of up to 8 CTAs per 64 columns and part (of
+// gridDim.y / cluster parts, which share the tiles of 128 tokens), joined in
+// distributed shared memory; `words` gets a row of ldw per part, dY's columns
+// first, the scales' from code_word on.  The grid's first dy_strips are dY's.
 __device__ __forceinline__ uint32_t finite_bits(float x) {
   const uint32_t b = abs_bits(x);
   return b < 0x7f800000u ? b : 0u;
 }
+template <bool A, class T>
+__device__ __forceinline__ void column_maxima(const T* x, int64_t ld, int vec, int64_t rows, int cols, int c, int tgrp,
+                                              uint32_t (&m)[8]) {
+  const int64_t tiles = (rows + kTokTile - 1) / kTokTile;
+  for (int64_t tt = blockIdx.y; tt < tiles; tt += gridDim.y) {
+    const int64_t t0 = tt * kTokTile + tgrp * 4;
+    Raw8<T> r[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) load8<A>(x + (t0 + j) * ld, c, t0 + j < rows ? cols : 0, vec, r[j]);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) m[i] = max(m[i], finite_bits(elt(r[j], i)));
+  }
+}
 template <class T, bool A>
-__global__ void __launch_bounds__(kThreads) k_act8_largest(Mat dy, const float* __restrict__ scales, int64_t nscales,
-                                                           Largest* out, int64_t rows, int cols, int lanes) {
+__global__ void __launch_bounds__(kThreads)
+k_act8_largest(Mat dy, int cols, unsigned dy_strips, const float* __restrict__ scales, int groups, int64_t rows,
+               uint32_t* words, int64_t ldw, int64_t code_word) {
   let_next_start();
-  __shared__ uint32_t slots[kThreads / 32];
-  __shared__ Largest mine;
-  const unsigned ctas = gridDim.x * gridDim.y;
-  const int64_t stride = int64_t(gridDim.x) * (kThreads / lanes);
-  const T* x = static_cast<const T*>(dy.p);
-  uint32_t m = 0, s = 0;
-  for (int64_t row = int64_t(blockIdx.x) * (kThreads / lanes) + threadIdx.x / lanes; row < rows; row += 4 * stride)
-    for (int64_t c = (int64_t(blockIdx.y) * lanes + threadIdx.x % lanes) * 8; c < cols; c += int64_t(gridDim.y) * lanes * 8) {
-      Raw8<T> r[4];
-#pragma unroll
-      for (int u = 0; u < 4; ++u)
-        load8<A>(x + (row + u * stride) * dy.ld, int(c), row + u * stride < rows ? cols : 0, dy.vec, r[u]);
-#pragma unroll
-      for (int u = 0; u < 4; ++u)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) m = max(m, finite_bits(elt(r[u], i)));
-    }
-#pragma unroll 4
-  for (int64_t i = int64_t(blockIdx.y * gridDim.x + blockIdx.x) * kThreads + threadIdx.x; i < nscales;
-       i += int64_t(ctas) * kThreads)
-    s = max(s, finite_bits(__ldg(scales + i)));
-  m = cta_max(m, slots);
-  s = cta_max(s, slots);
-  if (ctas > kColCluster) {
-    if (threadIdx.x == 0) {
-      atomicMax(&out->dy, m);
-      atomicMax(&out->scale, s);
-    }
-    return;
-  }
+  __shared__ uint32_t colmax[kColTile];
   cg::cluster_group cluster = cg::this_cluster();
-  if (threadIdx.x == 0) mine = Largest{s, m};
-  cluster.sync();
-  if (cluster.block_rank() == 0 && threadIdx.x == 0) {
-    for (unsigned k = 1; k < ctas; ++k) {
-      const Largest* l = cluster.map_shared_rank(&mine, k);
-      s = max(s, l->scale);
-      m = max(m, l->dy);
-    }
-    *out = Largest{s, m};
+  const bool codes = blockIdx.x >= dy_strips;
+  const int n = codes ? groups : cols, n0 = int(codes ? blockIdx.x - dy_strips : blockIdx.x) * kColTile;
+  const int cgrp = threadIdx.x & 7, tgrp = threadIdx.x >> 3;     // 8 columns, 4 tokens
+  if (threadIdx.x < kColTile) colmax[threadIdx.x] = 0;
+  __syncthreads();
+  uint32_t m[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+  if (codes) column_maxima<false>(scales, groups, 0, rows, n, n0 + cgrp * 8, tgrp, m);
+  else column_maxima<A>(static_cast<const T*>(dy.p), dy.ld, dy.vec, rows, n, n0 + cgrp * 8, tgrp, m);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {                         // over the warp's 4 token groups, then the CTA
+    m[i] = max(m[i], __shfl_xor_sync(0xffffffffu, m[i], 8));
+    m[i] = max(m[i], __shfl_xor_sync(0xffffffffu, m[i], 16));
+    if ((threadIdx.x & 24) == 0) atomicMax(&colmax[cgrp * 8 + i], m[i]);
   }
-  cluster.sync();                                        // nobody leaves while its word is read
+  const unsigned ctas = cluster.num_blocks();
+  cluster.sync();
+  if (cluster.block_rank() == 0 && threadIdx.x < kColTile) {
+    uint32_t all = 0;
+    for (unsigned k = 0; k < ctas; ++k) all = max(all, *cluster.map_shared_rank(&colmax[threadIdx.x], k));
+    const int at = n0 + int(threadIdx.x);
+    if (at < (n + 7) / 8 * 8) words[int64_t(blockIdx.y / ctas) * ldw + (codes ? code_word : 0) + at] = all;
+  }
+  cluster.sync();                                        // nobody leaves while its words are read
 }
 
 // The e with 2^13 < 2^e x < 2^15 for the x of these bits (0 for zero), within
-// the exponents whose powers are normal.
+// the exponents whose powers are normal.  (The bounds cost nothing: 2^126 x is
+// a multiple of 2^-23, a half's smallest step is 2^-24.)
 __device__ __forceinline__ int power_to(uint32_t bits) {
   return bits == 0u ? 0 : min(max(14 + 127 - int(bits >> 23), -126), 126);
 }
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float(uint32_t(127 + e) << 23); }
 // A value's largest is its scale's 127-fold, 2^7 of it.
-__device__ __forceinline__ int value_power(const Largest* l) {
-  return power_to(l->scale == 0u ? 0u : min(l->scale + (7u << 23), 0x7f000000u));
+__device__ __forceinline__ int value_power(uint32_t scale_bits) {
+  return power_to(scale_bits == 0u ? 0u : min(scale_bits + (7u << 23), 0x7f000000u));
 }
 
 template <int PARTS>
-__device__ __forceinline__ void store_halves(const float (&v)[8], float power, __half* o, int64_t plane, int c,
+__device__ __forceinline__ void store_halves(const float (&v)[8], const int (&e)[8], __half* o, int64_t plane, int c,
                                              int cols) {
   float hi[8], lo[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const float x = v[i] * power;
+    const float x = v[i] * pow2(e[i]);
     hi[i] = __half2float(__float2half_rn(x));
     lo[i] = x - hi[i];
   }
@@ -318,37 +318,73 @@ __device__ __forceinline__ void store_halves(const float (&v)[8], float power, _
 }
 
 // Both operands in one launch: the first code_blocks of blockIdx.y the codes'
-// values, the others dY.  4096 x 4096 codes and fp32 dY: 40 us, 5.5 TB/s.
-template <class T, int CODE_PARTS, bool A>
+// values, the others dY.  A column of dY has its power of two and so has a
+// group of the codes' columns, from the maxima; what undoes them goes to
+// `factor` (dY's columns, then from code_word on the groups).
+template <class T, int CODE_PARTS, int kRows, bool A>
 __global__ void __launch_bounds__(kThreads)
 k_act8_halves(Ckpt k, __half* co, int64_t ldco, int cols_c, Mat dy, __half* dyo, int64_t lddyo, int cols_dy,
-              const Largest* largest, float* factor, int64_t rows, unsigned code_blocks) {
+              const uint32_t* words, int parts, int64_t ldw, int64_t code_word, float* factor, int64_t rows,
+              unsigned code_blocks) {
   let_next_start();
   const bool codes = blockIdx.y < code_blocks;
-  const Piece<1> p(codes ? blockIdx.y : blockIdx.y - code_blocks);
+  const Piece<kRows> p(codes ? blockIdx.y : blockIdx.y - code_blocks);
   if (p.row >= rows || p.c >= (codes ? cols_c : cols_dy)) return;
-  wait_for_pass();
-  const Largest l = *largest;                            // cached: every CTA reads these words
-  float v[8];
-  if (codes) {
-    uint2 w;
-    load_codes8(k.codes + p.row * k.ldc, p.c, cols_c, w);
-    values8(w, __ldg(k.scales + p.row * k.groups + (p.c >> k.shift)), v);
-  } else {
-    Raw8<T> r;
-    load8<A>(static_cast<const T*>(dy.p) + p.row * dy.ld, p.c, cols_dy, dy.vec, r);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = elt(r, i);
-  }
-  const int ec = value_power(&l), ed = power_to(l.dy);
-  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0 && threadIdx.y == 0) {
-    const int e = -(ec + ed);                            // up to 252: two factors of half the exponent
-    factor[0] = pow2(e >> 1);
-    factor[1] = pow2(e - (e >> 1));
-  }
   constexpr int PARTS = sizeof(T) == 4 ? 2 : 1;
-  if (codes) store_halves<CODE_PARTS>(v, pow2(ec), co + p.row * ldco, rows * ldco, p.c, cols_c);
-  else store_halves<PARTS>(v, pow2(ed), dyo + p.row * lddyo, rows * lddyo, p.c, cols_dy);
+  int e[8];
+  if (codes) {
+    const int64_t group = p.c >> k.shift;
+    uint2 w[kRows];
+    float s[kRows];
+#pragma unroll
+    for (int u = 0; u < kRows; ++u) {
+      const int64_t row = p.at(u);
+      load_codes8(k.codes + row * k.ldc, p.c, row < rows ? cols_c : 0, w[u]);
+      s[u] = row < rows ? __ldg(k.scales + row * k.groups + group) : 0.0f;
+    }
+    wait_for_pass();
+    uint32_t top = 0;
+#pragma unroll 4
+    for (int i = 0; i < parts; ++i) top = max(top, words[i * ldw + code_word + group]);
+    const int power = value_power(top);
+    if (p.row == 0 && (p.c & ((1 << k.shift) - 1)) == 0) factor[code_word + group] = pow2(-power);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) e[i] = power;
+#pragma unroll
+    for (int u = 0; u < kRows; ++u) {
+      const int64_t row = p.at(u);
+      float v[8];
+      values8(w[u], s[u], v);
+      if (row < rows) store_halves<CODE_PARTS>(v, e, co + row * ldco, rows * ldco, p.c, cols_c);
+    }
+  } else {
+    Raw8<T> r[kRows];
+#pragma unroll
+    for (int u = 0; u < kRows; ++u)
+      load8<A>(static_cast<const T*>(dy.p) + p.at(u) * dy.ld, p.c, p.at(u) < rows ? cols_dy : 0, dy.vec, r[u]);
+    wait_for_pass();
+    uint32_t top[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll 4
+    for (int i = 0; i < parts; ++i) {
+      const uint4* w = reinterpret_cast<const uint4*>(words + i * ldw + p.c);
+      const uint4 a = w[0], b = w[1];
+      top[0] = max(top[0], a.x), top[1] = max(top[1], a.y), top[2] = max(top[2], a.z), top[3] = max(top[3], a.w);
+      top[4] = max(top[4], b.x), top[5] = max(top[5], b.y), top[6] = max(top[6], b.z), top[7] = max(top[7], b.w);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      e[i] = power_to(top[i]);
+      if (p.row == 0 && p.c + i < cols_dy) factor[p.c + i] = pow2(-e[i]);
+    }
+#pragma unroll
+    for (int u = 0; u < kRows; ++u) {
+      const int64_t row = p.at(u);
+      float v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = elt(r[u], i);
+      if (row < rows) store_halves<PARTS>(v, e, dyo + row * lddyo, rows * lddyo, p.c, cols_dy);
+    }
+  }
 }
 
 // The shares' sums, added in order, into the result (512 x 512: 4.6 us).
@@ -372,16 +408,20 @@ GradPath grad_path(int32_t group) { return group == 0 ? kDigits : kHalves; }
 
 size_t round_up(size_t n, size_t a) { return (n + a - 1) / a * a; }
 
-// Workspace of a gradient: scales (digits) or the largest magnitudes and the
-// result's factors (halves), dY (tokens x out) in the form its product takes,
+// Workspace of a gradient: scales (digits) or the result's factors and the
+// largest magnitudes (halves), dY (tokens x out) in the form its product takes,
 // then, but for digits, the codes' values (code_rows x inner) in 16 bits.
 struct GradPlan {
   GradPath path;
   int dy_parts, code_parts;      // halves of an element
   int64_t ld_dy, ld_code;        // elements
   size_t scale_bytes, dy_bytes, code_bytes;
+  unsigned ctas, parts;          // halves: the search's clusters, and how many share a strip of columns
+  int64_t code_word, ldw;        // of a row of maxima, and of the factors: the first group's, and the length
   int shares;                    // halves: parts of the contraction, and room for their sums
   size_t sum_bytes;
+  int64_t dy_strips() const { return (code_word + kColTile - 1) / kColTile; }
+  int64_t strips() const { return dy_strips() + (ldw - code_word + kColTile - 1) / kColTile; }
   size_t total() const { return scale_bytes + dy_bytes + code_bytes + sum_bytes; }
 };
 GradPlan grad_plan(bool weight, int32_t dtype, int32_t result, int32_t group, int64_t tokens, int64_t out,
@@ -397,7 +437,16 @@ GradPlan grad_plan(bool weight, int32_t dtype, int32_t result, int32_t group, in
   }
   p.dy_parts = dtype == ACT8_FP32 ? 2 : 1;
   p.code_parts = dtype == ACT8_BF16 && result == ACT8_BF16 ? 1 : 2;
-  p.scale_bytes = 256;
+  p.code_word = int64_t(round_up(size_t(out), 8));
+  p.ldw = p.code_word + int64_t(round_up(size_t(group_count(inner, group)), 8));
+  // Enough clusters for every SM's 2048 threads, as far as there are tiles.
+  // (65536 x 64: 10.5 us in 8 parts; 16 take 7.9, but the next pass, which
+  // reads a row of maxima per part, 62 where it takes 50.)
+  const int64_t tiles = (tokens + kTokTile - 1) / kTokTile, strips = p.strips();
+  p.ctas = 1;
+  while (p.ctas < kColCluster && int64_t(p.ctas) < tiles) p.ctas *= 2;
+  p.parts = unsigned(std::max<int64_t>(1, std::min<int64_t>({kMaxParts, 148 * 8 / (strips * p.ctas), tiles / p.ctas})));
+  p.scale_bytes = round_up(size_t(p.parts + 1) * size_t(p.ldw) * 4, 256);
   p.ld_dy = int64_t(round_up(size_t(out), 8));
   p.ld_code = int64_t(round_up(size_t(inner), 8));
   p.dy_bytes = round_up(size_t(tokens) * p.ld_dy * 2 * p.dy_parts, 256);
@@ -460,43 +509,29 @@ shampoo4_status digit_pass(bool weight, const void* dy, int32_t dtype, int64_t l
   }); });
 }
 
-// Both operands as halves at dyp and cp; the result's factors next to the
-// largest magnitudes at `largest`.
+// Both operands as halves at dyp and cp, and the result's factors.
 shampoo4_status halves_pass(const void* dy, int32_t dtype, int64_t lddy, const Ckpt& k, int64_t tokens, int64_t out,
-                            int64_t inner, Largest* largest, float* factor, const GradPlan& p, void* dyp, void* cp,
-                            cudaStream_t st) {
+                            int64_t inner, const GradPlan& p, float* factor, void* dyp, void* cp, cudaStream_t st) {
   const Mat m = mat(dy, lddy, dtype);
   const dim3 b = piece_block(std::max(out, inner));
+  const bool many = many_pieces(tokens, out + inner);
   dim3 g, gc;
-  if (!piece_grid(tokens, out, b, 1, &g) || !piece_grid(tokens, inner, b, 1, &gc) || g.y + gc.y > 65535)
+  if (!piece_grid(tokens, out, b, many ? 4 : 1, &g) || !piece_grid(tokens, inner, b, many ? 4 : 1, &gc) ||
+      g.y + gc.y > 65535)
     return SHAMPOO4_ERR_INVALID_ARG;
   g.y += gc.y;
-  // The search: up to 8 pieces per thread fit one cluster, which needs no
-  // zeroed words, and the next kernel starts under it (4 x 125 x 129: 14.6 ->
-  // 10.6 us in all); more take all SMs.
-  int lanes = 1;
-  while (lanes < kThreads && int64_t(lanes) * 8 < out) lanes *= 2;
-  const int64_t pieces = tokens * ((out + 7) / 8) + tokens * k.groups / 4, room = 148 * 4;
-  const int64_t x = std::min((tokens + kThreads / lanes - 1) / (kThreads / lanes), room);
-  const int64_t y = std::min((out + lanes * 8 - 1) / (lanes * 8), room / x);
-  dim3 ctas{unsigned(x), unsigned(y)}, cluster{1};
-  const bool small = pieces <= int64_t(kColCluster) * kThreads * 8;
-  if (small) {
-    while (cluster.x < kColCluster && cluster.x < x) cluster.x *= 2;
-    while (cluster.x * cluster.y < kColCluster && cluster.y < y) cluster.y *= 2;
-    ctas = cluster;
-  } else {
-    if (x * y <= kColCluster) ctas.x = unsigned(room / y);   // few elements, many scales
-    S4_CUDA(cudaMemsetAsync(largest, 0, sizeof(Largest), st));
-  }
+  uint32_t* words = reinterpret_cast<uint32_t*>(factor + p.ldw);
   return by_dtype(dtype, [&](auto* tag) { return by_flag(m.vec != 0, [&](auto flag) -> shampoo4_status {
     using T = std::remove_pointer_t<decltype(tag)>;
     constexpr bool A = decltype(flag)::value;
-    S4_TRY(start(k_act8_largest<T, A>, ctas, dim3(kThreads), cluster, false, st, m, k.scales,
-                 tokens * k.groups, largest, tokens, int(out), lanes));
-    return start(p.code_parts == 1 ? k_act8_halves<T, 1, A> : k_act8_halves<T, 2, A>, g, b, dim3(1), small, st, k,
-                 static_cast<__half*>(cp), p.ld_code, int(inner), m, static_cast<__half*>(dyp), p.ld_dy, int(out),
-                 largest, factor, tokens, gc.y);
+    S4_TRY(start(k_act8_largest<T, A>, dim3(unsigned(p.strips()), p.ctas * p.parts), dim3(kThreads), dim3(1, p.ctas),
+                 false, st, m, int(out), unsigned(p.dy_strips()), k.scales, k.groups, tokens, words, p.ldw,
+                 p.code_word));
+    const auto kern = p.code_parts == 1 ? (many ? k_act8_halves<T, 1, 4, A> : k_act8_halves<T, 1, 1, A>)
+                                        : (many ? k_act8_halves<T, 2, 4, A> : k_act8_halves<T, 2, 1, A>);
+    return start(kern, g, b, dim3(1), true, st, k, static_cast<__half*>(cp), p.ld_code, int(inner), m,
+                 static_cast<__half*>(dyp), p.ld_dy, int(out), words, int(p.parts), p.ldw, p.code_word, factor, tokens,
+                 gc.y);
   }); });
 }
 
@@ -521,17 +556,16 @@ shampoo4_status grad(bool weight, const void* dy, int32_t dtype, int64_t lddy, c
   }
   char *dyp = w + p.scale_bytes, *cp = dyp + p.dy_bytes;
   // groups: only the weight gradient has them
-  Largest* largest = reinterpret_cast<Largest*>(w);
-  float* factor = reinterpret_cast<float*>(largest + 1);
-  S4_TRY(halves_pass(dy, dtype, lddy, k, tokens, out, inner, largest, factor, p, dyp, cp, st));
+  float* factor = reinterpret_cast<float*>(w);
+  S4_TRY(halves_pass(dy, dtype, lddy, k, tokens, out, inner, p, factor, dyp, cp, st));
+  o.row_scale = factor;
+  o.col_scale = factor + p.code_word;
+  o.col_shift = k.shift;
   const Act8Operand a{cp, p.ld_code, K}, b{dyp, p.ld_dy, tokens};
-  if (p.shares == 1) {
-    o.factor = factor;
-    return launch_act8_halves(a, p.code_parts, b, p.dy_parts, inner, R, K, 1, o, flags, st);
-  }
+  if (p.shares == 1) return launch_act8_halves(a, p.code_parts, b, p.dy_parts, inner, R, K, 1, o, flags, st);
   float* sums = reinterpret_cast<float*>(cp + p.code_bytes);
   S4_TRY(launch_act8_halves(a, p.code_parts, b, p.dy_parts, inner, R, K, p.shares,
-                            Act8Out{sums, inner, ACT8_FP32, 0, nullptr, nullptr, nullptr, factor}, flags, st));
+                            Act8Out{sums, inner, ACT8_FP32, 0, o.row_scale, o.col_scale, nullptr, o.col_shift}, flags, st));
   const unsigned ctas = unsigned(std::min<int64_t>((R * inner + kThreads - 1) / kThreads, 148 * 8));
   return by_dtype(o.dtype, [&](auto* tag) -> shampoo4_status {
     using T = std::remove_pointer_t<decltype(tag)>;
@@ -567,7 +601,7 @@ static shampoo4_status grad_call(bool weight, const void* d_dy, int32_t dtype, i
   if (!mat_ok(d_y, result, M, inner, ldy) || !aligned(d_flags, 4)) return SHAMPOO4_ERR_INVALID_ARG;
   if (K > 0 && (!mat_ok(d_dy, dtype, tokens, out, lddy) || !codes_ok(codes, ldc, inner, scales)))
     return SHAMPOO4_ERR_INVALID_ARG;
-  const Act8Out o{d_y, ldy, result, accumulate ? 1 : 0, nullptr, nullptr, nullptr, nullptr};
+  const Act8Out o{d_y, ldy, result, accumulate ? 1 : 0, nullptr, nullptr, nullptr, 0};
   return grad(weight, d_dy, dtype, lddy, ckpt(codes, ldc, scales, inner, group), group,
               tokens, out, inner, o, d_ws, ws_bytes, d_flags, reinterpret_cast<cudaStream_t>(stream));
 }

@@ -576,7 +576,8 @@ shampoo4_status act8_linear(const void* d_x, int32_t xdtype, int64_t ldx, const 
  *                       below 2^-100 counts as 2^-100); exact integer
  *                       products and sums with the codes.
  *   scales per group    dY and xf to 22 bits, and no finer than 2^-39 of the
- *                       largest in the whole tensor; fp32 sums.  dY and
+ *                       largest over the contraction (dY: of the column; xf:
+ *                       of the group of columns); fp32 sums.  dY and
  *                       the result bfloat16: xf to 11 bits (2^-11, an eighth
  *                       of the result's rounding).
  * A non-finite element of dY, or a non-finite scale, makes every result it

@@ -86,3 +86,73 @@ def test_bfloat16_gradient_over_millions_of_tokens(group):
     want = dy.double().t() @ (codes.double() * scales.double())
     tol = 2.0 ** -11 + 64 * 2.0 ** -22 + 8 * 2.0 ** 6.5 * 2.0 ** -24 / 3 ** 0.5 + half_step("bf16")
     assert ((got - want).abs() <= tol * want).all()
+
+
+# ------------------------------------------ magnitudes far apart, in groups
+
+def group_tops(values, cols, group):
+    """Per column the largest magnitude that its group of columns reaches
+    over all rows, at least (a code may be 126.5 / 127 of its scale's top)."""
+    top = np.abs(values).max(axis=0)
+    out = np.zeros(cols)
+    for c in range(0, cols, group):
+        out[c:c + group] = top[c:c + group].max(initial=0.0)
+    return out * 1.01
+
+
+def grouped_tolerance(dy, codes, scales, group, dtype, result):
+    """dy and value as two halves (a 16-bit dy as one, exact) are off by 2^-22
+    of themselves and by 2^-39 of the largest that dy's column and the value's
+    group of columns have over the tokens; the omitted product of the lower
+    halves is at most 2^-22; at most 17 truncated additions of 2^-22 for each
+    of three kinds of products, a rounding per 256 tokens, and four of the
+    factors and of joining up to 32 shares; a bfloat16 result: the value as
+    one half (2^-11), 65 additions."""
+    v = A.values64(codes, scales, group)
+    a, b, tokens = np.abs(dy), np.abs(v), dy.shape[0]
+    S = a.T @ b
+    floor = 2.0 ** -39 * (a.max(axis=0).reshape(-1, 1) * b.sum(axis=0) + a.sum(axis=0).reshape(-1, 1)
+                          * group_tops(v, v.shape[1], group))
+    one = dtype == result == "bf16"
+    rel = 2.0 ** -11 + 65 * 2.0 ** -22 if one else (4 + 3 * 17) * 2.0 ** -22
+    return S * (rel + (tokens // 256 + 36) * 2.0 ** -24) + floor
+
+
+@pytest.mark.parametrize("dtype,result", [("fp32", "fp32"), ("bf16", "fp32"), ("bf16", "bf16"), ("fp32", "bf16")])
+@pytest.mark.parametrize("tokens,out,inner,group", [(70, 24, 96, 32), (1500, 130, 200, 64), (3000, 9, 520, 256)])
+def test_grouped_gradient_beside_a_loud_channel(tokens, out, inner, group, dtype, result):
+    """One output channel 10^14 times the others, and one group of input
+    columns 10^10 times the others: the quiet results are as precise as alone."""
+    api = _api()
+    rng = np.random.default_rng(tokens)
+    dy = rng.standard_normal((tokens, out)) * 1e-8
+    dy[:, 2] *= 1e14
+    dy[:, 5] = 0
+    x = rng.standard_normal((tokens, inner)).astype(np.float32)
+    x[:, :group] *= 1e10
+    d = torch.from_numpy(dy).to(DT[dtype]).cuda()
+    codes, scales = A.pack(x, group)
+    got = f64(api.act8_weight_grad(d, *to_gpu(codes, scales), group=group, dtype=DT[result]))
+    want = f64(d).T @ A.values64(codes, scales, group)
+    within(got, want, grouped_tolerance(f64(d), codes, scales, group, dtype, result)
+           + half_step(result) * np.abs(want) + TINY[result])
+    assert np.all(got[5] == 0)
+
+
+@pytest.mark.parametrize("up,down", [(1e36, 1e-30), (1e-30, 1e36), (1e-37, 1e-2), (3e-39, 1.0), (1e-20, 1e-20)])
+def test_grouped_gradient_over_the_whole_range(up, down):
+    """The factors that undo the two scalings multiply to more than fp32
+    holds, or to less, where the result does not; and dy next to fp32's
+    smallest numbers keeps its bits (2^126 dy as two halves: a half's smallest
+    step is 2^-24, so dy is off by 2^-151, less than its own step)."""
+    api = _api()
+    rng = np.random.default_rng(7)
+    dy = torch.from_numpy((rng.standard_normal((90, 40)) * up)).float().cuda()
+    x = (rng.standard_normal((90, 96)) * down).astype(np.float32)
+    codes, scales = A.pack(x, 32)
+    got = f64(api.act8_weight_grad(dy, *to_gpu(codes, scales), group=32))
+    want = f64(dy).T @ A.values64(codes, scales, 32)
+    # two factors one after the other may round a subnormal result twice
+    within(got, want, grouped_tolerance(f64(dy), codes, scales, 32, "fp32", "fp32")
+           + half_step("fp32") * np.abs(want) + 2 * TINY["fp32"])
+    assert np.abs(got).max() > 0
