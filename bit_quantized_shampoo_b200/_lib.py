@@ -57,6 +57,11 @@ class Param(C.Structure):
     _fields_ = [("rows", C.c_int64), ("cols", C.c_int64)]
 
 
+class Layer(C.Structure):
+    _fields_ = [("dy", C.c_void_p), ("dtype", C.c_int32), ("lddy", C.c_int64), ("codes", C.c_void_p),
+                ("ldc", C.c_int64), ("scales", C.c_void_p), ("tokens", C.c_int64)]
+
+
 class Shampoo4Error(RuntimeError):
     def __init__(self, fn, status):
         super().__init__(f"{fn} returned {STATUS_NAMES.get(status, status)}")
@@ -112,6 +117,8 @@ _SIGS = {
     "act8_grad_workspace": [_I, _I, _I, _N, _N, _N, _I, c_size_p],
     "act8_weight_grad": [_P, _I, _N, _P, _N, _P, _I, _N, _N, _N, _P, _I, _N, _I, _P, C.c_size_t, _P, _P],
     "act8_input_grad": [_P, _I, _N, _P, _N, _P, _N, _N, _N, _P, _I, _N, _I, _P, C.c_size_t, _P, _P],
+    "shampoo4_weight_grads_workspace": [_P, C.POINTER(Layer), _I, c_size_p],
+    "shampoo4_weight_grads": [_P, C.POINTER(Layer), _I, C.POINTER(_P), c_i64_p, _I, _P, C.c_size_t, _P],
     "act8_swiglu": [_P, _N, _P, _N, _I, _N, _N, _I, _P, _N, _P, _N, _P, _P, _N, _P, _P],
     "act8_swiglu_backward": [_P, _N, _I, _P, _N, _P, _P, _N, _P, _N, _N, _I, _P, _N, _P, _N, _P],
     "shampoo4_timing_enable": [C.c_void_p, C.c_int32],

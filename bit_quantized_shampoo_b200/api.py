@@ -99,19 +99,10 @@ class Shampoo4:
         bf16 or fp16) the gradient of its layer's output and inputs[p] =
         (codes, scales) the layer input as act8_pack or act8_linear stored it.
         ``grads`` (fp32, given or allocated) are overwritten, or added to with
-        ``accumulate`` (micro-batches).  Returns the list of gradients."""
-        if len(dys) != len(self.shapes) or len(inputs) != len(self.shapes):
-            raise ValueError(f"expected {len(self.shapes)} dys and inputs")
-        if grads is None:
-            if accumulate:
-                raise ValueError("accumulate needs grads")
-            grads = [torch.empty(s, dtype=torch.float32, device=self.device) for s in self.shapes]
-        self._ptrs(grads, "grads")
-        for (r, c), dy, (codes, scales), g in zip(self.shapes, dys, inputs, grads):
-            if dy.dim() != 2 or codes.dim() != 2 or dy.shape[1] != r or codes.shape[1] != c:
-                raise ValueError(f"dy and codes must be tokens x {r} and tokens x {c}")
-            act8_weight_grad(dy, codes, scales, group=group, out=g, accumulate=accumulate, stream=stream)
-        return grads
+        ``accumulate`` (micro-batches).  Everything is checked before the
+        first of them is written.  Returns the list of gradients."""
+        return (_act8_module or _act8()).weight_grads(self._h.value, self.state, self.shapes, dys, inputs, group,
+                                                      grads, accumulate, stream)
 
     def refresh_roots(self, stream=None):
         L.call("shampoo4_refresh_roots", self._h, _stream(stream))

@@ -54,4 +54,25 @@ shampoo4_status launch_act8_halves(const Act8Operand& a, int a_parts, const Act8
                                    int64_t R, int64_t K, int shares, const Act8Out& out, uint32_t* flags,
                                    cudaStream_t st);
 
+
+// A gradient as act8_weight_grad and act8_input_grad take it (weight: which).
+struct Act8Grad {
+  bool weight;
+  const void* dy;
+  int32_t dtype;
+  int64_t lddy;
+  const int8_t* codes;
+  int64_t ldc;
+  const float* scales;
+  int32_t group;
+  int64_t tokens, out, inner;
+  void* y;
+  int32_t result;
+  int64_t ldy;
+  int32_t accumulate;
+};
+// Everything that can be refused, and the workspace that the run needs.
+shampoo4_status act8_grad_check(const Act8Grad& g, size_t* bytes);
+shampoo4_status act8_grad_run(const Act8Grad& g, void* ws, uint32_t* flags, cudaStream_t st);
+
 }  // namespace s4

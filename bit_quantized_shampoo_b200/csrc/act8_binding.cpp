@@ -16,7 +16,10 @@
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
+#include <algorithm>
+#include <memory>
 #include <string>
+#include <vector>
 #include "shampoo4.h"
 
 namespace {
@@ -422,6 +425,83 @@ PyObject* grad(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// The items of a list or tuple of n.
+struct Items {
+  PyObject* fast;
+  Items(PyObject* o, Py_ssize_t n, const char* name) : fast(PySequence_Fast(o, name)) {
+    if (!fast) throw Refused();
+    if (PySequence_Fast_GET_SIZE(fast) != n) {
+      Py_DECREF(fast);
+      value_error("expected " + std::to_string(n) + " " + name);
+    }
+  }
+  Items(const Items&) = delete;
+  ~Items() { Py_DECREF(fast); }
+  PyObject* operator[](Py_ssize_t i) const { return PySequence_Fast_GET_ITEM(fast, i); }
+};
+
+// weight_grads(handle, state, shapes, dys, inputs, group, grads, accumulate, stream) -> grads (a new list, or the given one)
+PyObject* weight_grads(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    want_args(n, 9);
+    const auto h = static_cast<shampoo4_handle>(PyLong_AsVoidPtr(a[0]));
+    if (!h) throw Refused();
+    const c10::Device device = tensor(a[1], "state").device();
+    const Py_ssize_t count = PyObject_Length(a[2]);
+    if (count < 0) throw Refused();
+    const Items shapes(a[2], count, "shapes"), dys(a[3], count, "dys"), inputs(a[4], count, "inputs");
+    const int64_t group = integer(a[5], "group");
+    const int add = PyObject_IsTrue(a[7]);
+    if (add < 0) throw Refused();
+    const bool given = a[6] != Py_None;
+    if (add && !given) value_error("accumulate needs grads");
+    std::vector<shampoo4_layer> layers;
+    std::vector<at::Tensor> made;
+    std::vector<float*> grads;
+    std::vector<int64_t> ld;
+    const std::unique_ptr<Items> old(given ? new Items(a[6], count, "grads") : nullptr);
+    for (Py_ssize_t i = 0; i < count; ++i) {
+      const Items shape(shapes[i], 2, "sizes of a shape"), input(inputs[i], 2, "tensors (codes, scales) of an input");
+      const int64_t out = integer(shape[0], "shape"), inner = integer(shape[1], "shape");
+      const Mat dy = mat(dys[i], "dys");
+      same_device(dy.device, device, "dys");
+      const Codes k = codes_on(input[0], input[1], group, "inputs", device);
+      want_shape(dy, k.rows, out, "dys");
+      if (k.cols != inner) value_error("inputs: " + std::to_string(k.cols) + " columns, not " + std::to_string(inner));
+      layers.push_back({dy.p, dy.dtype, dy.ld, k.p, k.ld, k.scales, k.rows});
+      if (!given) continue;
+      const at::Tensor& t = tensor((*old)[i], "grads");
+      if (t.scalar_type() != at::kFloat) type_error("grads must be float32");
+      const Mat g = mat(t, "grads");
+      want_shape(g, out, inner, "grads");
+      same_device(g.device, device, "grads");
+      grads.push_back(static_cast<float*>(g.p));
+      ld.push_back(g.rows > 1 ? g.ld : std::max(g.ld, g.cols));
+    }
+    const Where w(device, a[8]);
+    for (Py_ssize_t i = 0; i < count && !given; ++i) {
+      const Items shape(shapes[i], 2, "sizes of a shape");
+      const int64_t out = integer(shape[0], "shape"), inner = integer(shape[1], "shape");
+      made.push_back(empty(out, inner, inner, at::kFloat, device));
+      grads.push_back(static_cast<float*>(made.back().data_ptr()));
+      ld.push_back(inner);
+    }
+    size_t bytes = 0;
+    check("shampoo4_weight_grads_workspace", shampoo4_weight_grads_workspace(h, layers.data(), int32_t(group), &bytes));
+    const at::Tensor work = w.scratch(int64_t(bytes));
+    check("shampoo4_weight_grads", shampoo4_weight_grads(h, layers.data(), int32_t(group), grads.data(), ld.data(), add,
+                                                         work.data_ptr(), bytes, w.stream()));
+    if (given) {
+      Py_INCREF(a[6]);
+      return a[6];
+    }
+    PyObject* r = PyList_New(count);
+    if (!r) throw Refused();
+    for (Py_ssize_t i = 0; i < count; ++i) PyList_SET_ITEM(r, i, THPVariable_Wrap(made[size_t(i)]));
+    return r;
+  });
+}
+
 // swiglu(gate, up, group, out, stream) -> (h, (gate codes, gate scales, up codes, up scales))
 PyObject* swiglu(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded([&]() -> PyObject* {
@@ -487,7 +567,7 @@ PyObject* set_check(PyObject*, PyObject* f) {
 }
 
 #define S4_FAST(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(name)), METH_FASTCALL, nullptr}
-PyMethodDef g_methods[] = {S4_FAST(pack), S4_FAST(unpack), S4_FAST(matmul), S4_FAST(linear), S4_FAST(grad),
+PyMethodDef g_methods[] = {S4_FAST(pack), S4_FAST(unpack), S4_FAST(matmul), S4_FAST(linear), S4_FAST(grad), S4_FAST(weight_grads),
                            S4_FAST(swiglu), S4_FAST(swiglu_backward),
                            {"set_check", set_check, METH_O, nullptr},
                            {nullptr, nullptr, 0, nullptr}};

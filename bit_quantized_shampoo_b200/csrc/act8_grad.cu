@@ -535,21 +535,38 @@ shampoo4_status halves_pass(const void* dy, int32_t dtype, int64_t lddy, const C
   }); });
 }
 
-// Both gradients: weight: Y[out, inner] = dY^T X; else Y[tokens, inner] = dY W.
-shampoo4_status grad(bool weight, const void* dy, int32_t dtype, int64_t lddy, const Ckpt& k, int32_t group,
-                     int64_t tokens, int64_t out, int64_t inner, Act8Out o, void* ws, size_t ws_bytes,
-                     uint32_t* flags, cudaStream_t st) {
+}  // namespace
+
+shampoo4_status act8_grad_check(const Act8Grad& g, size_t* bytes) {
+  *bytes = 0;
+  if (!shape_ok(g.tokens, g.out) || !shape_ok(0, g.inner) || !dtype_ok(g.dtype) || !dtype_ok(g.result) ||
+      !group_ok(g.group))
+    return SHAMPOO4_ERR_INVALID_ARG;
+  const int64_t M = g.weight ? g.out : g.tokens, K = g.weight ? g.tokens : g.out;
+  if (M == 0 || g.inner == 0) return SHAMPOO4_OK;
+  if (!mat_ok(g.y, g.result, M, g.inner, g.ldy)) return SHAMPOO4_ERR_INVALID_ARG;
+  if (K == 0) return SHAMPOO4_OK;
+  if (!mat_ok(g.dy, g.dtype, g.tokens, g.out, g.lddy) || !codes_ok(g.codes, g.ldc, g.inner, g.scales))
+    return SHAMPOO4_ERR_INVALID_ARG;
+  *bytes = grad_plan(g.weight, g.dtype, g.result, g.group, g.tokens, g.out, g.inner).total();
+  return SHAMPOO4_OK;
+}
+
+// weight: Y[out, inner] = dY^T X; else Y[tokens, inner] = dY W.
+shampoo4_status act8_grad_run(const Act8Grad& g, void* ws, uint32_t* flags, cudaStream_t st) {
+  const bool weight = g.weight;
+  const int64_t tokens = g.tokens, out = g.out, inner = g.inner;
   const int64_t K = weight ? tokens : out, R = weight ? out : tokens;
-  if (K == 0 && o.accumulate) return SHAMPOO4_OK;
+  if (R == 0 || inner == 0 || (K == 0 && g.accumulate)) return SHAMPOO4_OK;
+  Act8Out o{g.y, g.ldy, g.result, g.accumulate ? 1 : 0, nullptr, nullptr, nullptr, 0};
   if (K == 0) return launch_act8_codes(Act8Operand{}, Act8Operand{}, inner, R, 0, o, false, flags, st);   // zeros
-  const GradPlan p = grad_plan(weight, dtype, o.dtype, group, tokens, out, inner);
-  if (!ws || !aligned(ws, 256)) return SHAMPOO4_ERR_INVALID_ARG;
-  if (ws_bytes < p.total()) return SHAMPOO4_ERR_WORKSPACE;
+  const GradPlan p = grad_plan(weight, g.dtype, g.result, g.group, tokens, out, inner);
+  const Ckpt k = ckpt(g.codes, g.ldc, g.scales, inner, g.group);
   char* w = static_cast<char*>(ws);
   if (p.path == kDigits) {
     float* row_scale = reinterpret_cast<float*>(w);
     int8_t* digits = reinterpret_cast<int8_t*>(w + p.scale_bytes);
-    S4_TRY(digit_pass(weight, dy, dtype, lddy, k.scales, tokens, out, digits, p.ld_dy, row_scale, st));
+    S4_TRY(digit_pass(weight, g.dy, g.dtype, g.lddy, k.scales, tokens, out, digits, p.ld_dy, row_scale, st));
     o.row_scale = row_scale;
     return launch_act8_digits(Act8Operand{k.codes, k.ldc, 0}, Act8Operand{digits, p.ld_dy, R}, inner, R, K, o, flags,
                               st);
@@ -557,7 +574,7 @@ shampoo4_status grad(bool weight, const void* dy, int32_t dtype, int64_t lddy, c
   char *dyp = w + p.scale_bytes, *cp = dyp + p.dy_bytes;
   // groups: only the weight gradient has them
   float* factor = reinterpret_cast<float*>(w);
-  S4_TRY(halves_pass(dy, dtype, lddy, k, tokens, out, inner, p, factor, dyp, cp, st));
+  S4_TRY(halves_pass(g.dy, g.dtype, g.lddy, k, tokens, out, inner, p, factor, dyp, cp, st));
   o.row_scale = factor;
   o.col_scale = factor + p.code_word;
   o.col_shift = k.shift;
@@ -575,7 +592,6 @@ shampoo4_status grad(bool weight, const void* dy, int32_t dtype, int64_t lddy, c
   });
 }
 
-}  // namespace
 }  // namespace s4
 
 // ------------------------------------------------------------------ C ABI
@@ -590,20 +606,14 @@ extern "C" shampoo4_status act8_grad_workspace(int32_t weight, int32_t dtype, in
   return SHAMPOO4_OK;
 }
 
-static shampoo4_status grad_call(bool weight, const void* d_dy, int32_t dtype, int64_t lddy, const int8_t* codes,
-                                 int64_t ldc, const float* scales, int32_t group, int64_t tokens, int64_t out,
-                                 int64_t inner, void* d_y, int32_t result, int64_t ldy, int32_t accumulate,
-                                 void* d_ws, size_t ws_bytes, uint32_t* d_flags, shampoo4_stream_t stream) {
-  if (!shape_ok(tokens, out) || !shape_ok(0, inner) || !dtype_ok(dtype) || !dtype_ok(result) || !group_ok(group))
-    return SHAMPOO4_ERR_INVALID_ARG;
-  const int64_t M = weight ? out : tokens, K = weight ? tokens : out;
-  if (M == 0 || inner == 0) return SHAMPOO4_OK;
-  if (!mat_ok(d_y, result, M, inner, ldy) || !aligned(d_flags, 4)) return SHAMPOO4_ERR_INVALID_ARG;
-  if (K > 0 && (!mat_ok(d_dy, dtype, tokens, out, lddy) || !codes_ok(codes, ldc, inner, scales)))
-    return SHAMPOO4_ERR_INVALID_ARG;
-  const Act8Out o{d_y, ldy, result, accumulate ? 1 : 0, nullptr, nullptr, nullptr, 0};
-  return grad(weight, d_dy, dtype, lddy, ckpt(codes, ldc, scales, inner, group), group,
-              tokens, out, inner, o, d_ws, ws_bytes, d_flags, reinterpret_cast<cudaStream_t>(stream));
+static shampoo4_status grad_call(const Act8Grad& g, void* ws, size_t ws_bytes, uint32_t* flags,
+                                 shampoo4_stream_t stream) {
+  size_t bytes = 0;
+  if (!aligned(flags, 4)) return SHAMPOO4_ERR_INVALID_ARG;
+  S4_TRY(act8_grad_check(g, &bytes));
+  if (bytes && (!ws || !aligned(ws, 256))) return SHAMPOO4_ERR_INVALID_ARG;
+  if (ws_bytes < bytes) return SHAMPOO4_ERR_WORKSPACE;
+  return act8_grad_run(g, ws, flags, reinterpret_cast<cudaStream_t>(stream));
 }
 
 extern "C" shampoo4_status act8_weight_grad(const void* d_dy, int32_t dtype, int64_t lddy, const int8_t* d_xc,
@@ -611,8 +621,9 @@ extern "C" shampoo4_status act8_weight_grad(const void* d_dy, int32_t dtype, int
                                             int64_t out, int64_t inner, void* d_dw, int32_t result, int64_t lddw,
                                             int32_t accumulate, void* d_workspace, size_t workspace_bytes,
                                             uint32_t* d_flags, shampoo4_stream_t stream) {
-  return grad_call(true, d_dy, dtype, lddy, d_xc, ldxc, d_xs, group, tokens, out, inner, d_dw, result, lddw,
-                   accumulate, d_workspace, workspace_bytes, d_flags, stream);
+  return grad_call(Act8Grad{true, d_dy, dtype, lddy, d_xc, ldxc, d_xs, group, tokens, out, inner, d_dw, result, lddw,
+                            accumulate},
+                   d_workspace, workspace_bytes, d_flags, stream);
 }
 
 extern "C" shampoo4_status act8_input_grad(const void* d_dy, int32_t dtype, int64_t lddy, const int8_t* d_wc,
@@ -620,7 +631,8 @@ extern "C" shampoo4_status act8_input_grad(const void* d_dy, int32_t dtype, int6
                                            int64_t inner, void* d_dx, int32_t result, int64_t lddx,
                                            int32_t accumulate, void* d_workspace, size_t workspace_bytes,
                                            uint32_t* d_flags, shampoo4_stream_t stream) {
-  return grad_call(false, d_dy, dtype, lddy, d_wc, ldwc, d_ws, 0, tokens, out, inner, d_dx, result, lddx, accumulate,
+  return grad_call(Act8Grad{false, d_dy, dtype, lddy, d_wc, ldwc, d_ws, 0, tokens, out, inner, d_dx, result, lddx,
+                            accumulate},
                    d_workspace, workspace_bytes, d_flags, stream);
 }
 

@@ -596,6 +596,28 @@ shampoo4_status act8_input_grad(const void* d_dy, int32_t dtype, int64_t lddy, c
                                 int32_t result, int64_t lddx, int32_t accumulate, void* d_workspace,
                                 size_t workspace_bytes, uint32_t* d_flags, shampoo4_stream_t stream);
 
+/* The gradients of a handle's parameters, as shampoo4_update_stats takes them:
+ * parameter p of shape out x inner gets act8_weight_grad of layers[p], in
+ * fp32, at d_grads[p] (leading dimension ld[p] >= inner), overwritten or, with
+ * accumulate != 0, added to.  Every layer is checked before anything is
+ * enqueued; no gradient may overlap another or any input.  d_workspace:
+ * shampoo4_weight_grads_workspace bytes, 256-byte aligned, used by one layer
+ * after the other. */
+typedef struct {
+  const void* dy;        /* tokens x out of `dtype`, rows lddy elements apart */
+  int32_t dtype;
+  int64_t lddy;
+  const int8_t* codes;   /* tokens x inner, rows ldc bytes apart */
+  int64_t ldc;
+  const float* scales;   /* tokens x groups */
+  int64_t tokens;
+} shampoo4_layer;
+shampoo4_status shampoo4_weight_grads_workspace(shampoo4_handle h, const shampoo4_layer* layers, int32_t group,
+                                                size_t* bytes);
+shampoo4_status shampoo4_weight_grads(shampoo4_handle h, const shampoo4_layer* layers, int32_t group,
+                                      float* const* d_grads, const int64_t* ld, int32_t accumulate,
+                                      void* d_workspace, size_t workspace_bytes, shampoo4_stream_t stream);
+
 /* The gated activation h = gate * sigmoid(gate) * up (rows x cols, all of
  * `dtype`, fp32 arithmetic rounded once), which keeps gate and up as 8-bit
  * codes in the same pass; and its gradients from those codes:
