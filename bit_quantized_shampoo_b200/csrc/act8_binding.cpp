@@ -491,6 +491,7 @@ PyObject* weight_grads(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const at::Tensor work = w.scratch(int64_t(bytes));
     check("shampoo4_weight_grads", shampoo4_weight_grads(h, layers.data(), int32_t(group), grads.data(), ld.data(), add,
                                                          work.data_ptr(), bytes, w.stream()));
+    for (const at::Tensor& t : made) w.keep(t);
     if (given) {
       Py_INCREF(a[6]);
       return a[6];

@@ -1,5 +1,6 @@
 """Shampoo4.weight_grads: a handle's gradients from 8-bit checkpoints.  What
-cannot be done is refused before anything is written."""
+cannot be done is refused before anything is written, and results on a given
+stream stay allocated."""
 import pytest
 import torch
 
@@ -73,6 +74,28 @@ def test_gradients_are_those_of_the_calls(tokens, group):
     sh.weight_grads(dys, xs, group=group, grads=given, accumulate=True)
     assert all(torch.equal(g, 2 * w) for g, w in zip(given, want))
     assert sh.status_flags() == 0
+
+
+def test_gradients_dropped_early_stay_with_the_given_stream():
+    """Gradients made for another stream and dropped at once: what is
+    allocated next must not share their memory while that stream still writes."""
+    api = _api()
+    shapes = [(1024, 4096), (1024, 4096)]
+    sh = api.Shampoo4(shapes)
+    side = torch.cuda.Stream()
+    dys = [data(4096, 1024, "bf16", 5, scale=0.01) for _ in shapes]
+    xs = [stored(4096, 4096, 6)[0]] * 2
+    sh.weight_grads(dys, xs, stream=side)
+    torch.cuda.synchronize()
+    bad = 0
+    for _ in range(5):
+        for _ in range(4):
+            sh.weight_grads(dys, xs, stream=side)
+        mark = [torch.full(s, 3.0, device="cuda") for s in shapes]
+        side.synchronize()
+        bad += sum(int((m != 3.0).any()) for m in mark)
+        del mark
+    assert bad == 0
 
 
 def test_gradients_captured_and_replayed():
