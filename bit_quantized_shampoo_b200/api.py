@@ -100,7 +100,8 @@ class Shampoo4:
         (codes, scales) the layer input as act8_pack or act8_linear stored it.
         ``grads`` (fp32, given or allocated) are overwritten, or added to with
         ``accumulate`` (micro-batches).  Everything is checked before the
-        first of them is written.  Returns the list of gradients."""
+        first of them is written; a wait that expired in a product is in
+        status_flags().  Returns the list of gradients."""
         return (_act8_module or _act8()).weight_grads(self._h.value, self.state, self.shapes, dys, inputs, group,
                                                       grads, accumulate, stream)
 
@@ -340,8 +341,10 @@ def quant4_tables(codebook="linear_square"):
 # allocated, and must not overlap inputs; ``stream`` defaults to the current
 # stream of the tensors' device (another one has to wait for the current one
 # before the call, and the current one for it before the results are used).
-# Arguments that do not fit raise TypeError or ValueError before anything is
-# enqueued.  The checks and calls are in csrc/act8_binding.cpp: the smallest
+# Arguments that do not fit raise TypeError, ValueError or Shampoo4Error before
+# anything is enqueued.  The products' ``flags`` is an int32 word of the caller's,
+# in which a wait that expired raises FLAG_TIMEOUT (its result is then not
+# valid); without one it goes unreported.  The checks and calls are in csrc/act8_binding.cpp: the smallest
 # of these calls take a few microseconds, less than the same checks in Python.
 
 def _act8():

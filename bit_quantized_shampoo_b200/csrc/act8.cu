@@ -473,7 +473,7 @@ static shampoo4_status matmul(const int8_t* xc, int64_t ldxc, const float* xs, c
   // no columns: no group, so no scale either
   const Act8Out o{y, ldy, dtype, 0, inner > 0 ? xs : nullptr, inner > 0 ? ws : nullptr, bias, 0};
   return launch_act8_codes(Act8Operand{wc, ldwc, 0}, Act8Operand{xc, ldxc, 0}, out, tokens, inner, o, after_pack,
-                           flags, st);
+                           Act8Watch{flags}, st);
 }
 
 extern "C" shampoo4_status act8_matmul(const int8_t* d_xc, int64_t ldxc, const float* d_xs, const int8_t* d_wc,

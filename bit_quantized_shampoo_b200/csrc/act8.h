@@ -31,6 +31,14 @@ struct Act8Out {
   int32_t col_shift;                                   // halves: column m has col_scale[m >> col_shift]
 };
 
+// Where a product raises SHAMPOO4_FLAG_TIMEOUT (may be null), and the limit of
+// its waits (0: 2 s).  The loads, whose barriers also tell that nothing is
+// under way when a CTA leaves, keep the 2 s.
+struct Act8Watch {
+  uint32_t* flags = nullptr;
+  uint64_t wait_ns = 0;
+};
+
 // All products: Y[r, m] = row_scale[r] col_scale[m] sum_k B[r, k] A[m, k] + bias[m].
 
 // int8 codes both: a is M x K, b is R x K (K contiguous).  after_pass: b was
@@ -38,11 +46,11 @@ struct Act8Out {
 // the launch may then overlap that kernel's end.  (The others always
 // follow their own operand pass.)
 shampoo4_status launch_act8_codes(const Act8Operand& a, const Act8Operand& b, int64_t M, int64_t R, int64_t K,
-                                  const Act8Out& out, bool after_pass, uint32_t* flags, cudaStream_t st);
+                                  const Act8Out& out, bool after_pass, Act8Watch watch, cudaStream_t st);
 // a: codes K x M (M contiguous); b: kAct8Digits planes of R x K digits, most
 // significant first: B = 65536 d0 + 256 d1 + d2.
 shampoo4_status launch_act8_digits(const Act8Operand& a, const Act8Operand& b, int64_t M, int64_t R, int64_t K,
-                                   const Act8Out& out, uint32_t* flags, cudaStream_t st);
+                                   const Act8Out& out, Act8Watch watch, cudaStream_t st);
 // Halves both, operands the sums of their planes: a is K x M in a_parts, b is
 // K x R in b_parts: 2 and 1 or 2 (the product of the second planes is left
 // out), or 1 and 1.
@@ -51,7 +59,7 @@ shampoo4_status launch_act8_digits(const Act8Operand& a, const Act8Operand& b, i
 // R x M each, for the caller to add up.
 int act8_halves_shares(int64_t M, int64_t R, int64_t K);
 shampoo4_status launch_act8_halves(const Act8Operand& a, int a_parts, const Act8Operand& b, int b_parts, int64_t M,
-                                   int64_t R, int64_t K, int shares, const Act8Out& out, uint32_t* flags,
+                                   int64_t R, int64_t K, int shares, const Act8Out& out, Act8Watch watch,
                                    cudaStream_t st);
 
 
@@ -73,6 +81,6 @@ struct Act8Grad {
 };
 // Everything that can be refused, and the workspace that the run needs.
 shampoo4_status act8_grad_check(const Act8Grad& g, size_t* bytes);
-shampoo4_status act8_grad_run(const Act8Grad& g, void* ws, uint32_t* flags, cudaStream_t st);
+shampoo4_status act8_grad_run(const Act8Grad& g, void* ws, Act8Watch watch, cudaStream_t st);
 
 }  // namespace s4

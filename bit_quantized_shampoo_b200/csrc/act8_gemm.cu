@@ -27,9 +27,11 @@
 //
 // Warp roles (320 threads): warp 0 issues the TMA loads, warp 1 of the leader
 // the MMAs, warps 2..9 drain the accumulator, two per lane quarter with half of
-// the rows each.  Every wait is bounded (2 s);
-// on expiry a role raises SHAMPOO4_FLAG_TIMEOUT and stops, and the pair waits
-// for what it issued before it frees tensor memory and leaves.
+// the rows each.  Every wait is bounded; on expiry a role raises
+// SHAMPOO4_FLAG_TIMEOUT and stops, and the pair waits for its MMAs before it
+// frees tensor memory and leaves.  The loads' waits are bounded by 2 s whatever
+// the others' limit: a CTA leaves when every stage that it filled has been
+// read, or 2 s after it issued the last one.
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -85,6 +87,7 @@ struct GemmArgs {
   int32_t shares, share_blocks;            // pairs: parts of the contraction, k-blocks of each
   int64_t share_stride;                    // and elements of Y from one part's sums to the next
   uint32_t* flags;
+  uint64_t wait_ns;                        // limit of the MMAs' and the epilogue's waits
   Act8Out out;
 };
 
@@ -421,7 +424,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_act8_gemm(const __grid_cons
         bool some = true;                                   // no k-blocks at all: an empty sum
         for (int kb = t % shares * g.share_blocks; ok && some; ++i) {
           const int ab = i & 1;
-          ok = __all_sync(0xffffffffu, mbar_wait(&acc_empty[ab], ((i >> 1) & 1) ^ 1));
+          ok = __all_sync(0xffffffffu, mbar_wait(&acc_empty[ab], ((i >> 1) & 1) ^ 1, g.wait_ns));
           if (!ok) break;
           fence_after_sync();
           const uint32_t d = tmem + uint32_t(ab * C::kAccCols);
@@ -429,7 +432,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_act8_gemm(const __grid_cons
           const int k_first = kb;
           for (; kb < k_end; ++kb) {
             if (!__all_sync(0xffffffffu, ready)) {
-              ok = __all_sync(0xffffffffu, mbar_wait(&full_bar[s], phase));
+              ok = __all_sync(0xffffffffu, mbar_wait(&full_bar[s], phase, g.wait_ns));
               if (!ok) break;
             }
             fence_after_sync();
@@ -504,7 +507,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_act8_gemm(const __grid_cons
       float sum[C::CHUNK ? kChunks : 1][32];
       for (int pass = 0; pass < passes; ++pass, ++i) {
         const int ab = i & 1;
-        if (!mbar_wait(&acc_full[ab], (i >> 1) & 1)) {
+        // the whole warp goes on or stops: what follows is collective
+        if (!__all_sync(0xffffffffu, mbar_wait(&acc_full[ab], (i >> 1) & 1, g.wait_ns))) {
           if (g.flags && lane == 0) atomicOr(g.flags, SHAMPOO4_FLAG_TIMEOUT);
           ok = false;
           break;
@@ -689,7 +693,7 @@ __global__ void __launch_bounds__(kSmallThreads, 2) k_act8_small(const __grid_co
     bool ok = true;
     for (int it = 0; it < kb1 - kb0; ++it) {
       const int s = it % C::STAGES;
-      ok = __all_sync(0xffffffffu, mbar_wait(&full_bar[s], (it / C::STAGES) & 1));
+      ok = __all_sync(0xffffffffu, mbar_wait(&full_bar[s], (it / C::STAGES) & 1, g.wait_ns));
       if (!ok) break;
       fence_after_sync();
       const uint32_t a0 = base + uint32_t(s) * (C::kStage >> 4), b0 = a0 + (C::kATile >> 4);
@@ -860,9 +864,10 @@ shampoo4_status allow_smem(const void* kern, int dev) {
 
 template <class C>
 shampoo4_status fill_args(GemmArgs& g, const Act8Operand& a, int a_planes, const Act8Operand& b, int b_planes,
-                          int64_t M, int64_t R, int64_t K, const Act8Out& out, uint32_t* flags) {
+                          int64_t M, int64_t R, int64_t K, const Act8Out& out, Act8Watch watch) {
   g.out = out;
-  g.flags = flags;
+  g.flags = watch.flags;
+  g.wait_ns = watch.wait_ns == 0 || watch.wait_ns > kWaitNs ? kWaitNs : watch.wait_ns;
   g.M = int32_t(M);
   g.R = int32_t(R);
   g.kblocks = int32_t((K + C::kK - 1) / C::kK);
@@ -905,9 +910,9 @@ shampoo4_status start(K kern, int threads, dim3 grid, dim3 cluster, int smem, bo
 // shares > 1: Y receives that many fp32 sums of R x M, one after the other.
 template <class C>
 shampoo4_status launch(const Act8Operand& a, const Act8Operand& b, int64_t M, int64_t R, int64_t K,
-                       const Act8Out& out, bool after_pass, uint32_t* flags, cudaStream_t st, int shares = 1) {
+                       const Act8Out& out, bool after_pass, Act8Watch watch, cudaStream_t st, int shares = 1) {
   GemmArgs g{};
-  S4_TRY(fill_args<C>(g, a, C::PA, b, C::PB * C::ND, M, R, K, out, flags));
+  S4_TRY(fill_args<C>(g, a, C::PA, b, C::PB * C::ND, M, R, K, out, watch));
   if (shares > 1) {
     g.share_blocks = (g.kblocks + shares - 1) / shares;
     g.shares = shares;
@@ -923,9 +928,9 @@ shampoo4_status launch(const Act8Operand& a, const Act8Operand& b, int64_t M, in
 
 template <class C>
 shampoo4_status launch_small(const Act8Operand& a, const Act8Operand& b, int64_t M, int64_t R, int64_t K, int shares,
-                             const Act8Out& out, bool after_pass, uint32_t* flags, cudaStream_t st) {
+                             const Act8Out& out, bool after_pass, Act8Watch watch, cudaStream_t st) {
   GemmArgs g{};
-  S4_TRY(fill_args<C>(g, a, 1, b, C::ND, M, R, K, out, flags));
+  S4_TRY(fill_args<C>(g, a, 1, b, C::ND, M, R, K, out, watch));
   int dev = 0, sms = 0;
   S4_TRY(device_sms(&dev, &sms));
   auto kern = k_act8_small<C>;
@@ -973,26 +978,26 @@ using HalvesCfg = Cfg<           kHalf, true,  true,  128, 2, PB, 1, 2, STAGES, 
 using HalfCfg = Cfg<             kHalf, true,  true,  256, 1, 1,  1, 2, 6, 16>;
 
 shampoo4_status launch_act8_codes(const Act8Operand& a, const Act8Operand& b, int64_t M, int64_t R, int64_t K,
-                                  const Act8Out& out, bool after_pass, uint32_t* flags, cudaStream_t st) {
+                                  const Act8Out& out, bool after_pass, Act8Watch watch, cudaStream_t st) {
   const int rows[] = {16, 64, 128};
   const Form f = choose_form(M, R, K, CodesCfg::R, 1, rows, 3);
-  if (f.rows == 16) return launch_small<SmallCfg<false, 16, 1, 5>>(a, b, M, R, K, f.shares, out, after_pass, flags, st);
-  if (f.rows == 64) return launch_small<SmallCfg<false, 64, 1, 4>>(a, b, M, R, K, f.shares, out, after_pass, flags, st);
+  if (f.rows == 16) return launch_small<SmallCfg<false, 16, 1, 5>>(a, b, M, R, K, f.shares, out, after_pass, watch, st);
+  if (f.rows == 64) return launch_small<SmallCfg<false, 64, 1, 4>>(a, b, M, R, K, f.shares, out, after_pass, watch, st);
   if (f.rows == 128)
-    return launch_small<SmallCfg<false, 128, 1, 3>>(a, b, M, R, K, f.shares, out, after_pass, flags, st);
-  return launch<CodesCfg>(a, b, M, R, K, out, after_pass, flags, st);
+    return launch_small<SmallCfg<false, 128, 1, 3>>(a, b, M, R, K, f.shares, out, after_pass, watch, st);
+  return launch<CodesCfg>(a, b, M, R, K, out, after_pass, watch, st);
 }
 
 shampoo4_status launch_act8_digits(const Act8Operand& a, const Act8Operand& b, int64_t M, int64_t R, int64_t K,
-                                   const Act8Out& out, uint32_t* flags, cudaStream_t st) {
+                                   const Act8Out& out, Act8Watch watch, cudaStream_t st) {
   const int rows[] = {16, 32};
   // the small form keeps its integer sums whole
   const Form f = K <= kAct8MaxInner ? choose_form(M, R, K, DigitsCfg::R, kAct8Digits, rows, 2) : Form{0, 1};
   if (f.rows == 16)
-    return launch_small<SmallCfg<true, 16, kAct8Digits, 4>>(a, b, M, R, K, f.shares, out, true, flags, st);
+    return launch_small<SmallCfg<true, 16, kAct8Digits, 4>>(a, b, M, R, K, f.shares, out, true, watch, st);
   if (f.rows == 32)
-    return launch_small<SmallCfg<true, 32, kAct8Digits, 3>>(a, b, M, R, K, f.shares, out, true, flags, st);
-  return launch<DigitsCfg>(a, b, M, R, K, out, true, flags, st);
+    return launch_small<SmallCfg<true, 32, kAct8Digits, 3>>(a, b, M, R, K, f.shares, out, true, watch, st);
+  return launch<DigitsCfg>(a, b, M, R, K, out, true, watch, st);
 }
 
 // The estimated time (us): 0.5 per k-block and 2 per wave of tiles; the join
@@ -1013,11 +1018,11 @@ int act8_halves_shares(int64_t M, int64_t R, int64_t K) {
 }
 
 shampoo4_status launch_act8_halves(const Act8Operand& a, int a_parts, const Act8Operand& b, int b_parts, int64_t M,
-                                   int64_t R, int64_t K, int shares, const Act8Out& out, uint32_t* flags,
+                                   int64_t R, int64_t K, int shares, const Act8Out& out, Act8Watch watch,
                                    cudaStream_t st) {
-  if (a_parts == 1) return launch<HalfCfg>(a, b, M, R, K, out, true, flags, st, shares);
-  return b_parts == 1 ? launch<HalvesCfg<1, 5>>(a, b, M, R, K, out, true, flags, st, shares)
-                      : launch<HalvesCfg<2, 4>>(a, b, M, R, K, out, true, flags, st, shares);
+  if (a_parts == 1) return launch<HalfCfg>(a, b, M, R, K, out, true, watch, st, shares);
+  return b_parts == 1 ? launch<HalvesCfg<1, 5>>(a, b, M, R, K, out, true, watch, st, shares)
+                      : launch<HalvesCfg<2, 4>>(a, b, M, R, K, out, true, watch, st, shares);
 }
 
 }  // namespace s4

@@ -553,13 +553,13 @@ shampoo4_status act8_grad_check(const Act8Grad& g, size_t* bytes) {
 }
 
 // weight: Y[out, inner] = dY^T X; else Y[tokens, inner] = dY W.
-shampoo4_status act8_grad_run(const Act8Grad& g, void* ws, uint32_t* flags, cudaStream_t st) {
+shampoo4_status act8_grad_run(const Act8Grad& g, void* ws, Act8Watch watch, cudaStream_t st) {
   const bool weight = g.weight;
   const int64_t tokens = g.tokens, out = g.out, inner = g.inner;
   const int64_t K = weight ? tokens : out, R = weight ? out : tokens;
   if (R == 0 || inner == 0 || (K == 0 && g.accumulate)) return SHAMPOO4_OK;
   Act8Out o{g.y, g.ldy, g.result, g.accumulate ? 1 : 0, nullptr, nullptr, nullptr, 0};
-  if (K == 0) return launch_act8_codes(Act8Operand{}, Act8Operand{}, inner, R, 0, o, false, flags, st);   // zeros
+  if (K == 0) return launch_act8_codes(Act8Operand{}, Act8Operand{}, inner, R, 0, o, false, watch, st);   // zeros
   const GradPlan p = grad_plan(weight, g.dtype, g.result, g.group, tokens, out, inner);
   const Ckpt k = ckpt(g.codes, g.ldc, g.scales, inner, g.group);
   char* w = static_cast<char*>(ws);
@@ -568,7 +568,7 @@ shampoo4_status act8_grad_run(const Act8Grad& g, void* ws, uint32_t* flags, cuda
     int8_t* digits = reinterpret_cast<int8_t*>(w + p.scale_bytes);
     S4_TRY(digit_pass(weight, g.dy, g.dtype, g.lddy, k.scales, tokens, out, digits, p.ld_dy, row_scale, st));
     o.row_scale = row_scale;
-    return launch_act8_digits(Act8Operand{k.codes, k.ldc, 0}, Act8Operand{digits, p.ld_dy, R}, inner, R, K, o, flags,
+    return launch_act8_digits(Act8Operand{k.codes, k.ldc, 0}, Act8Operand{digits, p.ld_dy, R}, inner, R, K, o, watch,
                               st);
   }
   char *dyp = w + p.scale_bytes, *cp = dyp + p.dy_bytes;
@@ -579,10 +579,10 @@ shampoo4_status act8_grad_run(const Act8Grad& g, void* ws, uint32_t* flags, cuda
   o.col_scale = factor + p.code_word;
   o.col_shift = k.shift;
   const Act8Operand a{cp, p.ld_code, K}, b{dyp, p.ld_dy, tokens};
-  if (p.shares == 1) return launch_act8_halves(a, p.code_parts, b, p.dy_parts, inner, R, K, 1, o, flags, st);
+  if (p.shares == 1) return launch_act8_halves(a, p.code_parts, b, p.dy_parts, inner, R, K, 1, o, watch, st);
   float* sums = reinterpret_cast<float*>(cp + p.code_bytes);
   S4_TRY(launch_act8_halves(a, p.code_parts, b, p.dy_parts, inner, R, K, p.shares,
-                            Act8Out{sums, inner, ACT8_FP32, 0, o.row_scale, o.col_scale, nullptr, o.col_shift}, flags, st));
+                            Act8Out{sums, inner, ACT8_FP32, 0, o.row_scale, o.col_scale, nullptr, o.col_shift}, watch, st));
   const unsigned ctas = unsigned(std::min<int64_t>((R * inner + kThreads - 1) / kThreads, 148 * 8));
   return by_dtype(o.dtype, [&](auto* tag) -> shampoo4_status {
     using T = std::remove_pointer_t<decltype(tag)>;
@@ -613,7 +613,7 @@ static shampoo4_status grad_call(const Act8Grad& g, void* ws, size_t ws_bytes, u
   S4_TRY(act8_grad_check(g, &bytes));
   if (bytes && (!ws || !aligned(ws, 256))) return SHAMPOO4_ERR_INVALID_ARG;
   if (ws_bytes < bytes) return SHAMPOO4_ERR_WORKSPACE;
-  return act8_grad_run(g, ws, flags, reinterpret_cast<cudaStream_t>(stream));
+  return act8_grad_run(g, ws, Act8Watch{flags}, reinterpret_cast<cudaStream_t>(stream));
 }
 
 extern "C" shampoo4_status act8_weight_grad(const void* d_dy, int32_t dtype, int64_t lddy, const int8_t* d_xc,

@@ -2320,7 +2320,8 @@ extern "C" shampoo4_status shampoo4_weight_grads(shampoo4_handle h, const shampo
   if (bytes && (!d_workspace || !aligned(d_workspace, 256))) return SHAMPOO4_ERR_INVALID_ARG;
   if (workspace_bytes < bytes) return SHAMPOO4_ERR_WORKSPACE;
   if (!h->bound) return SHAMPOO4_ERR_NOT_READY;
-  for (const Act8Grad& g : calls) S4_TRY(act8_grad_run(g, d_workspace, nullptr, reinterpret_cast<cudaStream_t>(stream)));
+  const Act8Watch watch{reinterpret_cast<uint32_t*>(h->d_ws + h->ws_flags), h->wait_ns};
+  for (const Act8Grad& g : calls) S4_TRY(act8_grad_run(g, d_workspace, watch, reinterpret_cast<cudaStream_t>(stream)));
   return SHAMPOO4_OK;
 }
 

@@ -325,11 +325,12 @@ shampoo4_status shampoo4_debug_capture_layout(shampoo4_handle h, int32_t factor,
  * keeps the state). */
 shampoo4_status shampoo4_debug_refresh_parts(shampoo4_handle h, int32_t parts);
 
-/* Diagnostic: the time limit of the tensor-core products' pipeline waits
- * (a CTA waiting for a free stage, for loaded operands or for its finished
- * accumulator).  On expiry a CTA raises SHAMPOO4_FLAG_TIMEOUT, issues
- * nothing more, waits (up to 2 s) for the loads and MMAs it already issued,
- * frees its tensor memory and exits; the call's outputs are then undefined,
+/* Diagnostic: the time limit of the handle's tensor-core products' pipeline
+ * waits, shampoo4_weight_grads' among them (a CTA waiting for a free stage,
+ * for loaded operands or for its finished accumulator; shampoo4_weight_grads'
+ * loads keep the default).  On expiry a CTA raises SHAMPOO4_FLAG_TIMEOUT,
+ * issues no more products, waits (up to 2 s) for the loads and MMAs it already
+ * issued, frees its tensor memory and exits; the call's outputs are then undefined,
  * the handle and the CUDA context stay usable.  ns = 0 restores the default
  * of 2 s, which is also the largest limit.  Used by the tests to exercise
  * that return path; it takes effect at the next launch. */
@@ -599,8 +600,8 @@ shampoo4_status act8_input_grad(const void* d_dy, int32_t dtype, int64_t lddy, c
 /* The gradients of a handle's parameters, as shampoo4_update_stats takes them:
  * parameter p of shape out x inner gets act8_weight_grad of layers[p], in
  * fp32, at d_grads[p] (leading dimension ld[p] >= inner), overwritten or, with
- * accumulate != 0, added to.  Every layer is checked before anything is
- * enqueued; no gradient may overlap another or any input.  d_workspace:
+ * accumulate != 0, added to.  An expired wait of a product is in the handle's
+ * status flags.  Every layer is checked before anything is enqueued; no gradient may overlap another or any input.  d_workspace:
  * shampoo4_weight_grads_workspace bytes, 256-byte aligned, used by one layer
  * after the other. */
 typedef struct {

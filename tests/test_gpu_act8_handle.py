@@ -1,9 +1,10 @@
 """Shampoo4.weight_grads: a handle's gradients from 8-bit checkpoints.  What
-cannot be done is refused before anything is written, and results on a given
-stream stay allocated."""
+cannot be done is refused before anything is written, results on a given
+stream stay allocated, and an expired wait shows in the handle's flags."""
 import pytest
 import torch
 
+from bit_quantized_shampoo_b200 import _lib as L
 from test_gpu_act8 import data, stored
 
 pytestmark = pytest.mark.gpu
@@ -113,3 +114,24 @@ def test_gradients_captured_and_replayed():
     torch.cuda.synchronize()
     assert all(torch.equal(g, w) for g, w in zip(grads, want))
     del graph
+
+
+def test_an_expired_wait_is_in_the_handles_flags():
+    """With a limit of 1 ns the epilogue gives up on a sum over 20000 tokens
+    (some 40 us; a wait below a few us ends inside the first try and cannot
+    run out), the products on their accumulators; the loads are waited for with
+    the ordinary limit, and the call returns.  With the default limit the next
+    call is right."""
+    api = _api()
+    shape, tokens = (1024, 2048), 20000
+    sh = api.Shampoo4([shape])
+    dys = [data(tokens, shape[0], "bf16", 7, scale=0.01)]
+    xs = [stored(tokens, shape[1], 8)[0]]
+    want = [g.clone() for g in sh.weight_grads(dys, xs)]
+    assert sh.status_flags() == 0
+    L.call("shampoo4_debug_wait_limit", sh._h, 1)
+    sh.weight_grads(dys, xs)
+    assert sh.status_flags() & L.FLAG_TIMEOUT
+    L.call("shampoo4_debug_wait_limit", sh._h, 0)
+    got = sh.weight_grads(dys, xs)
+    assert sh.status_flags() == 0 and torch.equal(got[0], want[0])
