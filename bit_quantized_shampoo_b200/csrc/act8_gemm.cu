@@ -413,6 +413,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_act8_gemm(const __grid_cons
     // branch the issue, about 600 clocks a k-block, was the bound: 266 against
     // 234 us at 8192 x 11008 x 4096.)
     if (rank == 0) {
+      wait_previous();                                      // the limits count from here on
       constexpr uint32_t id = idesc<C>();
       constexpr int kParts = C::PA > C::PB ? C::PA : C::PB;
       const uint32_t base = smem_u32(smem) >> 4;
@@ -691,6 +692,7 @@ __global__ void __launch_bounds__(kSmallThreads, 2) k_act8_small(const __grid_co
                             (uint32_t(C::kN >> 3) << 17) | (uint32_t(kLanes >> 4) << 24);
     const uint32_t base = smem_u32(smem) >> 4;
     bool ok = true;
+    wait_previous();                                        // the limits count from here on
     for (int it = 0; it < kb1 - kb0; ++it) {
       const int s = it % C::STAGES;
       ok = __all_sync(0xffffffffu, mbar_wait(&full_bar[s], (it / C::STAGES) & 1, g.wait_ns));

@@ -135,3 +135,20 @@ def test_an_expired_wait_is_in_the_handles_flags():
     L.call("shampoo4_debug_wait_limit", sh._h, 0)
     got = sh.weight_grads(dys, xs)
     assert sh.status_flags() == 0 and torch.equal(got[0], want[0])
+
+
+def test_time_spent_by_the_operand_pass_does_not_count():
+    """The product starts under the pass that writes its operand and waits for
+    it.  The pass over 2^23 tokens of 64 columns has 8 CTAs and takes about 14
+    ms; the longest wait of the product itself, for 1024 k-blocks, is below
+    half a millisecond and must not run out at 4 ms."""
+    api = _api()
+    sh = api.Shampoo4([(64, 64)])
+    tokens = 1 << 23
+    dys = [torch.ones(tokens, 64, dtype=torch.bfloat16, device="cuda")]
+    xs = [(torch.ones(tokens, 64, dtype=torch.int8, device="cuda"), torch.ones(tokens, 1, device="cuda"))]
+    L.call("shampoo4_debug_wait_limit", sh._h, 4000000)
+    g, = sh.weight_grads(dys, xs)
+    assert sh.status_flags() == 0
+    # exact sums of 2^17 tokens, 64 of them added in fp32, six roundings of digits and scales
+    assert ((g.double() - tokens).abs() <= tokens * 70 * 2.0 ** -24).all()
