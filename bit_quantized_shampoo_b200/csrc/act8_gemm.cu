@@ -312,8 +312,10 @@ __device__ __forceinline__ void store_any(const Act8Out& o, int R, int M, int r0
   else if (o.dtype == ACT8_BF16) store_chunk<__nv_bfloat16>(o, R, M, r0, m, cs, bias, rs, v);
   else store_chunk<__half>(o, R, M, r0, m, cs, bias, rs, v);
 }
+// Written by the pass that this kernel may overlap, so not through the
+// read-only path: that holds for memory nobody writes while the kernel runs.
 __device__ __forceinline__ float row_scale(const Act8Out& o, int R, int r) {
-  return o.row_scale && r < R ? __ldg(o.row_scale + r) : 1.0f;
+  return o.row_scale && r < R ? __ldcg(o.row_scale + r) : 1.0f;
 }
 
 template <class C>
@@ -492,7 +494,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) k_act8_gemm(const __grid_cons
       tile_of(g, t / shares, tm, tr);
       const int m = (tm * C::CG + int(rank)) * kLanes + 32 * q + lane, r0 = tr * C::R + 32 * c0;
       const float cs = g.out.col_scale && m < g.M
-                           ? __ldg(g.out.col_scale + (C::KIND == kHalf ? m >> g.out.col_shift : m)) : 1.0f;
+                           ? __ldcg(g.out.col_scale + (C::KIND == kHalf ? m >> g.out.col_shift : m)) : 1.0f;
       const float bias = g.out.bias && m < g.M ? __ldg(g.out.bias + m) : 0.0f;
       float* rs = g.out.row_scale ? row_scales[warp - 2] : nullptr;   // fetched under the products
       if (rs) {
@@ -785,7 +787,7 @@ __global__ void __launch_bounds__(kSmallThreads, 2) k_act8_small(const __grid_co
 #pragma unroll
           for (int e = 0; e < 4; ++e) v[e] = fmaf(v[e], 256.0f, __int2float_rn(sum[e]));
         }
-        const float rs = g.out.row_scale ? __ldg(g.out.row_scale + r0 + j) : 1.0f;
+        const float rs = row_scale(g.out, g.R, r0 + j);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const float cs = g.out.col_scale && m + e < g.M ? __ldg(g.out.col_scale + m + e) : 1.0f;

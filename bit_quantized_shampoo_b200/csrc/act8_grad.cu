@@ -345,7 +345,7 @@ k_act8_halves(Ckpt k, __half* co, int64_t ldco, int cols_c, Mat dy, __half* dyo,
     wait_for_pass();
     uint32_t top = 0;
 #pragma unroll 4
-    for (int i = 0; i < parts; ++i) top = max(top, words[i * ldw + code_word + group]);
+    for (int i = 0; i < parts; ++i) top = max(top, __ldcg(words + i * ldw + code_word + group));
     const int power = value_power(top);
     if (p.row == 0 && (p.c & ((1 << k.shift) - 1)) == 0) factor[code_word + group] = pow2(-power);
 #pragma unroll
