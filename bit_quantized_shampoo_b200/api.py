@@ -356,6 +356,9 @@ def _act8():
             from . import _act8 as module
         except ImportError as e:
             raise RuntimeError("the act8 binding is not built: run `python -m bit_quantized_shampoo_b200.build`") from e
+        if module.built_for != torch.__version__:
+            raise RuntimeError(f"the act8 binding is for torch {module.built_for}, this is {torch.__version__}: run "
+                               "`python -m bit_quantized_shampoo_b200.build`")
         module.set_check(L.check)
         _act8_module = module
     return _act8_module

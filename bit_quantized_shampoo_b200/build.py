@@ -3,12 +3,14 @@
     python -m bit_quantized_shampoo_b200.build [--force] [-v]
 
 and beside it _act8.so, the Python binding of the 8-bit activation calls
-(g++, against this interpreter and its torch).
+(g++, against this interpreter and its torch; where their headers are missing
+the library is built alone, and the act8 calls say so).
 """
 from __future__ import annotations
 
 import concurrent.futures
 import os
+import shutil
 import subprocess
 import sys
 
@@ -56,7 +58,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
             print(" ".join(cmd), flush=True)
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
-            raise RuntimeError(f"nvcc failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+            raise RuntimeError(f"{os.path.basename(cmd[0])} failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
         return r
 
     with concurrent.futures.ThreadPoolExecutor(max_workers=max(1, min(8, os.cpu_count() or 1))) as ex:
@@ -64,10 +66,43 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if force or jobs or _stale(LIB, objs):
         run([NVCC, "-gencode", "arch=compute_100a,code=sm_100a", "-shared", "-o", LIB, *objs,
              "-lcudart_static", "-lrt", "-ldl", "-lpthread"])
-    src = os.path.join(CSRC, "act8_binding.cpp")
-    if force or _stale(BINDING, [src, os.path.join(INCLUDE, "shampoo4.h")]):
-        run(_binding_command(src))
+    _build_binding(run, force)
     return LIB
+
+
+def _build_binding(run, force):
+    """The binding, rebuilt when its sources change or its command does (which
+    names the interpreter and the torch that it is for)."""
+    missing = _binding_missing()
+    if missing:
+        if os.path.exists(BINDING):
+            os.remove(BINDING)                    # made for another interpreter or torch
+        print(f"_act8.so is not built: {missing}; the act8 calls of api.py will not work", file=sys.stderr)
+        return
+    src = os.path.join(CSRC, "act8_binding.cpp")
+    cmd = _binding_command(src)
+    stamp = os.path.join(BUILD, "act8_binding.command")
+    text = "\n".join(cmd)
+    same = os.path.exists(stamp) and open(stamp).read() == text
+    if force or not same or _stale(BINDING, [src, os.path.join(INCLUDE, "shampoo4.h")]):
+        run(cmd)
+        with open(stamp, "w") as f:
+            f.write(text)
+
+
+def _binding_missing():
+    """What the binding needs and this machine does not have, or None."""
+    import importlib.util
+    import sysconfig
+    cxx = os.environ.get("CXX", "g++")
+    if not shutil.which(cxx.split()[0]):
+        return f"no compiler {cxx}"
+    if not os.path.exists(os.path.join(sysconfig.get_paths()["include"], "Python.h")):
+        return "no Python.h"
+    spec = importlib.util.find_spec("torch")
+    if spec is None or not os.path.isdir(os.path.join(os.path.dirname(spec.origin), "include", "ATen")):
+        return "no torch headers"
+    return None
 
 
 def _binding_command(src):
@@ -77,10 +112,11 @@ def _binding_command(src):
     import torch
     base = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(NVCC))
-    flags = ["-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
+    flags = ["-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+             f'-DACT8_BUILT_FOR="{torch.__version__}"']
     inc = [INCLUDE, sysconfig.get_paths()["include"], os.path.join(base, "include"),
            os.path.join(base, "include", "torch", "csrc", "api", "include"), os.path.join(cuda, "include")]
-    return [os.environ.get("CXX", "g++"), *flags, *[f"-I{i}" for i in inc], src, "-o", BINDING,
+    return [*os.environ.get("CXX", "g++").split(), *flags, *[f"-I{i}" for i in inc], src, "-o", BINDING,
             f"-L{PKG}", "-l:libshampoo4.so", "-Wl,-rpath,$ORIGIN", f"-L{os.path.join(base, 'lib')}",
             "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
 

@@ -576,4 +576,11 @@ PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_act8", nullptr, -1, g_methods, 
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__act8() { return PyModule_Create(&g_module); }
+PyMODINIT_FUNC PyInit__act8() {
+  PyObject* m = PyModule_Create(&g_module);
+  if (m && PyModule_AddStringConstant(m, "built_for", ACT8_BUILT_FOR) < 0) {
+    Py_DECREF(m);
+    return nullptr;
+  }
+  return m;
+}
