@@ -62,6 +62,9 @@ shampoo4_status launch_act8_halves(const Act8Operand& a, int a_parts, const Act8
                                    int64_t R, int64_t K, int shares, const Act8Out& out, Act8Watch watch,
                                    cudaStream_t st);
 
+// The same with one plane each, and b R x K.
+shampoo4_status launch_act8_row_halves(const Act8Operand& a, const Act8Operand& b, int64_t M, int64_t R, int64_t K,
+                                       const Act8Out& out, Act8Watch watch, cudaStream_t st);
 
 // A gradient as act8_weight_grad and act8_input_grad take it (weight: which).
 struct Act8Grad {

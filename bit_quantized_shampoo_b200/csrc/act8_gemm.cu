@@ -979,7 +979,7 @@ using HalvesCfg = Cfg<           kHalf, true,  true,  128, 2, PB, 1, 2, STAGES, 
 // One half each.  The sum leaves the tensor core every 1024 k (64 additions,
 // each cut off at 2^-22 of the sum at most: 2^-16, far below the bfloat16
 // result); draining 256 rows takes a sixth of the time of those products.
-using HalfCfg = Cfg<             kHalf, true,  true,  256, 1, 1,  1, 2, 6, 16>;
+template <bool B_MN> using HalfCfg = Cfg<kHalf, true, B_MN, 256, 1, 1, 1, 2, 6, 16>;
 
 shampoo4_status launch_act8_codes(const Act8Operand& a, const Act8Operand& b, int64_t M, int64_t R, int64_t K,
                                   const Act8Out& out, bool after_pass, Act8Watch watch, cudaStream_t st) {
@@ -1024,9 +1024,14 @@ int act8_halves_shares(int64_t M, int64_t R, int64_t K) {
 shampoo4_status launch_act8_halves(const Act8Operand& a, int a_parts, const Act8Operand& b, int b_parts, int64_t M,
                                    int64_t R, int64_t K, int shares, const Act8Out& out, Act8Watch watch,
                                    cudaStream_t st) {
-  if (a_parts == 1) return launch<HalfCfg>(a, b, M, R, K, out, true, watch, st, shares);
+  if (a_parts == 1) return launch<HalfCfg<true>>(a, b, M, R, K, out, true, watch, st, shares);
   return b_parts == 1 ? launch<HalvesCfg<1, 5>>(a, b, M, R, K, out, true, watch, st, shares)
                       : launch<HalvesCfg<2, 4>>(a, b, M, R, K, out, true, watch, st, shares);
+}
+
+shampoo4_status launch_act8_row_halves(const Act8Operand& a, const Act8Operand& b, int64_t M, int64_t R, int64_t K,
+                                       const Act8Out& out, Act8Watch watch, cudaStream_t st) {
+  return launch<HalfCfg<false>>(a, b, M, R, K, out, true, watch, st);
 }
 
 }  // namespace s4

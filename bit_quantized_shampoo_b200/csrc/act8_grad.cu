@@ -4,7 +4,7 @@
 //   act8_input_grad    dX[t, i] = sum_o dY[t, o] sw[o] wc[o, i]
 //
 // The scale belongs to the contraction index, so it has to go into a factor.
-// Two ways, chosen by the scales alone (grad_path):
+// Three ways, chosen by the scales, types and sizes (grad_path):
 //
 //  digits  One scale per row of codes.  F = dY * scale in fp32 becomes fixed
 //          point relative to its largest magnitude over the contraction,
@@ -22,7 +22,12 @@
 //          value for a bfloat16 result of a bfloat16 dY (2^-11, an eighth of
 //          the result's own rounding; as one bfloat16 it would add as much
 //          again).  Three products (two, one), summed in fp32 outside the
-//          tensor core every 256 k (one: every 1024).  (Three bfloat16 parts each, six products, measured
+//          tensor core every 256 k (one: every 1024).  Also with one scale
+//          per row, for a large bfloat16 weight gradient.
+//  row     The large bfloat16 input gradient of a bfloat16 dY: F = dY * scale,
+//  halves  each row scaled by a power of two (its largest to about 2^14), as
+//          one half (2^-11, never coarser than 2^-39 of the row's largest),
+//          the codes as halves as they are: one product.  (Three bfloat16 parts each, six products, measured
 //          47 us where this takes 32 at 1537 x 768 x 2305 fp32.)
 //
 // The operand passes of this file stream; their bound is HBM bandwidth.
@@ -303,6 +308,56 @@ __device__ __forceinline__ int value_power(uint32_t scale_bits) {
   return power_to(scale_bits == 0u ? 0u : min(scale_bits + (7u << 23), 0x7f000000u));
 }
 
+// Rows of F = dY * scale as one half each, for act8_input_grad: a CTA per row,
+// read twice (the second time from cache).  factor: what undoes a row's power.
+template <bool A>
+__global__ void __launch_bounds__(kThreads)
+k_act8_row_halves(Mat dy, const float* __restrict__ scale, __half* o, int64_t ld, float* factor, int cols) {
+  let_next_start();
+  __shared__ uint32_t slots[kThreads / 32];
+  const int64_t row = blockIdx.x;
+  const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(dy.p) + row * dy.ld;
+  const bool vec = (reinterpret_cast<uintptr_t>(scale) & 15) == 0;
+  Raw8<__nv_bfloat16> r;
+  float s[8];
+  uint32_t m = 0;
+#pragma unroll 2
+  for (int c = int(threadIdx.x) * 8; c < cols; c += kThreads * 8) {   // past the last column: 0 * 0
+    load8<A>(x, c, cols, dy.vec, r);
+    scales8(scale, c, cols, vec, s);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = max(m, finite_bits(elt(r, i) * s[i]));
+  }
+  const int e = power_to(cta_max(m, slots));
+  if (threadIdx.x == 0) factor[row] = pow2(-e);
+  const float power = pow2(e);
+#pragma unroll 2
+  for (int c = int(threadIdx.x) * 8; c < cols; c += kThreads * 8) {
+    load8<A>(x, c, cols, dy.vec, r);
+    scales8(scale, c, cols, vec, s);
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = elt(r, i) * s[i] * power;
+    store8(o + row * ld, c, cols, 1, v);
+  }
+}
+// Codes as halves, exactly.
+__global__ void __launch_bounds__(kThreads) k_act8_code_halves(Ckpt k, __half* o, int64_t ld, int64_t rows, int cols) {
+  let_next_start();
+  const Piece<4> p;
+  if (p.row >= rows || p.c >= cols) return;
+  uint2 w[4];
+#pragma unroll
+  for (int u = 0; u < 4; ++u) load_codes8(k.codes + p.at(u) * k.ldc, p.c, p.at(u) < rows ? cols : 0, w[u]);
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    float v[8];
+    values8(w[u], 1.0f, v);
+    if (p.at(u) < rows) store8(o + p.at(u) * ld, p.c, cols, 1, v);
+  }
+  wait_for_pass();                       // nothing of it is read here, but the product relies on both
+}
+
 template <int PARTS>
 __device__ __forceinline__ void store_halves(const float (&v)[8], const int (&e)[8], __half* o, int64_t plane, int c,
                                              int cols) {
@@ -347,7 +402,7 @@ k_act8_halves(Ckpt k, __half* co, int64_t ldco, int cols_c, Mat dy, __half* dyo,
 #pragma unroll 4
     for (int i = 0; i < parts; ++i) top = max(top, __ldcg(words + i * ldw + code_word + group));
     const int power = value_power(top);
-    if (p.row == 0 && (p.c & ((1 << k.shift) - 1)) == 0) factor[code_word + group] = pow2(-power);
+    if (p.row == 0 && p.c == group << k.shift) factor[code_word + group] = pow2(-power);
 #pragma unroll
     for (int i = 0; i < 8; ++i) e[i] = power;
 #pragma unroll
@@ -403,8 +458,19 @@ __global__ void __launch_bounds__(kThreads) k_act8_join(const float* __restrict_
 
 // ------------------------------------------------------------------ host
 
-enum GradPath { kDigits, kHalves };
-GradPath grad_path(int32_t group) { return group == 0 ? kDigits : kHalves; }
+// One scale per row, dY and the result bfloat16: one product of halves, where
+// digits take half as long again per row of the result but need no copy of the
+// codes; and only on 256 x 256 tiles.  So it wants rows (input gradient, 11008
+// inner, 4096 of contraction: 1500 rows 130 us, digits 128; 2048 rows 155, 169)
+// and tiles (three per pair of CTAs; 2048 x 3200, 11008 of contraction, 104
+// tiles: 163, 157).  The result is the exact one rounded, either way.
+enum GradPath { kDigits, kHalves, kRowHalves };
+GradPath grad_path(bool weight, int32_t dtype, int32_t result, int32_t group, int64_t rows, int64_t inner) {
+  if (group) return kHalves;
+  const bool many = rows >= 2048 && ((rows + 255) / 256) * ((inner + 255) / 256) >= 222;
+  if (dtype != ACT8_BF16 || result != ACT8_BF16 || !many) return kDigits;
+  return weight ? kHalves : kRowHalves;
+}
 
 size_t round_up(size_t n, size_t a) { return (n + a - 1) / a * a; }
 
@@ -427,7 +493,7 @@ struct GradPlan {
 GradPlan grad_plan(bool weight, int32_t dtype, int32_t result, int32_t group, int64_t tokens, int64_t out,
                    int64_t inner) {
   GradPlan p{};
-  p.path = grad_path(group);
+  p.path = grad_path(weight, dtype, result, group, weight ? out : tokens, inner);
   if (p.path == kDigits) {
     const int64_t rows = weight ? out : tokens, k = weight ? tokens : out;
     p.ld_dy = int64_t(round_up(size_t(k), 16));
@@ -437,6 +503,14 @@ GradPlan grad_plan(bool weight, int32_t dtype, int32_t result, int32_t group, in
   }
   p.dy_parts = dtype == ACT8_FP32 ? 2 : 1;
   p.code_parts = dtype == ACT8_BF16 && result == ACT8_BF16 ? 1 : 2;
+  if (p.path == kRowHalves) {
+    p.scale_bytes = round_up(size_t(tokens) * 4, 256);
+    p.ld_dy = int64_t(round_up(size_t(out), 8));
+    p.ld_code = int64_t(round_up(size_t(inner), 8));
+    p.dy_bytes = round_up(size_t(tokens) * p.ld_dy * 2, 256);
+    p.code_bytes = round_up(size_t(out) * p.ld_code * 2, 256);
+    return p;
+  }
   p.code_word = int64_t(round_up(size_t(out), 8));
   p.ldw = p.code_word + int64_t(round_up(size_t(group_count(inner, group)), 8));
   // Enough clusters for every SM's 2048 threads, as far as there are tiles.
@@ -509,6 +583,19 @@ shampoo4_status digit_pass(bool weight, const void* dy, int32_t dtype, int64_t l
   }); });
 }
 
+// dY * scale in rows of halves at dyp, the codes as halves at cp.
+shampoo4_status row_halves_pass(const void* dy, int64_t lddy, const Ckpt& k, int64_t tokens, int64_t out,
+                                int64_t inner, const GradPlan& p, float* factor, void* dyp, void* cp,
+                                cudaStream_t st) {
+  const Mat m = mat(dy, lddy, ACT8_BF16);
+  const dim3 b = piece_block(inner);
+  dim3 g;
+  if (!piece_grid(out, inner, b, 4, &g)) return SHAMPOO4_ERR_INVALID_ARG;
+  S4_TRY(start(m.vec ? k_act8_row_halves<true> : k_act8_row_halves<false>, dim3(unsigned(tokens)), dim3(kThreads),
+               dim3(1), false, st, m, k.scales, static_cast<__half*>(dyp), p.ld_dy, factor, int(out)));
+  return start(k_act8_code_halves, g, b, dim3(1), true, st, k, static_cast<__half*>(cp), p.ld_code, out, int(inner));
+}
+
 // Both operands as halves at dyp and cp, and the result's factors.
 shampoo4_status halves_pass(const void* dy, int32_t dtype, int64_t lddy, const Ckpt& k, int64_t tokens, int64_t out,
                             int64_t inner, const GradPlan& p, float* factor, void* dyp, void* cp, cudaStream_t st) {
@@ -572,8 +659,13 @@ shampoo4_status act8_grad_run(const Act8Grad& g, void* ws, Act8Watch watch, cuda
                               st);
   }
   char *dyp = w + p.scale_bytes, *cp = dyp + p.dy_bytes;
-  // groups: only the weight gradient has them
   float* factor = reinterpret_cast<float*>(w);
+  if (p.path == kRowHalves) {
+    S4_TRY(row_halves_pass(g.dy, g.lddy, k, tokens, out, inner, p, factor, dyp, cp, st));
+    o.row_scale = factor;
+    return launch_act8_row_halves(Act8Operand{cp, p.ld_code, 0}, Act8Operand{dyp, p.ld_dy, 0}, inner, R, K, o, watch,
+                                  st);
+  }
   S4_TRY(halves_pass(g.dy, g.dtype, g.lddy, k, tokens, out, inner, p, factor, dyp, cp, st));
   o.row_scale = factor;
   o.col_scale = factor + p.code_word;

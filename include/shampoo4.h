@@ -575,12 +575,18 @@ shampoo4_status act8_linear(const void* d_x, int32_t xdtype, int64_t ldx, const 
  *   one scale per row   dY * scale in fp32, then fixed point: 24 bits below
  *                       its largest magnitude over the contraction (a largest
  *                       below 2^-100 counts as 2^-100); exact integer
- *                       products and sums with the codes.
+ *                       products and sums with the codes.  The step is the
+ *                       result row's: a token far louder than the others sets
+ *                       it for all columns, those where its codes are 0 too.
  *   scales per group    dY and xf to 22 bits, and no finer than 2^-39 of the
  *                       largest over the contraction (dY: of the column; xf:
- *                       of the group of columns); fp32 sums.  dY and
- *                       the result bfloat16: xf to 11 bits (2^-11, an eighth
- *                       of the result's rounding).
+ *                       of the group of columns); fp32 sums.
+ *   dY and the result bfloat16, with scales per group, or 2048 rows and 222
+ *                       tiles of 256 x 256 in the result and more: one factor
+ *                       (xf, or dY * scale in act8_input_grad) to 11 bits, an
+ *                       eighth of the result's own rounding, the other as it
+ *                       is, both no finer than 2^-39 of their largest over
+ *                       the contraction; fp32 sums.
  * A non-finite element of dY, or a non-finite scale, makes every result it
  * enters non-finite.
  * d_workspace: act8_grad_workspace bytes, 256-byte aligned (weight != 0 for

@@ -31,7 +31,8 @@ def values64(k, group=0):
 # ---------------------------------------------------- results in bfloat16
 
 @pytest.mark.parametrize("weight,tokens,out,inner,group", [
-    (False, 1100, 1900, 3100, 0), (True, 1900, 1100, 3100, 0), (True, 700, 200, 320, 64), (True, 1300, 900, 3200, 128),
+    (False, 1100, 1900, 3100, 0), (True, 1900, 1100, 3100, 0), (False, 2100, 1300, 6300, 0), (True, 1300, 2100, 6300, 0),
+    (True, 700, 200, 320, 64), (True, 1300, 900, 3200, 128),
     (False, 300, 500, 400, 0)])
 def test_bfloat16_gradients_are_the_rounded_result(weight, tokens, out, inner, group):
     """The error is that of rounding the exact result to bfloat16, whatever
@@ -156,3 +157,49 @@ def test_grouped_gradient_over_the_whole_range(up, down):
     within(got, want, grouped_tolerance(f64(dy), codes, scales, 32, "fp32", "fp32")
            + half_step("fp32") * np.abs(want) + 2 * TINY["fp32"])
     assert np.abs(got).max() > 0
+
+
+@pytest.mark.parametrize("pad,offset", [(0, 0), (8, 0), (3, 1)])
+@pytest.mark.parametrize("weight", [False, True])
+def test_large_bfloat16_gradients_at_any_magnitude(weight, pad, offset):
+    """Tokens (output channels) from 10^-18 to 10^18 side by side, one of them
+    zero, weights (inputs) of 10^-12 and 10^12, unaligned rows, into a part of
+    a larger result that is added to: each result's row is as precise as
+    alone.  One operand as one half (2^-11) and 65 truncated additions of
+    2^-22 (K below 2048: twice, and one rounding); an element is never coarser
+    than 2^-39 of its row's largest over the contraction."""
+    api = _api()
+    tokens, out, inner = (1300, 2100, 6300) if weight else (2100, 1300, 6300)
+    rng = np.random.default_rng(11)
+    size = 10.0 ** rng.integers(-18, 19, out if weight else tokens)
+    size[7] = 0
+    dy = rng.standard_normal((tokens, out)) * (size if weight else size.reshape(-1, 1))
+    room = torch.zeros(tokens * (out + pad) + offset, dtype=torch.bfloat16, device="cuda")
+    d = room[offset:].view(tokens, out + pad)[:, :out]
+    d.copy_(torch.from_numpy(dy))
+    for scale in (1e-12, 1e12):
+        k = stored(tokens if weight else out, inner, 12, 0, scale)[0]
+        v = values64(k)
+        F = d.double() if weight else d.double() * k[1].double().t()      # what is scaled per row of the result
+        cols = v if weight else k[0].double()
+        want = F.t() @ cols if weight else F @ cols
+        S = F.abs().t() @ cols.abs() if weight else F.abs() @ cols.abs()
+        K = cols.shape[0]
+        top = F.abs().amax(dim=0 if weight else 1).reshape(-1, 1)
+        floor = 2.0 ** -39 * top * cols.abs().sum(dim=0)
+        if weight:                                 # the values share one power of two
+            floor += 2.0 ** -39 * F.abs().sum(dim=0).reshape(-1, 1) * cols.abs().max() * 1.01
+        both = torch.full((want.shape[0], inner + 6), 5.0, dtype=torch.bfloat16, device="cuda")
+        part = both[:, 2:-4]
+        f = api.act8_weight_grad if weight else api.act8_input_grad
+        kw = dict(dtype=torch.bfloat16) if weight else {}
+        got = f(d, *k, **kw).double()
+        tol = S * (2.0 ** -11 + 2 * 65 * 2.0 ** -22 + 4 * 2.0 ** -24) + floor
+        half = half_step("bf16")
+        assert ((got - want).abs() <= tol + half * want.abs() + TINY["bf16"]).all()
+        assert (got[7] == 0).all()
+        part.fill_(2.0)
+        f(d, *k, out=part, accumulate=True)
+        assert ((part.double() - (want + 2)).abs()
+                <= tol + (half + 2.0 ** -23) * (want + 2).abs() + 2.0 ** -23 * 2 + TINY["bf16"]).all()
+        assert (both[:, :2] == 5).all() and (both[:, -4:] == 5).all()
