@@ -38,6 +38,10 @@ ROOT_NEWTON_Q4 = 2
 ACT8_FP32 = 0
 ACT8_BF16 = 1
 ACT8_FP16 = 2
+ACT8_WAY_CODES = 0
+ACT8_WAY_DIGITS = 1
+ACT8_WAY_HALVES = 2
+ACT8_WAY_ROW_HALVES = 3
 
 
 class Config(C.Structure):
@@ -60,6 +64,10 @@ class Param(C.Structure):
 class Layer(C.Structure):
     _fields_ = [("dy", C.c_void_p), ("dtype", C.c_int32), ("lddy", C.c_int64), ("codes", C.c_void_p),
                 ("ldc", C.c_int64), ("scales", C.c_void_p), ("tokens", C.c_int64)]
+
+
+class Form(C.Structure):
+    _fields_ = [("way", C.c_int32), ("tile_rows", C.c_int32), ("shares", C.c_int32), ("code_parts", C.c_int32)]
 
 
 class Shampoo4Error(RuntimeError):
@@ -117,6 +125,7 @@ _SIGS = {
     "act8_grad_workspace": [_I, _I, _I, _N, _N, _N, _I, c_size_p],
     "act8_weight_grad": [_P, _I, _N, _P, _N, _P, _I, _N, _N, _N, _P, _I, _N, _I, _P, C.c_size_t, _P, _P],
     "act8_input_grad": [_P, _I, _N, _P, _N, _P, _N, _N, _N, _P, _I, _N, _I, _P, C.c_size_t, _P, _P],
+    "act8_product_form": [_I, _I, _I, _N, _N, _N, _I, C.POINTER(Form)],
     "shampoo4_weight_grads_workspace": [_P, C.POINTER(Layer), _I, c_size_p],
     "shampoo4_weight_grads": [_P, C.POINTER(Layer), _I, C.POINTER(_P), c_i64_p, _I, _P, C.c_size_t, _P],
     "act8_swiglu": [_P, _N, _P, _N, _I, _N, _N, _I, _P, _N, _P, _N, _P, _P, _N, _P, _P],

@@ -39,6 +39,12 @@ struct Act8Watch {
   uint64_t wait_ns = 0;
 };
 
+// How an integer product is cut: tiles of `rows` rows by one CTA each (0: by
+// pairs of CTAs), the contraction in `shares`.
+struct Form { int rows, shares; };
+Form act8_codes_form(int64_t M, int64_t R, int64_t K);
+Form act8_digits_form(int64_t M, int64_t R, int64_t K);
+
 // All products: Y[r, m] = row_scale[r] col_scale[m] sum_k B[r, k] A[m, k] + bias[m].
 
 // int8 codes both: a is M x K, b is R x K (K contiguous).  after_pass: b was

@@ -950,7 +950,6 @@ shampoo4_status launch_small(const Act8Operand& a, const Act8Operand& b, int64_t
 // rows x digits columns: 4.9 + 0.004 n, and 0.15 + 0.0006 n per k-block, half
 // as much again or more when two CTAs share an SM; joining a split contraction
 // 1 and 0.07 per row and digit a CTA finishes; each further wave starts anew.
-struct Form { int rows, shares; };                          // rows 0: the pairs
 Form choose_form(int64_t M, int64_t R, int64_t K, int pair_rows, int digits, const int* tile_rows, int forms) {
   const double kb = double((K + 127) / 128);
   const double pair_tiles = double((M + 255) / 256) * double((R + pair_rows - 1) / pair_rows);
@@ -981,10 +980,19 @@ using HalvesCfg = Cfg<           kHalf, true,  true,  128, 2, PB, 1, 2, STAGES, 
 // result); draining 256 rows takes a sixth of the time of those products.
 template <bool B_MN> using HalfCfg = Cfg<kHalf, true, B_MN, 256, 1, 1, 1, 2, 6, 16>;
 
+Form act8_codes_form(int64_t M, int64_t R, int64_t K) {
+  const int rows[] = {16, 64, 128};
+  return choose_form(M, R, K, CodesCfg::R, 1, rows, 3);
+}
+Form act8_digits_form(int64_t M, int64_t R, int64_t K) {
+  const int rows[] = {16, 32};
+  // the small form keeps its integer sums whole
+  return K <= kAct8MaxInner ? choose_form(M, R, K, DigitsCfg::R, kAct8Digits, rows, 2) : Form{0, 1};
+}
+
 shampoo4_status launch_act8_codes(const Act8Operand& a, const Act8Operand& b, int64_t M, int64_t R, int64_t K,
                                   const Act8Out& out, bool after_pass, Act8Watch watch, cudaStream_t st) {
-  const int rows[] = {16, 64, 128};
-  const Form f = choose_form(M, R, K, CodesCfg::R, 1, rows, 3);
+  const Form f = act8_codes_form(M, R, K);
   if (f.rows == 16) return launch_small<SmallCfg<false, 16, 1, 5>>(a, b, M, R, K, f.shares, out, after_pass, watch, st);
   if (f.rows == 64) return launch_small<SmallCfg<false, 64, 1, 4>>(a, b, M, R, K, f.shares, out, after_pass, watch, st);
   if (f.rows == 128)
@@ -994,9 +1002,7 @@ shampoo4_status launch_act8_codes(const Act8Operand& a, const Act8Operand& b, in
 
 shampoo4_status launch_act8_digits(const Act8Operand& a, const Act8Operand& b, int64_t M, int64_t R, int64_t K,
                                    const Act8Out& out, Act8Watch watch, cudaStream_t st) {
-  const int rows[] = {16, 32};
-  // the small form keeps its integer sums whole
-  const Form f = K <= kAct8MaxInner ? choose_form(M, R, K, DigitsCfg::R, kAct8Digits, rows, 2) : Form{0, 1};
+  const Form f = act8_digits_form(M, R, K);
   if (f.rows == 16)
     return launch_small<SmallCfg<true, 16, kAct8Digits, 4>>(a, b, M, R, K, f.shares, out, true, watch, st);
   if (f.rows == 32)

@@ -698,6 +698,29 @@ extern "C" shampoo4_status act8_grad_workspace(int32_t weight, int32_t dtype, in
   return SHAMPOO4_OK;
 }
 
+extern "C" shampoo4_status act8_product_form(int32_t call, int32_t dtype, int32_t result, int64_t tokens,
+                                             int64_t out, int64_t inner, int32_t group, act8_form* form) {
+  if (!form || call < 0 || call > 2 || !dtype_ok(dtype) || !dtype_ok(result) || !group_ok(group) ||
+      (call == 2 && group) || !shape_ok(tokens, out) || !shape_ok(0, inner))
+    return SHAMPOO4_ERR_INVALID_ARG;
+  if (call == 0) {
+    const Form f = act8_codes_form(out, tokens, inner);
+    *form = act8_form{ACT8_WAY_CODES, f.rows, f.shares, 0};
+    return SHAMPOO4_OK;
+  }
+  const bool weight = call == 1;
+  const GradPlan p = grad_plan(weight, dtype, result, group, tokens, out, inner);
+  if (p.path == kDigits) {
+    const Form f = weight ? act8_digits_form(inner, out, tokens) : act8_digits_form(inner, tokens, out);
+    *form = act8_form{ACT8_WAY_DIGITS, f.rows, f.shares, 0};
+  } else if (p.path == kRowHalves) {
+    *form = act8_form{ACT8_WAY_ROW_HALVES, 0, 1, 1};
+  } else {
+    *form = act8_form{ACT8_WAY_HALVES, 0, p.shares, p.code_parts};
+  }
+  return SHAMPOO4_OK;
+}
+
 static shampoo4_status grad_call(const Act8Grad& g, void* ws, size_t ws_bytes, uint32_t* flags,
                                  shampoo4_stream_t stream) {
   size_t bytes = 0;

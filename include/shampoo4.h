@@ -603,6 +603,25 @@ shampoo4_status act8_input_grad(const void* d_dy, int32_t dtype, int64_t lddy, c
                                 int32_t result, int64_t lddx, int32_t accumulate, void* d_workspace,
                                 size_t workspace_bytes, uint32_t* d_flags, shampoo4_stream_t stream);
 
+/* Diagnostic: how a product would be computed, for tests that have to reach
+ * every way.  call: 0 act8_matmul and act8_linear (dtype, result and group do
+ * not matter), 1 act8_weight_grad, 2 act8_input_grad (group 0).  Touches no
+ * device. */
+typedef enum {
+  ACT8_WAY_CODES = 0,        /* the codes as they are                        */
+  ACT8_WAY_DIGITS = 1,       /* dY in fixed point                            */
+  ACT8_WAY_HALVES = 2,       /* dY and values as halves                      */
+  ACT8_WAY_ROW_HALVES = 3    /* dY * scale as one half, codes as halves      */
+} act8_way;
+typedef struct {
+  int32_t way;
+  int32_t tile_rows;         /* of a one-CTA tile; 0: tiles of a pair of CTAs */
+  int32_t shares;            /* parts of the contraction                     */
+  int32_t code_parts;        /* halves of a value (way HALVES)               */
+} act8_form;
+shampoo4_status act8_product_form(int32_t call, int32_t dtype, int32_t result, int64_t tokens, int64_t out,
+                                  int64_t inner, int32_t group, act8_form* form);
+
 /* The gradients of a handle's parameters, as shampoo4_update_stats takes them:
  * parameter p of shape out x inner gets act8_weight_grad of layers[p], in
  * fp32, at d_grads[p] (leading dimension ld[p] >= inner), overwritten or, with
