@@ -203,3 +203,56 @@ def test_large_bfloat16_gradients_at_any_magnitude(weight, pad, offset):
         assert ((part.double() - (want + 2)).abs()
                 <= tol + (half + 2.0 ** -23) * (want + 2).abs() + 2.0 ** -23 * 2 + TINY["bf16"]).all()
         assert (both[:, :2] == 5).all() and (both[:, -4:] == 5).all()
+
+
+# --------------------------------------------- non-finite and huge elements
+
+# weight, tokens, out, inner, group, dtype, result: digits in one-CTA tiles and in pairs, two halves, one half,
+# one half per row
+WAYS = [(True, 70, 40, 96, 0, "fp32", "fp32"), (True, 1501, 1003, 2601, 0, "bf16", "fp32"),
+        (True, 300, 130, 200, 32, "fp32", "fp32"), (True, 300, 130, 200, 64, "fp16", "bf16"),
+        (True, 300, 130, 200, 64, "bf16", "bf16"), (True, 600, 2100, 6300, 0, "bf16", "bf16"),
+        (False, 40, 70, 96, 0, "fp16", "fp16"), (False, 1003, 1501, 2601, 0, "fp32", "fp32"),
+        (False, 2100, 600, 6300, 0, "bf16", "bf16")]
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("weight,tokens,out,inner,group,dtype,result", WAYS)
+def test_non_finite_elements_show_where_they_enter(weight, tokens, out, inner, group, dtype, result, value):
+    """An element of dy reaches its output channel's (token's) results, a
+    scale those of its group of columns (all, with one scale per row), both
+    all of them, zeros in the other factor or not; the others stay finite."""
+    api = _api()
+    f = api.act8_weight_grad if weight else api.act8_input_grad
+    kw = dict(group=group) if weight else {}
+    dy = data(tokens, out, dtype, 21, scale=0.01)
+    codes, scales = stored(tokens if weight else out, inner, 22, group)[0]
+    bad = dy.clone()
+    bad[tokens // 2, out // 2] = value                     # a row of zeros otherwise
+    got = torch.isfinite(f(bad, codes, scales, dtype=DT[result], **kw))
+    row = out // 2 if weight else tokens // 2
+    assert not got[row].any() and got[:row].all() and got[row + 1:].all()
+    worse = scales.clone()
+    g = scales.shape[1] // 2
+    worse[scales.shape[0] // 3, g] = value                 # a row of zero codes
+    got = torch.isfinite(f(dy, codes, worse, dtype=DT[result], **kw))
+    c0, c1 = (g * group, min((g + 1) * group, inner)) if group else (0, inner)
+    assert not got[:, c0:c1].any() and got[:, :c0].all() and got[:, c1:].all()
+
+
+@pytest.mark.parametrize("group", [0, 32])
+@pytest.mark.parametrize("dtype,result", [("fp32", "fp32"), ("bf16", "bf16")])
+def test_gradient_next_to_the_largest_number(group, dtype, result):
+    """One term of 3.38e38.  Digits: a step of 1 / 8355704 and 7 roundings of
+    2^-24; halves: 2^-22 of each factor and of the lower parts; one half
+    2^-11; then the result's rounding."""
+    api = _api()
+    dy = torch.zeros(40, 6, dtype=DT[dtype], device="cuda")
+    dy[0] = 3.38e38
+    codes = np.zeros((40, 96), np.int8)
+    codes[0] = 127
+    scales = np.full((40, 3 if group else 1), 1 / 127, np.float32)
+    got = f64(api.act8_weight_grad(dy, *to_gpu(codes, scales), group=group, dtype=DT[result]))
+    want = f64(dy).T @ A.values64(codes, scales, group)
+    rel = 2.0 ** -11 if group and result == "bf16" else 3 * 2.0 ** -22 + 8 * 2.0 ** -24
+    within(got, want, want * (rel + half_step(result)))
