@@ -344,8 +344,10 @@ def quant4_tables(codebook="linear_square"):
 # Arguments that do not fit raise TypeError, ValueError or Shampoo4Error before
 # anything is enqueued.  The products' ``flags`` is an int32 word of the caller's,
 # in which a wait that expired raises FLAG_TIMEOUT (its result is then not
-# valid); without one it goes unreported.  The checks and calls are in csrc/act8_binding.cpp: the smallest
-# of these calls take a few microseconds, less than the same checks in Python.
+# valid); without one it goes unreported.  Nothing here is recorded for autograd:
+# results carry no history, and the gradients are calls of their own.  The checks
+# and calls are in csrc/act8_binding.cpp: the smallest of these calls take a few
+# microseconds, less than the same checks in Python.
 
 def _act8():
     """The binding module; like the library, it has to be built."""

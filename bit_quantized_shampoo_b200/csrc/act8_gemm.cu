@@ -22,8 +22,9 @@
 // one's products.  The pairs are persistent, one CTA per SM.  Bound by the
 // tensor cores, and in a loop by the power cap: 8192 x 11008 x 4096 codes 215
 // us alone (3.4 POPS), 227 to 239 in a loop; its weight gradient in digits 648
-// us alone (3.4 POPS of three products); the tensor
-// pipe is 88 to 92% busy where tiles fill the waves.
+// us alone (3.4 POPS of three products); 8192 x 4096 x 11008 as one half each
+// 478 to 504 us (1.5 PFLOP/s); the tensor pipe is 88 to 92% busy where tiles
+// fill the waves.
 //
 // Warp roles (320 threads): warp 0 issues the TMA loads, warp 1 of the leader
 // the MMAs, warps 2..9 drain the accumulator, two per lane quarter with half of
@@ -255,7 +256,6 @@ __device__ __forceinline__ uint32_t pack_pair(__half*, float lo, float hi) {
   const __half2 x = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&x);
 }
-__device__ __forceinline__ uint32_t pack_pair(float*, float, float) { return 0u; }   // not used
 
 // 32 rows r0.. of column m to Y: a store instruction writes 32 consecutive
 // columns of a row, or, of 16-bit results whose rows are 4-byte aligned, a
@@ -282,19 +282,23 @@ __device__ __forceinline__ void store_chunk(const Act8Out& o, int R, int M, int 
 #pragma unroll
   for (int j = 0; j < 32; ++j) v[j] = fmaf(v[j], cs, bias);
   const bool whole = !o.accumulate && r0 + 32 <= R && __all_sync(0xffffffffu, m < M);
-  if (sizeof(T) == 2 && whole && ((reinterpret_cast<uintptr_t>(o.y) | uintptr_t(o.ld * 2)) & 3) == 0) {
-    const bool odd = m & 1;
-    uint32_t* p = reinterpret_cast<uint32_t*>(y - (odd ? 1 : 0) + (odd ? 2 : 0) * o.ld);   // even lanes rows 4k, odd 4k + 2
-    const int64_t step = o.ld / 2;                          // words
+  if constexpr (sizeof(T) == 2) {
+    if (whole && ((reinterpret_cast<uintptr_t>(o.y) | uintptr_t(o.ld * 2)) & 3) == 0) {
+      const bool odd = m & 1;
+      uint32_t* p = reinterpret_cast<uint32_t*>(y - (odd ? 1 : 0) + (odd ? 2 : 0) * o.ld);   // even lanes rows 4k, odd 4k + 2
+      const int64_t step = o.ld / 2;                          // words
 #pragma unroll
-    for (int j = 0; j < 32; j += 4) {
-      const uint32_t a = pack_pair(y, v[j], v[j + 1]), b = pack_pair(y, v[j + 2], v[j + 3]);
-      const uint32_t mine = odd ? b : a, other = __shfl_xor_sync(0xffffffffu, odd ? a : b, 1);
-      const uint32_t left = odd ? other : mine, right = odd ? mine : other;   // columns m & ~1 and m | 1
-      p[j * step] = __byte_perm(left, right, 0x5410);
-      p[(j + 1) * step] = __byte_perm(left, right, 0x7632);
+      for (int j = 0; j < 32; j += 4) {
+        const uint32_t a = pack_pair(y, v[j], v[j + 1]), b = pack_pair(y, v[j + 2], v[j + 3]);
+        const uint32_t mine = odd ? b : a, other = __shfl_xor_sync(0xffffffffu, odd ? a : b, 1);
+        const uint32_t left = odd ? other : mine, right = odd ? mine : other;   // columns m & ~1 and m | 1
+        p[j * step] = __byte_perm(left, right, 0x5410);
+        p[(j + 1) * step] = __byte_perm(left, right, 0x7632);
+      }
+      return;
     }
-  } else if (whole) {
+  }
+  if (whole) {
 #pragma unroll
     for (int j = 0; j < 32; ++j) put(y + int64_t(j) * o.ld, v[j]);
   } else if (m < M) {
@@ -945,7 +949,7 @@ shampoo4_status launch_small(const Act8Operand& a, const Act8Operand& b, int64_t
 
 // Which form an integer product takes: the estimated time (us) of each,
 // fitted to measurements on a B200 (1 to 2048 rows, 768 to 11008 columns, 6 to
-// 86 k-blocks; within 15% of most).  The pairs: 8.3 and, per wave of tiles,
+// 86 k-blocks; its 148 SMs are in the rule: 74 pairs, two small CTAs per SM).  The pairs: 8.3 and, per wave of tiles,
 // 0.31 (digits 0.25) per k-block or the results' stores.  A small tile of n =
 // rows x digits columns: 4.9 + 0.004 n, and 0.15 + 0.0006 n per k-block, half
 // as much again or more when two CTAs share an SM; joining a split contraction

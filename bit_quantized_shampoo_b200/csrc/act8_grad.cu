@@ -68,9 +68,7 @@ __device__ __forceinline__ uint32_t bytes4(uint32_t x0, uint32_t x1, uint32_t x2
   return __byte_perm(__byte_perm(x0, x1, sel), __byte_perm(x2, x3, sel), 0x5410);
 }
 
-// Rows of dY as they are (act8_input_grad): a CTA per row, or a warp per row
-// of up to 1024 columns, read twice (the second time from cache).  8192 x 4096
-// fp16: 37 us, 4.5 TB/s of dY read once and the digits written.
+// Scales c .. c + 7 of n, zeros past the end.
 __device__ __forceinline__ void scales8(const float* s, int c, int n, bool vec, float (&v)[8]) {
   if (vec && c + 8 <= n) {
     const float4 a = __ldg(reinterpret_cast<const float4*>(s + c)), b = __ldg(reinterpret_cast<const float4*>(s + c + 4));
@@ -81,6 +79,9 @@ __device__ __forceinline__ void scales8(const float* s, int c, int n, bool vec, 
     for (int i = 0; i < 8; ++i) v[i] = c + i < n ? __ldg(s + c + i) : 0.0f;
   }
 }
+// Rows of dY as they are (act8_input_grad): a CTA per row, or a warp per row
+// of up to 1024 columns, read twice (the second time from cache).  8192 x 4096
+// fp16: 37 us, 4.5 TB/s of dY read once and the digits written.
 template <class T, bool WARP, bool A>
 __global__ void __launch_bounds__(kThreads)
 k_act8_digit_rows(Mat dy, const float* __restrict__ scale, int8_t* digits, int64_t ld, float* row_scale, int64_t rows,
@@ -245,6 +246,8 @@ k_act8_digit_columns(Mat dy, const float* __restrict__ scale, int8_t* digits, in
 // gridDim.y / cluster parts, which share the tiles of 128 tokens), joined in
 // distributed shared memory; `words` gets a row of ldw per part, dY's columns
 // first, the scales' from code_word on.  The grid's first dy_strips are dY's.
+// 4096 x 4096 fp32 28 us, 8192 x 4096 bf16 30 to 37, under the next kernel's
+// first loads from 20 us on.
 __device__ __forceinline__ uint32_t finite_bits(float x) {
   const uint32_t b = abs_bits(x);
   return b < 0x7f800000u ? b : 0u;
@@ -310,6 +313,8 @@ __device__ __forceinline__ int value_power(uint32_t scale_bits) {
 
 // Rows of F = dY * scale as one half each, for act8_input_grad: a CTA per row,
 // read twice (the second time from cache).  factor: what undoes a row's power.
+// Bound by HBM and the second reading: 8192 x 11008 81 us, 4.5 TB/s of dY read
+// once and the halves written.
 template <bool A>
 __global__ void __launch_bounds__(kThreads)
 k_act8_row_halves(Mat dy, const float* __restrict__ scale, __half* o, int64_t ld, float* factor, int cols) {
@@ -341,7 +346,7 @@ k_act8_row_halves(Mat dy, const float* __restrict__ scale, __half* o, int64_t ld
     store8(o + row * ld, c, cols, 1, v);
   }
 }
-// Codes as halves, exactly.
+// Codes as halves, exactly.  11008 x 4096: 28 us, 4.9 TB/s.
 __global__ void __launch_bounds__(kThreads) k_act8_code_halves(Ckpt k, __half* o, int64_t ld, int64_t rows, int cols) {
   let_next_start();
   const Piece<4> p;
@@ -375,7 +380,9 @@ __device__ __forceinline__ void store_halves(const float (&v)[8], const int (&e)
 // Both operands in one launch: the first code_blocks of blockIdx.y the codes'
 // values, the others dY.  A column of dY has its power of two and so has a
 // group of the codes' columns, from the maxima; what undoes them goes to
-// `factor` (dY's columns, then from code_word on the groups).
+// `factor` (dY's columns, then from code_word on the groups).  Bound by HBM:
+// 4096 x 4096 codes and fp32 dY 48 us, 4.6 TB/s; 8192 x 11008 codes and
+// 8192 x 4096 bf16, one half each, 90 us.
 template <class T, int CODE_PARTS, int kRows, bool A>
 __global__ void __launch_bounds__(kThreads)
 k_act8_halves(Ckpt k, __half* co, int64_t ldco, int cols_c, Mat dy, __half* dyo, int64_t lddyo, int cols_dy,
@@ -515,7 +522,7 @@ GradPlan grad_plan(bool weight, int32_t dtype, int32_t result, int32_t group, in
   p.ldw = p.code_word + int64_t(round_up(size_t(group_count(inner, group)), 8));
   // Enough clusters for every SM's 2048 threads, as far as there are tiles.
   // (65536 x 64: 10.5 us in 8 parts; 16 take 7.9, but the next pass, which
-  // reads a row of maxima per part, 62 where it takes 50.)
+  // reads a row of maxima per part, 12 more.)
   const int64_t tiles = (tokens + kTokTile - 1) / kTokTile, strips = p.strips();
   p.ctas = 1;
   while (p.ctas < kColCluster && int64_t(p.ctas) < tiles) p.ctas *= 2;
@@ -601,7 +608,11 @@ shampoo4_status halves_pass(const void* dy, int32_t dtype, int64_t lddy, const C
                             int64_t inner, const GradPlan& p, float* factor, void* dyp, void* cp, cudaStream_t st) {
   const Mat m = mat(dy, lddy, dtype);
   const dim3 b = piece_block(std::max(out, inner));
-  const bool many = many_pieces(tokens, out + inner);
+  // Four rows per thread, which share the reading of the maxima, where that
+  // leaves every SM its 64 warps (a warp takes 256 columns of a row, however
+  // few there are: two operands of 65536 x 64 take 30 us, 50 with a row per
+  // thread).
+  const bool many = tokens * ((out + kChunk - 1) / kChunk + (inner + kChunk - 1) / kChunk) >= int64_t(4) * 148 * 64;
   dim3 g, gc;
   if (!piece_grid(tokens, out, b, many ? 4 : 1, &g) || !piece_grid(tokens, inner, b, many ? 4 : 1, &gc) ||
       g.y + gc.y > 65535)

@@ -2260,26 +2260,6 @@ Span bytes_of(const void* p, int64_t rows, int64_t cols, int64_t ld, int64_t siz
   return {b, rows > 0 && cols > 0 ? b + uintptr_t(size * ((rows - 1) * ld + cols)) : b};
 }
 
-// The parameters' gradients one by one, all of them checked; *bytes: the
-// largest workspace of any.
-shampoo4_status plan_weight_grads(shampoo4_handle h, const shampoo4_layer* layers, int32_t group,
-                                  float* const* d_grads, const int64_t* ld, int32_t accumulate,
-                                  std::vector<Act8Grad>* calls, size_t* bytes) {
-  if (!layers) return SHAMPOO4_ERR_INVALID_ARG;
-  *bytes = 0;
-  for (size_t i = 0; i < h->params.size(); ++i) {
-    const shampoo4_layer& l = layers[i];
-    const shampoo4_param& q = h->params[i];
-    const Act8Grad g{true, l.dy, l.dtype, l.lddy, l.codes, l.ldc, l.scales, group, l.tokens, q.rows, q.cols,
-                     d_grads[i], ACT8_FP32, ld[i], accumulate};
-    size_t n = 0;
-    S4_TRY(act8_grad_check(g, &n));
-    *bytes = std::max(*bytes, n);
-    calls->push_back(g);
-  }
-  return SHAMPOO4_OK;
-}
-
 }  // namespace
 
 extern "C" shampoo4_status shampoo4_weight_grads_workspace(shampoo4_handle h, const shampoo4_layer* layers,
@@ -2299,16 +2279,26 @@ extern "C" shampoo4_status shampoo4_weight_grads_workspace(shampoo4_handle h, co
 extern "C" shampoo4_status shampoo4_weight_grads(shampoo4_handle h, const shampoo4_layer* layers, int32_t group,
                                                  float* const* d_grads, const int64_t* ld, int32_t accumulate,
                                                  void* d_workspace, size_t workspace_bytes, shampoo4_stream_t stream) {
-  if (!h) return SHAMPOO4_ERR_INVALID_ARG;
+  if (!h || !layers) return SHAMPOO4_ERR_INVALID_ARG;
   S4_TRY(check_matrices(h, const_cast<const float* const*>(d_grads), ld));
-  std::vector<Act8Grad> calls;
+  const size_t np = h->params.size();
+  const auto call = [&](size_t i) {
+    const shampoo4_layer& l = layers[i];
+    return Act8Grad{true, l.dy, l.dtype, l.lddy, l.codes, l.ldc, l.scales, group, l.tokens, h->params[i].rows,
+                    h->params[i].cols, d_grads[i], ACT8_FP32, ld[i], accumulate};
+  };
   size_t bytes = 0;
-  S4_TRY(plan_weight_grads(h, layers, group, d_grads, ld, accumulate, &calls, &bytes));
+  for (size_t i = 0; i < np; ++i) {
+    size_t n = 0;
+    S4_TRY(act8_grad_check(call(i), &n));
+    bytes = std::max(bytes, n);
+  }
   // no gradient may share memory with another or with what any of them reads
-  for (size_t i = 0; i < calls.size(); ++i) {
-    const Span y = bytes_of(calls[i].y, calls[i].out, calls[i].inner, calls[i].ldy, 4);
-    for (size_t j = 0; j < calls.size(); ++j) {
-      const Act8Grad& g = calls[j];
+  for (size_t i = 0; i < np; ++i) {
+    const Act8Grad a = call(i);
+    const Span y = bytes_of(a.y, a.out, a.inner, a.ldy, 4);
+    for (size_t j = 0; j < np; ++j) {
+      const Act8Grad g = call(j);
       const int64_t groups = group ? (g.inner + group - 1) / group : 1;
       if ((i != j && meet(y, bytes_of(g.y, g.out, g.inner, g.ldy, 4))) ||
           meet(y, bytes_of(g.dy, g.tokens, g.out, g.lddy, g.dtype == ACT8_FP32 ? 4 : 2)) ||
@@ -2321,7 +2311,8 @@ extern "C" shampoo4_status shampoo4_weight_grads(shampoo4_handle h, const shampo
   if (workspace_bytes < bytes) return SHAMPOO4_ERR_WORKSPACE;
   if (!h->bound) return SHAMPOO4_ERR_NOT_READY;
   const Act8Watch watch{reinterpret_cast<uint32_t*>(h->d_ws + h->ws_flags), h->wait_ns};
-  for (const Act8Grad& g : calls) S4_TRY(act8_grad_run(g, d_workspace, watch, reinterpret_cast<cudaStream_t>(stream)));
+  for (size_t i = 0; i < np; ++i)
+    S4_TRY(act8_grad_run(call(i), d_workspace, watch, reinterpret_cast<cudaStream_t>(stream)));
   return SHAMPOO4_OK;
 }
 
