@@ -22,13 +22,14 @@
 //          value for a bfloat16 result of a bfloat16 dY (2^-11, an eighth of
 //          the result's own rounding; as one bfloat16 it would add as much
 //          again).  Three products (two, one), summed in fp32 outside the
-//          tensor core every 256 k (one: every 1024).  Also with one scale
-//          per row, for a large bfloat16 weight gradient.
+//          tensor core every 256 k (one: every 1024).  (Three bfloat16
+//          parts each, six products, measured 47 us where this took 32 at
+//          1537 x 768 x 2305 fp32.)  Also with one scale per row, for a large
+//          bfloat16 weight gradient.
 //  row     The large bfloat16 input gradient of a bfloat16 dY: F = dY * scale,
 //  halves  each row scaled by a power of two (its largest to about 2^14), as
 //          one half (2^-11, never coarser than 2^-39 of the row's largest),
-//          the codes as halves as they are: one product.  (Three bfloat16 parts each, six products, measured
-//          47 us where this takes 32 at 1537 x 768 x 2305 fp32.)
+//          the codes as halves as they are: one product.
 //
 // The operand passes of this file stream; their bound is HBM bandwidth.
 #include <cooperative_groups.h>
@@ -714,6 +715,8 @@ extern "C" shampoo4_status act8_product_form(int32_t call, int32_t dtype, int32_
   if (!form || call < 0 || call > 2 || !dtype_ok(dtype) || !dtype_ok(result) || !group_ok(group) ||
       (call == 2 && group) || !shape_ok(tokens, out) || !shape_ok(0, inner))
     return SHAMPOO4_ERR_INVALID_ARG;
+  *form = act8_form{ACT8_WAY_CODES, 0, 0, 0};
+  if (tokens == 0 || out == 0 || inner == 0) return SHAMPOO4_OK;
   if (call == 0) {
     const Form f = act8_codes_form(out, tokens, inner);
     *form = act8_form{ACT8_WAY_CODES, f.rows, f.shares, 0};

@@ -605,8 +605,8 @@ shampoo4_status act8_input_grad(const void* d_dy, int32_t dtype, int64_t lddy, c
 
 /* Diagnostic: how a product would be computed, for tests that have to reach
  * every way.  call: 0 act8_matmul and act8_linear (dtype, result and group do
- * not matter), 1 act8_weight_grad, 2 act8_input_grad (group 0).  Touches no
- * device. */
+ * not matter), 1 act8_weight_grad, 2 act8_input_grad (group 0).  An empty one
+ * has no shares.  Touches no device. */
 typedef enum {
   ACT8_WAY_CODES = 0,        /* the codes as they are                        */
   ACT8_WAY_DIGITS = 1,       /* dY in fixed point                            */
@@ -626,7 +626,8 @@ shampoo4_status act8_product_form(int32_t call, int32_t dtype, int32_t result, i
  * parameter p of shape out x inner gets act8_weight_grad of layers[p], in
  * fp32, at d_grads[p] (leading dimension ld[p] >= inner), overwritten or, with
  * accumulate != 0, added to.  An expired wait of a product is in the handle's
- * status flags.  Every layer is checked before anything is enqueued; no gradient may overlap another or any input.  d_workspace:
+ * status flags.  Every layer is checked before anything is enqueued; no
+ * gradient may overlap another or any input.  d_workspace:
  * shampoo4_weight_grads_workspace bytes, 256-byte aligned, used by one layer
  * after the other. */
 typedef struct {

@@ -29,6 +29,13 @@ def test_gradients(call, case):
     assert (f.way, f.tile_rows, f.shares > 1, f.code_parts) == (way, rows, split, parts)
 
 
+@pytest.mark.parametrize("call", [0, 1, 2])
+@pytest.mark.parametrize("sizes", [(0, 0, 0), (0, 8, 8), (8, 0, 8), (8, 8, 0), (8, 0, 0), (0, 0, 8)])
+def test_empty(call, sizes):
+    for group in ([0, 32] if call == 1 else [0]):
+        assert form(call, *sizes, group=group).shares == 0
+
+
 def test_every_form_is_among_them():
     assert {(r, s) for *_, r, s in MATMUL} == {(16, False), (16, True), (64, False), (64, True), (128, False),
                                                (128, True), (0, False)}

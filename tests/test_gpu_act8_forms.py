@@ -147,3 +147,42 @@ def test_layers_back_to_back_take_their_own_scales(tokens, out, inner):
             y, dx = api.act8_linear(xs[k], *w), api.act8_input_grad(dys[k], *w)
             assert torch.equal(y, ys[k]) and torch.equal(dx, dxs[k])
             y, dx = None, None
+
+
+def test_gradients_on_two_streams_and_replayed():
+    """Every way of the gradients, on two streams at once (each call has its
+    own scratch) and captured with three passes in a row: the results are those
+    of the calls one by one, bit for bit."""
+    api = _api()
+    calls = []
+    for weight, cases in ((True, WEIGHT), (False, INPUT)):
+        for n, (tokens, out, inner, dtype, result, group, *_) in enumerate(cases):
+            dy = some_gradients(tokens, out, dtype, 10 + n)
+            k = some_codes(tokens if weight else out, inner, group, 30 + n)
+            f = api.act8_weight_grad if weight else api.act8_input_grad
+            kw = dict(group=group, dtype=DT[result]) if weight else dict(dtype=DT[result])
+            calls.append(lambda f=f, dy=dy, k=k, kw=kw: f(dy, *k, **kw))
+    want = []
+    for c in calls:
+        want.append(c())
+        torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(2):
+        got = [[], []]
+        for c in calls:
+            for s, g in zip(streams, got):
+                with torch.cuda.stream(s):
+                    g.append(c())
+        torch.cuda.synchronize()
+        for g in got:
+            assert all(torch.equal(a, b) for a, b in zip(g, want))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = [c() for c in calls]
+    for _ in range(2):
+        for t in got:
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    del graph
